@@ -1,8 +1,10 @@
 """Python binding of the MI355X fused SwiGLU + top-k weight + FP8/FP4 cast,
-the stand-alone cast, the top-k gating and the weighted top-k reduce.
+the stand-alone cast, the top-k gating and the weighted top-k reduce, and of
+the operators of an MoE layer around them (RMS norm with FP8 output, routing,
+the experts' products with 4-bit weights).
 
 Argument marshalling only: every function here forwards to the C ABI in
-``include/tk.h`` (library ``libtk.so`` built from ``csrc/*.hip``) under the
+``include/tk.h`` and ``include/tk_layer.h`` (library ``libtk.so`` built from ``csrc/*.hip``) under the
 same name, through the small CPython extension ``_tkpy`` (``csrc/tk_py.c``,
 a fraction of a microsecond per call where ctypes took a few).  All
 arithmetic runs in the library's HIP kernels; there is no CPU fallback, and
@@ -24,9 +26,11 @@ LIB_PATH = os.path.join(_HERE, "libtk.so")
 
 __all__ = [
     "TkStatus", "TK_SCALE_FP32", "TK_SCALE_UE8M0", "TK_SCALE_FP32_COLMAJOR", "TK_SCALE_UE8M0_COLMAJOR",
-    "TK_SCALE_UE8M0_PACKED", "TK_DTYPE_BF16", "TK_DTYPE_FP32", "LIB_PATH", "load_library", "load_extension",
+    "TK_SCALE_UE8M0_PACKED", "TK_DTYPE_BF16", "TK_DTYPE_FP32", "TK_DTYPE_FP8", "TK_SCORE_SIGMOID", "TK_SCORE_SOFTMAX",
+    "TK_RMSNORM_PARTS", "LIB_PATH", "load_library", "load_extension",
     "tk_init", "tk_swiglu_cast_fp8", "tk_swiglu_cast_fp4", "tk_swiglu_forward", "tk_cast_fp8", "tk_cast_fp4",
-    "tk_topk_gate", "tk_moe_reduce", "tk_status_str",
+    "tk_topk_gate", "tk_moe_reduce", "tk_status_str", "tk_rmsnorm_cast_fp8", "tk_rmsnorm_backward", "tk_route",
+    "tk_route_backward", "tk_expert_gemv_fp4",
 ]
 
 TK_SCALE_FP32 = 0
@@ -36,6 +40,10 @@ TK_SCALE_UE8M0_COLMAJOR = 3
 TK_SCALE_UE8M0_PACKED = 4
 TK_DTYPE_BF16 = 0
 TK_DTYPE_FP32 = 1
+TK_DTYPE_FP8 = 2
+TK_SCORE_SIGMOID = 0
+TK_SCORE_SOFTMAX = 1
+TK_RMSNORM_PARTS = 512
 
 
 class TkStatus(enum.IntEnum):
@@ -47,7 +55,7 @@ class TkStatus(enum.IntEnum):
 
 _lib: Optional[ctypes.CDLL] = None
 
-# the exported symbols and their C signatures, as declared in include/tk.h
+# the exported symbols and their C signatures, as declared in include/tk.h and include/tk_layer.h
 _CAST_ARGS = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
               ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
               ctypes.c_void_p]
@@ -69,6 +77,24 @@ SIGNATURES = {
     "tk_topk_to_pos": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "tk_status_str": (ctypes.c_char_p, [ctypes.c_int]),
+    "tk_rmsnorm_cast_fp8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                           ctypes.c_int64, ctypes.c_int64, ctypes.c_float, ctypes.c_int64,
+                                           ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "tk_rmsnorm_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "tk_route": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "tk_route_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
+    "tk_expert_gemv_fp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                          ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                          ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                          ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                          ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
 }
 
 
@@ -173,6 +199,44 @@ def tk_topk_to_pos(topk_idx, tokens, k, experts, pos, expert_offsets, stream=Non
     """See tk_topk_to_pos in include/tk.h."""
     return _STATUS[(_ext or load_extension()).tk_topk_to_pos(topk_idx, tokens, k, experts, pos, expert_offsets,
                                                                stream)]
+
+
+def tk_rmsnorm_cast_fp8(x, residual, in_dtype, weight, n, hidden, eps, group_size, scale_fmt, residual_out, y, rstd,
+                        codes, scales, stream=None) -> TkStatus:
+    """See tk_rmsnorm_cast_fp8 in include/tk_layer.h."""
+    return _STATUS[(_ext or load_extension()).tk_rmsnorm_cast_fp8(
+        x, residual, in_dtype, weight, n, hidden, eps, group_size, scale_fmt, residual_out, y, rstd, codes, scales,
+        stream)]
+
+
+def tk_rmsnorm_backward(dy, h, in_dtype, weight, rstd, dresidual, n, hidden, dx, dweight, workspace,
+                        stream=None) -> TkStatus:
+    """See tk_rmsnorm_backward in include/tk_layer.h."""
+    return _STATUS[(_ext or load_extension()).tk_rmsnorm_backward(dy, h, in_dtype, weight, rstd, dresidual, n, hidden,
+                                                                  dx, dweight, workspace, stream)]
+
+
+def tk_route(logits, in_dtype, bias, tokens, experts, k, n_group, topk_group, scoring, normalise, scale, topk_idx,
+             topk_weight, stream=None) -> TkStatus:
+    """See tk_route in include/tk_layer.h."""
+    return _STATUS[(_ext or load_extension()).tk_route(logits, in_dtype, bias, tokens, experts, k, n_group, topk_group,
+                                                       scoring, normalise, scale, topk_idx, topk_weight, stream)]
+
+
+def tk_route_backward(dweight, topk_idx, logits, in_dtype, tokens, experts, k, scoring, normalise, scale, dlogits,
+                      stream=None) -> TkStatus:
+    """See tk_route_backward in include/tk_layer.h."""
+    return _STATUS[(_ext or load_extension()).tk_route_backward(dweight, topk_idx, logits, in_dtype, tokens, experts, k,
+                                                                scoring, normalise, scale, dlogits, stream)]
+
+
+def tk_expert_gemv_fp4(x, x_scales, x_dtype, x_scale_fmt, x_group, topk_idx, tokens, k, x_slots, codes, scales,
+                       scale_fmt, group_size, experts, out_features, in_features, out_dtype, out,
+                       stream=None) -> TkStatus:
+    """See tk_expert_gemv_fp4 in include/tk_layer.h."""
+    return _STATUS[(_ext or load_extension()).tk_expert_gemv_fp4(
+        x, x_scales, x_dtype, x_scale_fmt, x_group, topk_idx, tokens, k, x_slots, codes, scales, scale_fmt, group_size,
+        experts, out_features, in_features, out_dtype, out, stream)]
 
 
 def tk_status_str(status: int) -> str:

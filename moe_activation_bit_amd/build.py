@@ -35,7 +35,8 @@ def _run(cmd):
 
 
 OBJ_DIR = os.path.join(HERE, "_build")
-TK_SOURCES = ["tk_swiglu_cast.hip", "tk_cast.hip", "tk_topk.hip", "tk_reduce.hip", "tk_pos.hip"]
+TK_SOURCES = ["tk_swiglu_cast.hip", "tk_cast.hip", "tk_topk.hip", "tk_reduce.hip", "tk_pos.hip",
+              "tk_rmsnorm.hip", "tk_route.hip", "tk_gemv.hip"]
 
 
 def _hip_object(src):

@@ -1,5 +1,5 @@
 /* tk_py.c -- the CPython extension module `_tkpy`: argument marshalling from
- * Python objects to the C ABI of include/tk.h, one function per entry point
+ * Python objects to the C ABI of include/tk.h and include/tk_layer.h, one function per entry point
  * under the same name.  Nothing else happens here: every function converts its
  * arguments and calls the library.
  *
@@ -20,6 +20,7 @@
 #include <Python.h>
 
 #include "tk.h"
+#include "tk_layer.h"
 
 static PyObject* g_stream_getter = NULL; /* callable returning a stream handle */
 
@@ -242,6 +243,103 @@ static PyObject* py_tk_moe_reduce(PyObject* self, PyObject* args)
     return status(rc);
 }
 
+static PyObject* py_tk_rmsnorm_cast_fp8(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *x, *residual, *weight, *residual_out, *y, *rstd, *codes, *scales, *stream = NULL;
+    long long n, hidden, group;
+    float eps;
+    int in_dtype, sfmt;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&O&iO&LLfLiO&O&O&O&O&|O", as_ptr, &x, as_ptr, &residual, &in_dtype, as_ptr, &weight,
+                          &n, &hidden, &eps, &group, &sfmt, as_ptr, &residual_out, as_ptr, &y, as_ptr, &rstd, as_ptr,
+                          &codes, as_ptr, &scales, &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_rmsnorm_cast_fp8(x, residual, (tk_dtype)in_dtype, (const float*)weight, n, hidden, eps, group,
+                                    (tk_scale_fmt)sfmt, residual_out, y, (float*)rstd, codes, scales, stream));
+    return status(rc);
+}
+
+static PyObject* py_tk_rmsnorm_backward(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *dy, *h, *weight, *rstd, *dresidual, *dx, *dweight, *workspace, *stream = NULL;
+    long long n, hidden;
+    int in_dtype;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&O&iO&O&O&LLO&O&O&|O", as_ptr, &dy, as_ptr, &h, &in_dtype, as_ptr, &weight, as_ptr,
+                          &rstd, as_ptr, &dresidual, &n, &hidden, as_ptr, &dx, as_ptr, &dweight, as_ptr, &workspace,
+                          &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_rmsnorm_backward(dy, h, (tk_dtype)in_dtype, (const float*)weight, (const float*)rstd, dresidual, n,
+                                    hidden, dx, (float*)dweight, (float*)workspace, stream));
+    return status(rc);
+}
+
+static PyObject* py_tk_route(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *logits, *bias, *idx, *w, *stream = NULL;
+    long long tokens, experts, k, n_group, topk_group;
+    float scale;
+    int in_dtype, scoring, normalise;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&iO&LLLLLipfO&O&|O", as_ptr, &logits, &in_dtype, as_ptr, &bias, &tokens, &experts,
+                          &k, &n_group, &topk_group, &scoring, &normalise, &scale, as_ptr, &idx, as_ptr, &w, &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_route(logits, (tk_dtype)in_dtype, (const float*)bias, tokens, experts, k, n_group, topk_group,
+                         (tk_scoring)scoring, normalise, scale, (int32_t*)idx, (float*)w, stream));
+    return status(rc);
+}
+
+static PyObject* py_tk_route_backward(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *dweight, *idx, *logits, *dlogits, *stream = NULL;
+    long long tokens, experts, k;
+    float scale;
+    int in_dtype, scoring, normalise;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&O&O&iLLLipfO&|O", as_ptr, &dweight, as_ptr, &idx, as_ptr, &logits, &in_dtype,
+                          &tokens, &experts, &k, &scoring, &normalise, &scale, as_ptr, &dlogits, &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_route_backward((const float*)dweight, (const int32_t*)idx, logits, (tk_dtype)in_dtype, tokens,
+                                  experts, k, (tk_scoring)scoring, normalise, scale, dlogits, stream));
+    return status(rc);
+}
+
+static PyObject* py_tk_expert_gemv_fp4(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *x, *x_scales, *idx, *codes, *scales, *out, *stream = NULL;
+    long long x_group, tokens, k, group, experts, out_features, in_features;
+    int x_dtype, x_sfmt, x_slots, sfmt, out_dtype;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&O&iiLO&LLpO&O&iLLLLiO&|O", as_ptr, &x, as_ptr, &x_scales, &x_dtype, &x_sfmt,
+                          &x_group, as_ptr, &idx, &tokens, &k, &x_slots, as_ptr, &codes, as_ptr, &scales, &sfmt,
+                          &group, &experts, &out_features, &in_features, &out_dtype, as_ptr, &out, &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_expert_gemv_fp4(x, x_scales, x_dtype, (tk_scale_fmt)x_sfmt, x_group, (const int32_t*)idx, tokens, k,
+                                   x_slots, codes, scales, (tk_scale_fmt)sfmt, group, experts, out_features,
+                                   in_features, (tk_dtype)out_dtype, out, stream));
+    return status(rc);
+}
+
 static PyMethodDef kMethods[] = {
     {"_set_stream_getter", py_set_stream_getter, METH_O, "set the callable that supplies the default stream"},
     {"tk_init", py_tk_init, METH_VARARGS, "tk_init(device)"},
@@ -265,6 +363,20 @@ static PyMethodDef kMethods[] = {
      "stream=None)"},
     {"tk_topk_to_pos", py_tk_topk_to_pos, METH_VARARGS,
      "tk_topk_to_pos(topk_idx, tokens, k, experts, pos, expert_offsets, stream=None)"},
+    {"tk_rmsnorm_cast_fp8", py_tk_rmsnorm_cast_fp8, METH_VARARGS,
+     "tk_rmsnorm_cast_fp8(x, residual, in_dtype, weight, n, hidden, eps, group_size, scale_fmt, residual_out, y, "
+     "rstd, codes, scales, stream=None)"},
+    {"tk_rmsnorm_backward", py_tk_rmsnorm_backward, METH_VARARGS,
+     "tk_rmsnorm_backward(dy, h, in_dtype, weight, rstd, dresidual, n, hidden, dx, dweight, workspace, stream=None)"},
+    {"tk_route", py_tk_route, METH_VARARGS,
+     "tk_route(logits, in_dtype, bias, tokens, experts, k, n_group, topk_group, scoring, normalise, scale, topk_idx, "
+     "topk_weight, stream=None)"},
+    {"tk_route_backward", py_tk_route_backward, METH_VARARGS,
+     "tk_route_backward(dweight, topk_idx, logits, in_dtype, tokens, experts, k, scoring, normalise, scale, dlogits, "
+     "stream=None)"},
+    {"tk_expert_gemv_fp4", py_tk_expert_gemv_fp4, METH_VARARGS,
+     "tk_expert_gemv_fp4(x, x_scales, x_dtype, x_scale_fmt, x_group, topk_idx, tokens, k, x_slots, codes, scales, "
+     "scale_fmt, group_size, experts, out_features, in_features, out_dtype, out, stream=None)"},
     {NULL, NULL, 0, NULL},
 };
 

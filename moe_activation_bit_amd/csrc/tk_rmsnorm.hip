@@ -1,0 +1,646 @@
+// tk_rmsnorm.hip -- residual addition + root-mean-square norm + FP8 cast and
+// its gradient, behind tk_rmsnorm_cast_fp8 and tk_rmsnorm_backward in
+// include/tk_layer.h.
+//
+// Forward, per row: h = x + residual (rounded to the stream's type), rstd =
+// 1/sqrt(mean h^2 + eps), y = h * rstd * weight, then the abs-max -> scale ->
+// code tail of the casts (tk_quant.h).  A row is held in registers between its
+// sum and its cast, so every input is read and every output written once.
+// Backward: dx = rstd * (g - a * mean(g*a)) + dresidual with g = dy * weight and
+// a = rstd * h, and dweight = sum over the rows of dy * a, gathered by each
+// workgroup over its rows in registers, written as one partial row, and summed
+// over the partial rows by a second kernel in their order.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "tk.h"
+#include "tk_layer.h"
+#include "tk_quant.h"
+
+namespace {
+
+using namespace tk_detail;
+
+constexpr uint32_t kMaxBlocks = 1u << 20;
+constexpr int64_t kMaxHidden = 32768; // 16 waves of 4 steps of 512 columns
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return as_float(w & 0xFFFF0000u); }
+
+// two floats rounded to bf16 (nearest even), the first in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// The lane slot's 8 columns as fp32.
+template <bool F32>
+__device__ __forceinline__ void load_slot(const void* base, size_t slot, float (&v)[8])
+{
+    if constexpr (F32) {
+        const uint4* p = static_cast<const uint4*>(base) + 2 * slot;
+        const uint4 a = load16(p), b = load16(p + 1);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = as_float(w[j]);
+    } else {
+        const uint4 a = load16(static_cast<const uint4*>(base) + slot);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = bf16_lo(w[j]);
+            v[2 * j + 1] = bf16_hi(w[j]);
+        }
+    }
+}
+
+// ... and the 8 columns written, rounded to the type.
+template <bool F32>
+__device__ __forceinline__ void store_slot(void* base, size_t slot, const float (&v)[8])
+{
+    if constexpr (F32) {
+        v4u* p = static_cast<v4u*>(base) + 2 * slot;
+        const v4u a = {as_uint(v[0]), as_uint(v[1]), as_uint(v[2]), as_uint(v[3])};
+        const v4u b = {as_uint(v[4]), as_uint(v[5]), as_uint(v[6]), as_uint(v[7])};
+        __builtin_nontemporal_store(a, p);
+        __builtin_nontemporal_store(b, p + 1);
+    } else {
+        const v4u a = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+        __builtin_nontemporal_store(a, static_cast<v4u*>(base) + slot);
+    }
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+    return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v)
+{
+    return v + as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)as_uint(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ double read_lane(double v, int lane)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float read_lane(float v, int lane)
+{
+    return as_float(__builtin_amdgcn_readlane(as_uint(v), lane));
+}
+
+// sum over all 64 lanes (every lane active), in a fixed order
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v)
+{
+    v = dpp_add<0xB1>(v);  // quad_perm [1,0,3,2]: lane ^ 1
+    v = dpp_add<0x4E>(v);  // quad_perm [2,3,0,1]: lane ^ 2
+    v = dpp_add<0x141>(v); // row_half_mirror
+    v = dpp_add<0x140>(v); // row_mirror: every lane holds its row's sum
+    return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
+}
+
+// 1/sqrt(m) to within a few units of the 64-bit last place: the hardware's
+// estimate refined twice by Newton's iteration.  0, infinity and NaN keep the
+// estimate's own limit values.
+__device__ __forceinline__ double rsqrt64(double m)
+{
+    const double r0 = __builtin_amdgcn_rsq(m);
+    double r = r0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        r = r * __builtin_fma(-0.5 * m * r, r, 1.5);
+    return (m > 0.0 && m < (double)INFINITY) ? r : r0;
+}
+
+struct NormParams {
+    Params q;              // codes, scales and their layout
+    const void* x;
+    const void* residual;  // or null
+    const float* weight;
+    void* residual_out;    // or null
+    void* y;               // or null
+    float* rstd;           // or null
+    uint32_t n;
+    uint32_t waves;        // waves per row; 1: every wave of the workgroup has a row of its own
+    double inv_hidden;
+    double eps;
+};
+
+constexpr int kGroupRow = 0;   // one scale per row
+constexpr int kGroupLanes = 1; // groups of 2^gl_log2 lanes of one step
+constexpr int kGroupLds = 2;   // any other width: the slots' maxima meet in LDS
+
+// One row per `waves` waves: step s of wave w of a row is slots
+// (s * waves + w) * 64 .. + 63, a lane holding 8 columns of each of its S steps.
+template <bool F32, int S, int GM, int SFMT, int MAXT>
+__global__ __launch_bounds__(MAXT) void rmsnorm_cast_kernel(NormParams p)
+{
+    __shared__ double part_sum[2][16]; // by the parity of the pass, so that one barrier a pass is enough
+    __shared__ uint32_t part_max[2][16];
+    extern __shared__ uint32_t dyn[]; // kGroupLds: each row's slot maxima, then its groups' multipliers
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1);
+    const uint32_t wib = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
+    const uint32_t rows = p.waves == 1 ? blockDim.x / kWaveSize : 1u; // rows of this workgroup
+    const uint32_t part = p.waves == 1 ? 0u : wib;
+    const uint32_t row_in = p.waves == 1 ? wib : 0u;
+    uint32_t parity = 0;
+    // rows past the grid (a launch holds fewer than 2^32 work-items) take further passes
+    for (uint32_t first = blockIdx.x * rows; first < p.n; first += gridDim.x * rows, parity ^= 1u) {
+        const uint32_t row = first + row_in;
+        const bool valid = row < p.n; // wave-uniform; waves without a row still meet the barriers
+        const uint32_t slots = p.q.slots;
+        const size_t row_slot = (size_t)row * slots;
+
+        float v[S][8], w[S][8];
+        double sum = 0.0;
+    #pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const uint32_t slot = ((uint32_t)s * p.waves + part) * kWaveSize + lane;
+    #pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[s][j] = 0.0f, w[s][j] = 0.0f;
+            if (valid && slot < slots) {
+                load_slot<F32>(p.x, row_slot + slot, v[s]);
+                const float4* wp = reinterpret_cast<const float4*>(p.weight) + 2 * slot;
+                const float4 a = wp[0], b = wp[1];
+                w[s][0] = a.x, w[s][1] = a.y, w[s][2] = a.z, w[s][3] = a.w;
+                w[s][4] = b.x, w[s][5] = b.y, w[s][6] = b.z, w[s][7] = b.w;
+                if (p.residual) {
+                    float r[8];
+                    load_slot<F32>(p.residual, row_slot + slot, r);
+    #pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[s][j] += r[j];
+                    if constexpr (!F32) { // the norm is of the stream as it is stored
+    #pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            const uint32_t b2 = pack_bf16(v[s][j], v[s][j + 1]);
+                            v[s][j] = bf16_lo(b2);
+                            v[s][j + 1] = bf16_hi(b2);
+                        }
+                    }
+                }
+                if (p.residual_out)
+                    store_slot<F32>(p.residual_out, row_slot + slot, v[s]);
+    #pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sum = __builtin_fma((double)v[s][j], (double)v[s][j], sum);
+            }
+        }
+        sum = wave_sum(sum);
+        if (p.waves > 1) {
+            if (lane == 0)
+                part_sum[parity][wib] = sum;
+            __syncthreads();
+            sum = 0.0;
+            for (uint32_t i = 0; i < p.waves; ++i)
+                sum += part_sum[parity][i];
+        }
+        const float rstd = (float)rsqrt64(__builtin_fma(sum, p.inv_hidden, p.eps));
+        if (valid && p.rstd && part == 0 && lane == 0)
+            p.rstd[row] = rstd;
+
+        uint32_t m[S];
+    #pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const uint32_t slot = ((uint32_t)s * p.waves + part) * kWaveSize + lane;
+            m[s] = 0;
+    #pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[s][j] = (v[s][j] * rstd) * w[s][j];
+                m[s] = max(m[s], as_uint(v[s][j]) & 0x7FFFFFFFu);
+            }
+            if (!(valid && slot < slots))
+                m[s] = 0;
+            else if (p.y)
+                store_slot<false>(p.y, row_slot + slot, v[s]);
+        }
+        if (!p.q.codes)
+            continue; // the whole grid
+        uint8_t* row_codes = p.q.codes + (size_t)row * slots * 8u;
+
+        if constexpr (GM == kGroupRow) {
+            uint32_t mb = wave_umax(lane_max<S>(m, S));
+            if (p.waves > 1) {
+                if (lane == 0)
+                    part_max[parity][wib] = mb;
+                __syncthreads();
+                for (uint32_t i = 0; i < p.waves; ++i)
+                    mb = max(mb, part_max[parity][i]);
+            }
+            float s32 = 0.0f;
+            uint32_t s8 = 0;
+            const float inv = group_scale<8, SFMT>(mb, s32, s8);
+            if (valid && part == 0 && lane == 0)
+                store_scale<SFMT>(p.q, row, 0, s32, s8);
+    #pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const uint32_t slot = ((uint32_t)s * p.waves + part) * kWaveSize + lane;
+                if (valid && slot < slots)
+                    quantize_store<8>(row_codes, slot, v[s], inv);
+            }
+        } else if constexpr (GM == kGroupLanes) {
+    #pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const uint32_t slot = ((uint32_t)s * p.waves + part) * kWaveSize + lane;
+                float s32 = 0.0f;
+                uint32_t s8 = 0;
+                const float inv = group_scale<8, SFMT>(group_umax(m[s], p.q.gl_log2), s32, s8);
+                if (valid && slot < slots) {
+                    quantize_store<8>(row_codes, slot, v[s], inv);
+                    if ((lane & ((1u << p.q.gl_log2) - 1u)) == 0)
+                        store_scale<SFMT>(p.q, row, slot >> p.q.gl_log2, s32, s8);
+                }
+            }
+        } else {
+            const uint32_t gs = p.q.gslots, ngr = p.q.groups_row;
+            uint32_t* buf = dyn + (size_t)row_in * (slots + ngr);
+            float* invs = reinterpret_cast<float*>(buf + slots);
+    #pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const uint32_t slot = ((uint32_t)s * p.waves + part) * kWaveSize + lane;
+                if (slot < slots)
+                    buf[slot] = m[s];
+            }
+            __syncthreads();
+            // 2^l_log2 lanes of one wave reduce a group, each a run of its slots
+            const uint32_t lanes = p.waves * kWaveSize, at = part * kWaveSize + lane;
+            uint32_t l_log2 = 0;
+            while (l_log2 < 6 && (ngr << (l_log2 + 1)) <= lanes)
+                ++l_log2;
+            const uint32_t lpg = 1u << l_log2, chunk = (gs + lpg - 1u) >> l_log2;
+            for (uint32_t base = 0; base < ngr; base += lanes >> l_log2) {
+                const uint32_t k = base + (at >> l_log2), sub = at & (lpg - 1u);
+                uint32_t mb = 0;
+                if (k < ngr) {
+                    const uint32_t e = min(k * gs + (sub + 1u) * chunk, (k + 1u) * gs);
+                    for (uint32_t i = k * gs + sub * chunk; i < e; ++i)
+                        mb = max(mb, buf[i]);
+                }
+                mb = group_umax(mb, l_log2);
+                if (k < ngr && sub == 0) {
+                    float s32 = 0.0f;
+                    uint32_t s8 = 0;
+                    invs[k] = group_scale<8, SFMT>(mb, s32, s8);
+                    if (valid)
+                        store_scale<SFMT>(p.q, row, k, s32, s8);
+                }
+            }
+            __syncthreads();
+    #pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const uint32_t slot = ((uint32_t)s * p.waves + part) * kWaveSize + lane;
+                if (valid && slot < slots)
+                    quantize_store<8>(row_codes, slot, v[s], invs[__umulhi(slot, p.q.gmagic)]);
+            }
+        }
+    }
+}
+
+struct NormBwdParams {
+    const void* dy;
+    const void* h;
+    const float* weight;
+    const float* rstd;
+    const void* dresidual; // or null
+    void* dx;
+    float* partial;        // [gridDim.x][hidden], or null
+    uint32_t n;
+    uint32_t slots;
+    float inv_hidden;
+};
+
+// One row per pass of a workgroup, rows blockIdx.x, + gridDim.x, ...; the
+// weight and the rows' dy * a sums stay in registers.
+template <bool F32, int S, int MAXT>
+__global__ __launch_bounds__(MAXT) void rmsnorm_backward_kernel(NormBwdParams p)
+{
+    __shared__ float part_dot[2][16];
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1);
+    const uint32_t wib = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
+    const uint32_t waves = blockDim.x / kWaveSize;
+    float w[S][8], dw[S][8];
+    uint32_t slot[S];
+    bool in[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        slot[s] = ((uint32_t)s * waves + wib) * kWaveSize + lane;
+        in[s] = slot[s] < p.slots;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[s][j] = in[s] ? p.weight[8 * slot[s] + j] : 0.0f, dw[s][j] = 0.0f;
+    }
+    uint32_t parity = 0;
+    for (uint32_t row = blockIdx.x; row < p.n; row += gridDim.x, parity ^= 1u) {
+        const size_t row_slot = (size_t)row * p.slots;
+        const float rstd = p.rstd[row];
+        float a[S][8], g[S][8];
+        float dot = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                a[s][j] = 0.0f, g[s][j] = 0.0f;
+            if (in[s]) {
+                load_slot<F32>(p.dy, row_slot + slot[s], g[s]);
+                load_slot<F32>(p.h, row_slot + slot[s], a[s]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[s][j] *= rstd;
+                dw[s][j] += g[s][j] * a[s][j];
+                g[s][j] *= w[s][j];
+                dot += g[s][j] * a[s][j];
+            }
+        }
+        dot = wave_sum(dot);
+        if (waves > 1) {
+            if (lane == 0)
+                part_dot[parity][wib] = dot;
+            __syncthreads();
+            dot = 0.0f;
+            for (uint32_t i = 0; i < waves; ++i)
+                dot += part_dot[parity][i];
+        }
+        const float mean = dot * p.inv_hidden;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            if (in[s]) {
+                float d[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    d[j] = rstd * (g[s][j] - a[s][j] * mean);
+                if (p.dresidual) {
+                    float r[8];
+                    load_slot<F32>(p.dresidual, row_slot + slot[s], r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        d[j] += r[j];
+                }
+                store_slot<F32>(p.dx, row_slot + slot[s], d);
+            }
+        }
+    }
+    if (p.partial) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            if (in[s]) {
+                float4* o = reinterpret_cast<float4*>(p.partial + ((size_t)blockIdx.x * p.slots + slot[s]) * 8u);
+                o[0] = make_float4(dw[s][0], dw[s][1], dw[s][2], dw[s][3]);
+                o[1] = make_float4(dw[s][4], dw[s][5], dw[s][6], dw[s][7]);
+            }
+        }
+    }
+}
+
+// dweight[c] = the partial rows' sum: 16 waves of a workgroup share 64 columns,
+// wave w taking partial rows w, w + 16, ..., then their sums in wave order.
+// parts == 0 writes zeros.
+__global__ __launch_bounds__(1024) void rmsnorm_dweight_kernel(const float* __restrict__ partial, uint32_t parts,
+                                                              uint32_t hidden, float* __restrict__ dweight)
+{
+    __shared__ float sums[16][kWaveSize];
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1), wv = threadIdx.x / kWaveSize;
+    const uint32_t c = blockIdx.x * kWaveSize + lane;
+    float s = 0.0f;
+    if (c < hidden)
+        for (uint32_t i = wv; i < parts; i += 16)
+            s += partial[(size_t)i * hidden + c];
+    sums[wv][lane] = s;
+    __syncthreads();
+    if (wv == 0 && c < hidden) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            s += sums[i][lane];
+        dweight[c] = s;
+    }
+}
+
+template <bool F32, int S, int MAXT, int GM>
+void launch_norm(int sfmt, const NormParams& p, dim3 grid, dim3 block, size_t lds, hipStream_t s)
+{
+    if (sfmt == TK_SCALE_FP32)
+        hipLaunchKernelGGL((rmsnorm_cast_kernel<F32, S, GM, TK_SCALE_FP32, MAXT>), grid, block, lds, s, p);
+    else
+        hipLaunchKernelGGL((rmsnorm_cast_kernel<F32, S, GM, TK_SCALE_UE8M0, MAXT>), grid, block, lds, s, p);
+}
+
+template <bool F32, int S, int MAXT>
+void launch_norm_gm(int gm, int sfmt, const NormParams& p, dim3 grid, dim3 block, size_t lds, hipStream_t s)
+{
+    if (gm == kGroupRow)
+        launch_norm<F32, S, MAXT, kGroupRow>(sfmt, p, grid, block, 0, s);
+    else if (gm == kGroupLanes)
+        launch_norm<F32, S, MAXT, kGroupLanes>(sfmt, p, grid, block, 0, s);
+    else
+        launch_norm<F32, S, MAXT, kGroupLds>(sfmt, p, grid, block, lds, s);
+}
+
+// The steps a lane holds of a row of `steps` 512-column steps: `pref`, more
+// where 16 waves would not cover the row.
+uint32_t steps_per_wave(uint32_t steps, uint32_t pref)
+{
+    uint32_t S = pref;
+    while ((steps + S - 1) / S > 16)
+        S <<= 1;
+    return S;
+}
+
+} // namespace
+
+extern "C" {
+
+tk_status tk_rmsnorm_cast_fp8(const void* x, const void* residual, tk_dtype in_dtype, const float* weight, int64_t n,
+                              int64_t hidden, float eps, int64_t group_size, tk_scale_fmt scale_fmt,
+                              void* residual_out, void* y, float* rstd, void* codes, void* scales, void* stream)
+{
+    // ---- validation: no HIP call before every argument is checked ----
+    if (n < 0 || n >= (int64_t)INT_MAX || hidden <= 0 || hidden % kSlotCols != 0 || hidden > (int64_t)INT_MAX / 8)
+        return TK_ERR_INVALID_ARG;
+    if (group_size < 0 || (group_size != 0 && (group_size % kSlotCols != 0 || hidden % group_size != 0)))
+        return TK_ERR_INVALID_ARG;
+    if ((int)in_dtype != TK_DTYPE_BF16 && (int)in_dtype != TK_DTYPE_FP32)
+        return TK_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || !std::isfinite(eps))
+        return TK_ERR_INVALID_ARG;
+    const int64_t groups = hidden / (group_size ? group_size : hidden);
+    ScaleSpec sp;
+    if (!scale_spec((int)scale_fmt, n, groups, sp))
+        return TK_ERR_INVALID_ARG;
+    if (n > 0 && (!x || !weight || (!codes != !scales) || (!codes && !residual_out && !y && !rstd)))
+        return TK_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+        !aligned(y, 16) || !aligned(rstd, 4) || !aligned(codes, 8) || !aligned(scales, sp.align))
+        return TK_ERR_INVALID_ARG;
+    const bool f32 = (int)in_dtype == TK_DTYPE_FP32;
+    const size_t elems = (size_t)n * (size_t)hidden, t_bytes = elems * (f32 ? 4u : 2u);
+    if (n > 0) {
+        struct Span {
+            const void* p;
+            size_t bytes;
+        };
+        const Span in[] = {{x, t_bytes}, {residual, t_bytes}, {weight, (size_t)hidden * 4u}};
+        const Span out[] = {{residual_out, t_bytes}, {y, elems * 2u}, {rstd, (size_t)n * 4u}, {codes, elems},
+                            {scales, sp.bytes}};
+        for (int i = 0; i < 5; ++i) {
+            for (int j = 0; j < 3; ++j) {
+                if (i == 0 && j < 2 && out[i].p == in[j].p)
+                    continue; // the stream updated in place
+                if (overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+                    return TK_ERR_INVALID_ARG;
+            }
+            for (int j = 0; j < i; ++j)
+                if (overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+                    return TK_ERR_INVALID_ARG;
+        }
+    }
+    if (hidden > kMaxHidden)
+        return TK_ERR_UNSUPPORTED;
+    if (n == 0)
+        return TK_OK;
+
+    NormParams p{};
+    p.x = x;
+    p.residual = residual;
+    p.weight = weight;
+    p.residual_out = residual_out;
+    p.y = y;
+    p.rstd = rstd;
+    p.n = (uint32_t)n;
+    p.inv_hidden = 1.0 / (double)hidden;
+    p.eps = (double)eps;
+    p.q.codes = static_cast<uint8_t*>(codes);
+    p.q.scales = scales;
+    p.q.scale_layout = sp.layout;
+    p.q.scale_ld = sp.ld;
+    p.q.slots = (uint32_t)(hidden / kSlotCols);
+    p.q.groups_row = (uint32_t)groups;
+    p.q.gslots = p.q.slots / p.q.groups_row;
+    int gm = kGroupLds;
+    if (groups == 1) {
+        gm = kGroupRow;
+    } else if ((p.q.gslots & (p.q.gslots - 1)) == 0 && p.q.gslots <= (uint32_t)kWaveSize) {
+        gm = kGroupLanes;
+        p.q.gl_log2 = (uint32_t)__builtin_ctz(p.q.gslots);
+    } else {
+        p.q.gmagic = (uint32_t)(((1ull << 32) + p.q.gslots - 1) / p.q.gslots);
+    }
+    const uint32_t steps = (p.q.slots + kWaveSize - 1) / kWaveSize;
+    const uint32_t S = steps_per_wave(steps, n >= 2048 ? 4u : 1u);
+    p.waves = (steps + S - 1) / S;
+    const uint32_t rows = p.waves == 1 ? 4u : 1u;
+    const uint32_t blocks = (p.n + rows - 1) / rows;
+    const dim3 grid(blocks < kMaxBlocks ? blocks : kMaxBlocks), block(rows * p.waves * kWaveSize);
+    const size_t lds = (size_t)rows * (p.q.slots + p.q.groups_row) * 4u;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+#define TK_NORM(SS)                                                                      \
+    case SS:                                                                             \
+        if (block.x <= 256)                                                              \
+            f32 ? launch_norm_gm<true, SS, 256>(gm, sp.kind, p, grid, block, lds, s)      \
+                : launch_norm_gm<false, SS, 256>(gm, sp.kind, p, grid, block, lds, s);    \
+        else                                                                             \
+            f32 ? launch_norm_gm<true, SS, 1024>(gm, sp.kind, p, grid, block, lds, s)     \
+                : launch_norm_gm<false, SS, 1024>(gm, sp.kind, p, grid, block, lds, s);   \
+        break;
+    switch (S) {
+        TK_NORM(1)
+        TK_NORM(2)
+        TK_NORM(4)
+    }
+#undef TK_NORM
+    return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
+}
+
+tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, const float* weight,
+                              const float* rstd, const void* dresidual, int64_t n, int64_t hidden, void* dx,
+                              float* dweight, float* workspace, void* stream)
+{
+    if (n < 0 || n >= (int64_t)INT_MAX || hidden <= 0 || hidden % kSlotCols != 0 || hidden > (int64_t)INT_MAX / 8)
+        return TK_ERR_INVALID_ARG;
+    if ((int)in_dtype != TK_DTYPE_BF16 && (int)in_dtype != TK_DTYPE_FP32)
+        return TK_ERR_INVALID_ARG;
+    if (n > 0 && (!dy || !h || !weight || !rstd || !dx || (dweight && !workspace)))
+        return TK_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(rstd, 4) || !aligned(dresidual, 16) ||
+        !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(workspace, 16))
+        return TK_ERR_INVALID_ARG;
+    const bool f32 = (int)in_dtype == TK_DTYPE_FP32;
+    const size_t t_bytes = (size_t)n * (size_t)hidden * (f32 ? 4u : 2u), w_bytes = (size_t)hidden * 4u;
+    const uint32_t parts = (uint32_t)(n < TK_RMSNORM_PARTS ? n : TK_RMSNORM_PARTS);
+    const size_t ws_bytes = dweight ? (size_t)parts * w_bytes : 0;
+    {
+        const void* in[] = {dy, h, dresidual, weight, rstd};
+        const size_t in_bytes[] = {t_bytes, t_bytes, t_bytes, w_bytes, (size_t)n * 4u};
+        const void* out[] = {dx, dweight, workspace};
+        const size_t out_bytes[] = {t_bytes, w_bytes, ws_bytes};
+        for (int i = 0; i < 3; ++i) {
+            for (int j = 0; j < 5; ++j) {
+                if (i == 0 && (j == 0 || j == 2) && out[i] == in[j])
+                    continue; // a gradient replaced in place
+                if (overlaps(out[i], out_bytes[i], in[j], in_bytes[j]))
+                    return TK_ERR_INVALID_ARG;
+            }
+            for (int j = 0; j < i; ++j)
+                if (overlaps(out[i], out_bytes[i], out[j], out_bytes[j]))
+                    return TK_ERR_INVALID_ARG;
+        }
+    }
+    if (hidden > kMaxHidden)
+        return TK_ERR_UNSUPPORTED;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (n > 0) {
+        NormBwdParams p{};
+        p.dy = dy;
+        p.h = h;
+        p.weight = weight;
+        p.rstd = rstd;
+        p.dresidual = dresidual;
+        p.dx = dx;
+        p.partial = dweight ? workspace : nullptr;
+        p.n = (uint32_t)n;
+        p.slots = (uint32_t)(hidden / kSlotCols);
+        p.inv_hidden = 1.0f / (float)hidden;
+        const uint32_t steps = (p.slots + kWaveSize - 1) / kWaveSize;
+        const uint32_t S = steps_per_wave(steps, 1u);
+        const dim3 grid(parts), block((steps + S - 1) / S * kWaveSize);
+#define TK_NORM_BWD(SS)                                                                                        \
+    case SS:                                                                                                   \
+        if (f32)                                                                                               \
+            hipLaunchKernelGGL((rmsnorm_backward_kernel<true, SS, 1024>), grid, block, 0, s, p);               \
+        else                                                                                                   \
+            hipLaunchKernelGGL((rmsnorm_backward_kernel<false, SS, 1024>), grid, block, 0, s, p);              \
+        break;
+        switch (S) {
+            TK_NORM_BWD(1)
+            TK_NORM_BWD(2)
+            TK_NORM_BWD(4)
+        }
+#undef TK_NORM_BWD
+        if (hipGetLastError() != hipSuccess)
+            return TK_ERR_HIP;
+    }
+    if (dweight) {
+        hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((uint32_t)((hidden + kWaveSize - 1) / kWaveSize)), dim3(1024),
+                           0, s, workspace, parts, (uint32_t)hidden, dweight);
+        if (hipGetLastError() != hipSuccess)
+            return TK_ERR_HIP;
+    }
+    return TK_OK;
+}
+
+} // extern "C"

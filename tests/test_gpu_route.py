@@ -1,0 +1,208 @@
+"""tk_route and tk_route_backward on the GPU against the plain 64-bit reference:
+indices equal, weights within their one rounding, gradients within bounds that
+count roundings."""
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as ref
+import moe_activation_bit_amd as tk
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+OK = tk.TkStatus.TK_OK
+PAD = 64
+
+
+def say(*a):
+    print("[gpu-case]", *a, flush=True)
+
+
+def up(a):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def make(seed, T, E, bf16, masked=0.0, sigma=2.0):
+    rng = np.random.default_rng(seed)
+    x = (sigma * rng.standard_normal((T, E))).astype(np.float32)
+    x[rng.random((T, E)) < masked] = -np.inf
+    return ref.round_bf16(x) if bf16 else x, (0.1 * rng.standard_normal(E)).astype(np.float32)
+
+
+def run_route(x, bf16, bias, k, ng, tg, softmax, normalise, scale=2.5):
+    T, E = x.shape
+    idx = torch.full((T * k + 2 * PAD,), -77, dtype=torch.int32, device=DEV)
+    w = torch.full((T * k + 2 * PAD,), -77.0, dtype=torch.float32, device=DEV)
+    xd = up(ref.bf16_bits(x).view(np.int16)) if bf16 else up(x)
+    rc = tk.tk_route(xd, tk.TK_DTYPE_BF16 if bf16 else tk.TK_DTYPE_FP32, up(bias), T, E, k, ng, tg,
+                     tk.TK_SCORE_SOFTMAX if softmax else tk.TK_SCORE_SIGMOID, normalise, scale,
+                     idx.data_ptr() + 4 * PAD, w.data_ptr() + 4 * PAD)
+    assert rc == OK, tk.tk_status_str(rc)
+    torch.cuda.synchronize()
+    i, ww = idx.cpu().numpy(), w.cpu().numpy()
+    for a in (i, ww):
+        assert (a[:PAD] == -77).all() and (a[PAD + T * k:] == -77).all(), "canary"
+    return i[PAD:PAD + T * k].reshape(T, k), ww[PAD:PAD + T * k].reshape(T, k)
+
+
+def check_route(x, bias, k, ng, tg, softmax, normalise, got, scale=2.5):
+    idx, w = ref.route(x, bias, k, ng, tg, softmax, normalise, scale)
+    assert np.array_equal(got[0], idx), f"indices differ at {np.argwhere(got[0] != idx)[:3].tolist()}"
+    assert np.array_equal(np.isnan(got[1]), np.isnan(w))
+    # computed in 64 bits and rounded once (2^-149: half the smallest fp32 step, and room for its 64-bit error)
+    assert np.all(np.isnan(w) | (np.abs(got[1] - w) <= ref.U32 * (1 + 2.0 ** -10) * np.abs(w) + 2.0 ** -149)), "weights"
+
+
+SHAPES = [  # experts, k, groups, kept groups
+    (1, 1, 1, 1), (2, 2, 1, 1), (8, 2, 1, 1), (33, 5, 1, 1), (60, 4, 1, 1), (64, 6, 1, 1), (64, 64, 1, 1), (100, 3, 1, 1),
+    (128, 8, 1, 1), (129, 9, 1, 1), (160, 6, 1, 1), (256, 8, 1, 1), (256, 16, 1, 1), (256, 17, 1, 1), (300, 8, 1, 1),
+    (384, 8, 1, 1), (512, 8, 1, 1), (512, 64, 1, 1), (500, 33, 1, 1),
+    (256, 8, 8, 4), (256, 8, 8, 1), (256, 8, 8, 8), (256, 8, 4, 2), (256, 4, 2, 1), (160, 6, 8, 3), (96, 5, 3, 2),
+    (72, 4, 8, 2), (64, 8, 32, 4), (512, 8, 16, 8), (512, 8, 256, 9), (100, 7, 5, 2), (128, 16, 8, 4), (64, 4, 4, 2),
+    (192, 8, 8, 4), (14, 3, 7, 2),
+]
+
+
+@pytest.mark.parametrize("E,k,ng,tg", SHAPES)
+@pytest.mark.parametrize("softmax", [False, True])
+def test_route(E, k, ng, tg, softmax):
+    say("route", E, k, ng, tg, softmax)
+    for n, (T, bf16, with_bias, normalise, masked) in enumerate([
+            (1, False, True, 1, 0.0), (37, False, True, 1, 0.0), (64, True, False, 0, 0.0), (18, True, True, 0, 0.3),
+            (13, False, False, 1, 0.9), (5, True, True, 1, 0.99)]):
+        x, bias = make(E * 100 + k + n, T, E, bf16, masked)
+        b = bias if with_bias else None
+        check_route(x, b, k, ng, tg, softmax, normalise, run_route(x, bf16, b, k, ng, tg, softmax, normalise))
+
+
+@pytest.mark.parametrize("E,k,ng,tg", [(256, 8, 8, 4), (64, 6, 1, 1), (512, 8, 16, 8), (160, 8, 8, 3)])
+def test_route_ties_extremes_and_masks(E, k, ng, tg):
+    say("route values", E, k, ng, tg)
+    rng = np.random.default_rng(E)
+    x, bias = make(E, 24, E, False)
+    x[0] = 0.0                                         # every expert ties
+    x[1] = rng.integers(-2, 3, E)                      # many ties
+    x[2] = -np.inf                                     # nothing remains
+    x[3] = -np.inf
+    x[3, E // 2] = 1.0                                 # one remains
+    x[4] = 40 + rng.standard_normal(E)                 # sigmoid saturates: equal rounded scores
+    x[5] = -300 - 50 * rng.random(E)                   # scores below fp32
+    x[6] = -3e38
+    x[7] = np.where(rng.random(E) < 0.5, 3e38, -3e38)
+    x[8, ::2] = -np.inf
+    x[9] = np.where(np.arange(E) < E - 1, -np.inf, -1000.0)
+    x[10, 3] = np.nan
+    x[11] = np.nan
+    x[12, 5] = np.inf
+    x[13, 1], x[13, 2] = np.inf, -np.inf
+    x[14] = np.finfo(np.float32).tiny * rng.standard_normal(E)
+    x[15] = -0.0
+    x[15, ::3] = 0.0
+    b2 = bias.copy()
+    b2[::5] = -np.inf                                  # masked by the bias
+    b2[3] = 3e38
+    for softmax in (False, True):
+        for normalise in (0, 1):
+            for b in (None, bias, b2, np.zeros(E, np.float32)):
+                check_route(x, b, k, ng, tg, softmax, normalise, run_route(x, False, b, k, ng, tg, softmax, normalise))
+
+
+def test_route_tokens_do_not_depend_on_their_number():
+    say("route batch")
+    x, bias = make(1, 3000, 256, False)
+    i, w = run_route(x, False, bias, 8, 8, 4, False, 1)
+    for lo, hi in ((0, 1), (5, 8), (2990, 3000)):
+        i2, w2 = run_route(x[lo:hi], False, bias, 8, 8, 4, False, 1)
+        assert np.array_equal(i[lo:hi], i2) and np.array_equal(w[lo:hi].view(np.uint32), w2.view(np.uint32))
+
+
+def test_route_large():
+    say("route large")
+    for E, k, ng, tg, softmax, bf16, masked in ((256, 8, 8, 4, False, False, 0.0), (64, 6, 1, 1, True, True, 0.1)):
+        x, bias = make(2, 20000, E, bf16, masked)
+        b = bias if ng > 1 else None
+        check_route(x, b, k, ng, tg, softmax, ng > 1, run_route(x, bf16, b, k, ng, tg, softmax, ng > 1))
+
+
+# ---- backward -----------------------------------------------------------------------------------
+
+
+def run_backward(dw, idx, x, bf16, softmax, normalise, scale=2.5):
+    T, E = x.shape
+    k, item = idx.shape[1], 2 if bf16 else 4
+    out = torch.full((T * E * item + 2 * PAD,), 0xC3, dtype=torch.uint8, device=DEV)
+    xd = up(ref.bf16_bits(x).view(np.int16)) if bf16 else up(x)
+    rc = tk.tk_route_backward(up(dw), up(idx), xd, tk.TK_DTYPE_BF16 if bf16 else tk.TK_DTYPE_FP32, T, E, k,
+                              tk.TK_SCORE_SOFTMAX if softmax else tk.TK_SCORE_SIGMOID, normalise, scale,
+                              out.data_ptr() + PAD)
+    assert rc == OK, tk.tk_status_str(rc)
+    torch.cuda.synchronize()
+    o = out.cpu().numpy()
+    assert (o[:PAD] == 0xC3).all() and (o[PAD + T * E * item:] == 0xC3).all(), "canary"
+    body = o[PAD:PAD + T * E * item]
+    return (ref.bf16_value(body.view(np.uint16)) if bf16 else body.view(np.float32)).reshape(T, E)
+
+
+def check_backward(dw, idx, x, bf16, softmax, normalise, got):
+    want, mag = ref.route_backward(dw, idx, x, softmax, normalise, 2.5)
+    live = x[np.isfinite(x)]
+    reach = float(live.max() - live.min()) if live.size else 0.0
+    # an fp32 exponential's argument is off by half a step of its size, twice where a score is a ratio of them;
+    # the sums' depth is 8 additions on a lane and 6 over the lanes, twice; some 16 roundings besides
+    bound = ref.U32 * mag * (3 * reach + 2 * 14 + 16) + (ref.UB16 if bf16 else ref.U32) * np.abs(want) + 2.0 ** -126
+    err = np.abs(got - want)
+    assert np.all(err <= bound), f"off by {np.max(err / bound):.2f} of the bound"
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 2), (33, 5), (64, 6), (100, 8), (160, 6), (256, 8), (300, 64), (512, 8)])
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("normalise", [0, 1])
+def test_backward(E, k, softmax, normalise):
+    say("route backward", E, k, softmax, normalise)
+    for n, (T, bf16, masked) in enumerate([(1, False, 0.0), (41, False, 0.0), (23, True, 0.0), (18, False, 0.4)]):
+        rng = np.random.default_rng(E * 10 + k + n)
+        x, _ = make(E + n, T, E, bf16, masked)
+        idx, _ = ref.route(x, None, k, 1, 1, softmax, normalise, 2.5)
+        idx[rng.random(idx.shape) < 0.05] = -1
+        dw = rng.standard_normal((T, k)).astype(np.float32)
+        check_backward(dw, idx, x, bf16, softmax, normalise, run_backward(dw, idx, x, bf16, softmax, normalise))
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("normalise", [0, 1])
+def test_backward_absent_repeated_and_extreme(softmax, normalise):
+    say("route backward values", softmax, normalise)
+    rng = np.random.default_rng(3)
+    x, _ = make(7, 12, 48, False)
+    idx = np.argsort(-x, axis=1, kind="stable")[:, :6].astype(np.int32)
+    idx[0] = -1                                   # every slot absent
+    idx[1, 2:] = [idx[1, 0], 48, -5, idx[1, 1]]   # repeats and entries out of range
+    x[2] = -200 - 5 * rng.random(48)              # scores below fp32 share the weight all the same
+    x[3] = 60 + rng.standard_normal(48)           # saturated
+    x[4, idx[4, 1:]] = -np.inf                    # masked but for one
+    dw = rng.standard_normal((12, 6)).astype(np.float32)
+    dw[5] = 0
+    got = run_backward(dw, idx, x, False, softmax, normalise)
+    check_backward(dw, idx, x, False, softmax, normalise, got)
+    assert not got[0].any() and not got[5].any()
+
+
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("normalise", [0, 1])
+def test_backward_of_the_forward_is_the_difference_quotient(softmax, normalise):
+    say("route backward differences", softmax, normalise)
+    x, bias = make(9, 16, 64, False, sigma=1.0)
+    idx, _ = run_route(x, False, bias, 6, 8, 4, softmax, normalise)
+    rng, t = np.random.default_rng(1), 1e-4
+    dw = rng.standard_normal(idx.shape).astype(np.float32)
+    g = run_backward(dw, idx, x, False, softmax, normalise).astype(np.float64)
+    for _ in range(4):
+        u = rng.standard_normal(x.shape)
+
+        def loss(s):
+            p = ref.scores(x.astype(np.float64) + s * u, softmax)
+            w = np.take_along_axis(p, idx.astype(np.int64), 1)
+            return 2.5 * (dw * (w / w.sum(1, keepdims=True) if normalise else w)).sum()
+
+        # about 100 terms of order 1, some 30 roundings each, and t^2
+        assert abs((loss(t) - loss(-t)) / (2 * t) - (g * u).sum()) <= 100 * 30 * ref.U32 + 1e-6
