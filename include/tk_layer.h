@@ -200,7 +200,7 @@ tk_status tk_route_backward(const float* dweight, const int32_t* topk_idx, const
  *  group_size   0 (one scale a row) or a divisor of in_features: a multiple of
  *               32 for UE8M0, of 128 for FP32 (other widths that divide:
  *               TK_ERR_UNSUPPORTED); x_group likewise.
- *  experts      1..2^20;  out_features  1..2^24;  in_features  a positive
+ *  experts      1..32768;  out_features  1..2^24;  in_features  a positive
  *               multiple of 32, at most 2^20.
  *  out_dtype    TK_DTYPE_BF16 or TK_DTYPE_FP32.
  *  out          [tokens*k, out_features], aligned to the element.

@@ -4,6 +4,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "tk.h"
 #include "tk_layer.h"
@@ -33,10 +34,11 @@ struct GemvParams {
     int x_kind, scale_u8, out_bf16;
     uint32_t group_magic, x_group_magic;       // of the groups' width in blocks of 32 columns
     uint32_t group_magic128, x_group_magic128; // ... in steps of 128
-    uint32_t steps;      // of kBlock columns, the last part-filled when in_features is no multiple
+    uint32_t steps;      // of kStep columns, the last part-filled when in_features is no multiple
     uint32_t steps_wave; // a wave's share of them
     uint32_t ks;         // waves that share a tile's columns: 1, 2 or 4
-    uint32_t grid_y;     // rows, or experts and one more
+    uint32_t tiles;      // tiles of 16 weight rows a wave goes through
+    uint32_t lds_x;      // bytes for staged rows
     int by_row;
 };
 
@@ -44,250 +46,398 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 
+// ceil(2^32 / d), by which divide() is exact for q * d < 2^32; 0 stands for d = 1
+__host__ __device__ __forceinline__ uint32_t magic(uint32_t d) { return d <= 1u ? 0u : 0xFFFFFFFFu / d + 1u; }
 // q / d by d's magic()
 __device__ __forceinline__ uint32_t divide(uint32_t q, uint32_t magic) { return magic ? __umulhi(q, magic) : q; }
 
-constexpr int kTile = 16;   // weight rows and x rows of a matrix instruction
-constexpr int kBlock = 128; // columns of a step
+// two of a word's four E4M3 codes, the lower or the upper ones, times a power of two
+template <bool UPPER>
+__device__ __forceinline__ uint32_t fp8_to_bf16(uint32_t codes, float scale)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, UPPER));
+}
+
+// x, opaque to the compiler: what is derived from it inside a loop stays there
+// instead of being computed before the loop and held (or spilled) through it
+__device__ __forceinline__ uint32_t here(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// LDS that only this wave's lanes exchange through: what was written before is
+// read after, with no wait on the other waves
+__device__ __forceinline__ void wave_exchange()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// f(0), f(1), ... f(N - 1), each with its number as a constant
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void for_slots(F&& f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        for_slots<N, I + 1>(f);
+    }
+}
+
+constexpr int kTile = 16;            // weight rows and x rows of a matrix instruction
+constexpr int kStep = 256;           // columns of a step: 128 bytes, a cache line, of each weight row
+constexpr int kAhead = 2;            // steps of weights in flight
+constexpr uint32_t kMaxStage = 16;   // steps staged at a time at most
+constexpr uint32_t kStepBytes = 512; // a staged x row's bytes a step
+constexpr uint32_t kRowPad = 16;     // between staged x rows, which would else share their LDS banks
+constexpr uint32_t kScalePitch = 8 * kMaxStage + 8; // bytes of a weight row's staged scales
 
 // Matrix instructions on 16 weight rows at a time, for up to 16 * NT of the
-// rows that chose the expert.  In a step of 128 columns lane (r, q) = (l & 15,
-// l >> 4) holds weight row r's 32 codes of columns 32q.. (16 bytes, within one
-// group) and x row r's same columns.  Codes and FP8 activations become bf16 in
+// rows that chose the expert.  Codes and FP8 activations become bf16 in
 // registers, with their UE8M0 scales on the way: both are exact (two and four
-// significant bits), and the products and sums of the four 16x16x32 bf16
-// instructions of a step are those of fp32.  (The E2M1 x E4M3 instruction would
-// take the codes as they are, but drops what lies 2^-14 below the largest
-// product of a step: random E4M3 bytes gave sums off by up to 7.7e-5 of their
-// terms' magnitude, where the bf16 instructions were exact.)
+// significant bits), and the products and sums of the 16x16x32 bf16
+// instructions are those of fp32.  (The E2M1 x E4M3 instruction would take the
+// codes as they are, but drops what lies 2^-14 below the largest product of a
+// step: random E4M3 bytes gave sums off by up to 7.7e-5 of their terms'
+// magnitude, where the bf16 instructions were exact.)
+//
+// What bounds it is the weights' bytes, so everything else keeps out of their
+// way.  A wave reads a step's 16 x 128 bytes with two instructions of eight
+// whole lines (lane l: row l / 8, 16 bytes l % 8), kAhead steps before their
+// use, and passes them through 2 KiB of LDS of its own into the instruction's
+// layout, lane (r, q) = (l & 15, l >> 4): weight row r, columns 32q.. of each
+// half.  (Read in that layout, a line is asked for by two instructions and the
+// lines in flight overfill the L1: 30.2 us instead of 25.8 for a bare stream of
+// the 7168 -> 4096 top-8 weights.)  The x rows, as bf16, and the scales are
+// staged in LDS, at most kMaxStage steps at a time (scales read step by step
+// cost as many line requests as the weights: 25.8 instead of 24.7 us).
 // fp32 scales enter afterwards: one scale a row in the epilogue, one for 128
-// columns or a multiple of that (PART) on each step's own result.
+// columns or a multiple of that on each half step's own result (PART 1: the
+// activations' alone; 2: the weights' too).
 // A result's column n (x row) is lane & 15, its rows 4q .. 4q + 3.
-//   WS 0: UE8M0, groups of 32, whole pairs of steps: a pair's eight scales of a
-//     row are one load;  1: any group width;  2: a last step part-filled too.
-template <bool FP8X, bool PART, int NT, int WS>
-struct GemvWave {
-    const GemvParams& p;
-    uint32_t r, q;
-    const uint8_t* w_row;  // this lane's weight row
-    const uint8_t* s_row;  // its UE8M0 scales
-    const char* x_row[NT]; // this lane's x rows
-    const void* xs_row[NT];
-    size_t tile_row;       // the tile's first row of weights, over all experts
-    v4f acc[NT];
-
-    __device__ __forceinline__ explicit GemvWave(const GemvParams& pp) : p(pp) {}
-
-    __device__ __forceinline__ uint32_t w_scale(uint32_t b) const
-    {
-        if (!p.scale_u8)
-            return 127u;
-        const uint32_t g = min(4u * b + q, p.in_features / 32u - 1u);
-        return s_row[divide(g, p.group_magic)];
-    }
-    __device__ __forceinline__ uint32_t x_scale(int nt, uint32_t b) const
-    {
-        if (p.x_kind != kXFp8E8)
-            return 127u;
-        const uint32_t g = min(4u * b + q, p.in_features / 32u - 1u);
-        return static_cast<const uint8_t*>(xs_row[nt])[divide(g, p.x_group_magic)];
-    }
-    // the 16 bytes at column c of a row, zeros past its end
-    __device__ __forceinline__ uint4 load(const char* row, uint32_t c, uint32_t bytes_num, uint32_t bytes_den) const
-    {
-        if (WS == 2 && c >= p.in_features)
-            return make_uint4(0, 0, 0, 0);
-        return *reinterpret_cast<const uint4*>(row + (size_t)c * bytes_num / bytes_den);
-    }
-
-    template <int U>
-    __device__ __forceinline__ void steps(uint32_t b, uint32_t ntiles)
-    {
-        uint4 w[U];
-        uint32_t ws[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            w[u] = load(reinterpret_cast<const char*>(w_row), (b + u) * kBlock + 32u * q, 1, 2);
-        if constexpr (WS == 0) {
-#pragma unroll
-            for (int u = 0; u < U; u += 2) {
-                const uint2 s = *reinterpret_cast<const uint2*>(s_row + 4u * (b + u));
-                ws[u] = (s.x >> (8u * q)) & 255u;
-                ws[U > 1 ? u + 1 : 0] = (s.y >> (8u * q)) & 255u;
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                ws[u] = w_scale(b + u);
-        }
-        // fp32 scales of the weights by group, for the result's four rows
-        float sw[PART ? U : 1][4];
-        const bool w_part = PART && !p.scale_u8 && p.groups > 1;
-        if constexpr (PART) {
-            if (w_part) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const size_t row = min(tile_row + 4u * q + i, (size_t)p.experts * p.out_features - 1u);
-                        sw[u][i] = static_cast<const float*>(p.scales)[row * p.groups + divide(b + u, p.group_magic128)];
-                    }
-            }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && (uint32_t)nt >= ntiles)
-                break; // wave-uniform
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                v4f c = PART ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[nt];
-                const float s = as_float(ws[u] << 23); // only the exponent is looked at: 0 is 2^-127, 255 NaN
-                const uint32_t w4[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-                const uint32_t col = (b + u) * kBlock + 32u * q;
-                v8b B[4];
-                if constexpr (FP8X) {
-                    const uint4 x0 = load(x_row[nt], col, 1, 1), x1 = load(x_row[nt], col + 16u, 1, 1);
-                    const uint32_t x8[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                    const float sx = as_float(x_scale(nt, b + u) << 23);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const v2b a0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x8[2 * i], sx, false);
-                        const v2b a1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x8[2 * i], sx, true);
-                        const v2b a2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x8[2 * i + 1], sx, false);
-                        const v2b a3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x8[2 * i + 1], sx, true);
-                        B[i] = v8b{a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        B[i] = __builtin_bit_cast(v8b, load(x_row[nt], col + 8u * i, 2, 1));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const v2b a0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w4[i], s, 0);
-                    const v2b a1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w4[i], s, 1);
-                    const v2b a2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w4[i], s, 2);
-                    const v2b a3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w4[i], s, 3);
-                    const v8b A = {a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
-                    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B[i], c, 0, 0, 0);
-                }
-                if constexpr (PART) {
-                    const float sx = FP8X && p.x_kind == kXFp8F32 && p.x_groups > 1
-                                         ? static_cast<const float*>(xs_row[nt])[divide(b + u, p.x_group_magic128)]
-                                         : 1.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[nt][i] = __builtin_fmaf(c[i], w_part ? sx * sw[u][i] : sx, acc[nt][i]);
-                } else {
-                    acc[nt] = c;
-                }
-            }
-        }
-    }
-};
-
-// One workgroup: KS waves along the columns of each of 4 / KS tiles of 16
-// weight rows.  Its rows are those whose expert is e, in order, 16 * NT at a
-// time.  by_row: blockIdx.y is a row, and the first row of an expert does the
-// work of all of them; else blockIdx.y is an expert, and the one past the last
-// writes the absent rows' zeros.
-template <bool FP8X, bool PART, int NT, int WS>
-__global__ __launch_bounds__(kThreads) void gemv_fp4_kernel(GemvParams p)
+//   FAST: UE8M0 weight scales of 32 columns and whole steps; else any.
+template <int XK, int PART, int NT, bool FAST>
+__global__ __launch_bounds__(kThreads, PART == 2 || NT == 2 ? 3 : 4) void gemv_fp4_kernel(GemvParams p)
 {
     constexpr uint32_t kWaves = kThreads / kWaveSize, kRows = kTile * NT;
     __shared__ uint32_t s_list[kWaves][kRows];
+    __shared__ v4u s_w4[kWaves][kTile * 8];
+    __shared__ uint2 s_ws2[kWaves][kTile * kScalePitch / 8];
     __shared__ v4f s_acc[kWaves][NT][kWaveSize];
+    extern __shared__ uint4 s_x4[]; // the staged rows, then their fp32 scales
+    char* const s_x = reinterpret_cast<char*>(s_x4);
+    float* const s_sx = reinterpret_cast<float*>(s_x + p.lds_x);
     const uint32_t lane = threadIdx.x & (kWaveSize - 1);
+    const uint32_t r = lane & 15u, q = lane >> 4;
     const uint32_t wv = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
     const uint32_t ks = wv & (p.ks - 1u), rt = wv / p.ks;
-    const uint32_t o0 = (blockIdx.x * (kWaves / p.ks) + rt) * kTile; // this wave's first weight row of the expert
+    // this wave's weight rows of an expert: tiles o_first, + o_next, ... of which it has p.tiles
+    const uint32_t o_next = kWaves / p.ks * kTile;
+    const uint32_t o_first = blockIdx.x * p.tiles * o_next + rt * kTile;
+    // its steps of a row: `share` from b0 on (none from step 0 on when the waves before it have them all)
+    const uint32_t share = ks * p.steps_wave < p.steps ? min(p.steps_wave, p.steps - ks * p.steps_wave) : 0u;
+    const uint32_t b0 = share ? ks * p.steps_wave : 0u;
+    const uint32_t last_step = share ? share - 1u : 0u;
     const uint64_t below = (1ull << lane) - 1u;
+    const bool x_part = PART != 0 && XK == kXFp8F32 && p.x_groups > 1;
+    // x rows of a pass: what leaves room for kAhead steps of each
+    const uint32_t pass_rows = min(kRows, p.lds_x / (p.ks * (kAhead * kStepBytes + kRowPad)));
+    // LDS slots of this lane's weights: row r keeps columns 32p.. in slot p ^ (r / 2), so that neither the
+    // writes nor the reads of 16 rows meet in a bank
+    const uint32_t lrow = lane >> 3, lpiece = lane & 7u;
+    v4u* const w_put = s_w4[wv] + lrow * 8u + (lpiece ^ (lrow >> 1));
+    v4u* const w_put8 = s_w4[wv] + (lrow + 8u) * 8u + (lpiece ^ ((lrow + 8u) >> 1));
+    const v4u* const w_get = s_w4[wv] + r * 8u + (q ^ (r >> 1));
+    const v4u* const w_get4 = s_w4[wv] + r * 8u + ((q + 4u) ^ (r >> 1));
+    char* const s_ws = reinterpret_cast<char*>(s_ws2[wv]);
 
-    for (uint32_t y = blockIdx.y; y < p.grid_y; y += gridDim.y) {
-        uint32_t e = 0, next = 0;
-        if (p.idx) {
-            if (p.by_row) {
-                next = y;
-                e = (uint32_t)p.idx[y];
-                bool earlier = false;
-                for (uint32_t base = 0; base < y; base += kWaveSize)
-                    earlier |= base + lane < y && (uint32_t)p.idx[base + lane] == e;
-                if (e < p.experts && __builtin_amdgcn_ballot_w64(earlier) != 0)
-                    continue; // an earlier row's workgroup does this one (the same for all its waves)
-            } else {
-                e = y;
+    // One workgroup: ks waves along the columns of each of kWaves / ks tiles of
+    // 16 weight rows.  Its rows are those whose expert is e, in order,
+    // pass_rows at a time.  by_row: y is a row, and the first row of an expert
+    // does the work of all of them; else y is an expert, and the one past the
+    // last writes the absent rows' zeros.  Every branch around a barrier is the
+    // same for all waves.
+    const uint32_t y = blockIdx.y;
+    uint32_t e = 0, next = 0;
+    if (p.idx) {
+        if (p.by_row) {
+            next = y;
+            e = (uint32_t)p.idx[y];
+            bool earlier = false;
+            for (uint32_t base = 0; base < y; base += kWaveSize)
+                earlier |= base + lane < y && (uint32_t)p.idx[base + lane] == e;
+            if (e < p.experts && __builtin_amdgcn_ballot_w64(earlier) != 0)
+                return; // an earlier row's workgroup does this one
+        } else {
+            e = y;
+        }
+    }
+    if (e >= p.experts) { // absent rows: this one, or all of them
+        for (uint32_t row = p.by_row ? y : 0u; row < (p.by_row ? y + 1u : p.rows); ++row) {
+            if ((uint32_t)p.idx[row] < p.experts)
+                continue;
+            for (uint32_t i = threadIdx.x; i < p.tiles * o_next; i += kThreads) {
+                const uint32_t o = blockIdx.x * p.tiles * o_next + i;
+                if (o >= p.out_features)
+                    break;
+                if (p.out_bf16)
+                    static_cast<uint16_t*>(p.out)[(size_t)row * p.out_features + o] = 0;
+                else
+                    static_cast<float*>(p.out)[(size_t)row * p.out_features + o] = 0.0f;
             }
         }
-        if (e >= p.experts) { // absent rows: this one, or all of them
-            for (uint32_t row = p.by_row ? y : 0u; row < (p.by_row ? y + 1u : p.rows); ++row) {
-                if ((uint32_t)p.idx[row] < p.experts)
-                    continue;
-                const uint32_t o = blockIdx.x * (kWaves / p.ks) * kTile + threadIdx.x;
-                if (threadIdx.x < (kWaves / p.ks) * kTile && o < p.out_features) {
-                    if (p.out_bf16)
-                        static_cast<uint16_t*>(p.out)[(size_t)row * p.out_features + o] = 0;
-                    else
-                        static_cast<float*>(p.out)[(size_t)row * p.out_features + o] = 0.0f;
-                }
-            }
-            continue;
-        }
-        while (true) {
-            // ---- the next rows of this expert, at most kRows
-            uint32_t n = 0;
-            while (next < p.rows && n < kRows) {
-                const uint32_t base = next & ~(uint32_t)(kWaveSize - 1), row = base + lane;
-                const bool hit = row >= next && row < p.rows && (!p.idx || (uint32_t)p.idx[row] == e);
-                const uint64_t mask = __builtin_amdgcn_ballot_w64(hit);
-                const uint32_t rank = n + (uint32_t)__builtin_popcountll(mask & below);
-                if (hit && rank < kRows)
-                    s_list[wv][rank] = row;
-                const uint64_t left = __builtin_amdgcn_ballot_w64(hit && rank >= kRows);
-                next = left ? base + (uint32_t)__builtin_ctzll(left) : base + kWaveSize;
-                n = left ? kRows : n + (uint32_t)__builtin_popcountll(mask);
-            }
-            if (n == 0)
-                break; // the same for every wave of the workgroup
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+        return;
+    }
 
-            GemvWave<FP8X, PART, NT, WS> g(p);
-            g.r = lane & 15u;
-            g.q = lane >> 4;
-            g.tile_row = (size_t)e * p.out_features + o0;
-            const size_t w_row = (size_t)e * p.out_features + min(o0 + g.r, p.out_features - 1u);
-            g.w_row = p.codes + w_row * (p.in_features / 2u);
-            g.s_row = static_cast<const uint8_t*>(p.scales) + (p.scale_u8 ? w_row * p.groups : 0u);
-            uint32_t row[NT];
+    const size_t e_row = (size_t)e * p.out_features;
+    // The weights of the wave's steps go through kAhead slots of registers, over the tiles' ends: `cur` is the
+    // tile that is computed, `nxt` the one after it.  Tile rows past the last weight row read that row, and
+    // their results are not stored.
+    struct Tile {
+        const char* base;   // its first row (wave-uniform)
+        uint32_t off, off8; // bytes from there to this lane's 16 of row lane / 8, and of row lane / 8 + 8
+    };
+    auto tile = [&](uint32_t j) {
+        const uint32_t o = o_first + j * o_next, last = p.out_features - 1u, first = min(o, last);
+        const uint32_t row_bytes = p.in_features / 2u, ln = here(lane), lrow = ln >> 3, lpiece = ln & 7u;
+        return Tile{reinterpret_cast<const char*>(p.codes) + (e_row + first) * row_bytes,
+                    (min(o + lrow, last) - first) * row_bytes + 16u * lpiece,
+                    (min(o + lrow + 8u, last) - first) * row_bytes + 16u * lpiece};
+    };
+    v4u w0[kAhead], w1[kAhead];
+    auto fetch = [&](auto slot, const Tile& from, uint32_t t) { // the wave's step t of a tile into a slot
+        constexpr int u = decltype(slot)::value;
+        const uint32_t b = b0 + t;
+        if constexpr (FAST) {
+            const char* const at = from.base + (size_t)b * (kStep / 2);
+            w0[u] = *reinterpret_cast<const v4u*>(at + from.off);
+            w1[u] = *reinterpret_cast<const v4u*>(at + from.off8);
+        } else { // columns past the row's end: its first ones, made zero
+            const bool in = b * kStep + 32u * lpiece < p.in_features;
+            const uint32_t at = in ? b * (kStep / 2) : 0u - 16u * lpiece;
+            const v4u v0 = *reinterpret_cast<const v4u*>(from.base + (from.off + at));
+            const v4u v1 = *reinterpret_cast<const v4u*>(from.base + (from.off8 + at));
+            const uint32_t keep = in ? ~0u : 0u;
+            w0[u] = v0 & keep;
+            w1[u] = v1 & keep;
+        }
+    };
+    // The scales of a tile's rows, a byte for 32 columns, at the wave's steps t0 .. t0 + cnt - 1: lane l takes
+    // row l / 4.  FAST: through registers, so that the next tile's can be on their way during this one.
+    uint2 sreg[kMaxStage / 4];
+    auto scale_row = [&](uint32_t j) {
+        return (e_row + min(o_first + j * o_next + (lane >> 2), p.out_features - 1u)) * p.groups;
+    };
+    auto fetch_scales = [&](uint32_t j, uint32_t t0) {
+        if constexpr (FAST) {
+            const uint32_t o = o_first + j * o_next, last = p.out_features - 1u, first = min(o, last);
+            const char* const base = static_cast<const char*>(p.scales) + (e_row + first) * p.groups;
+            const uint32_t ln = here(lane), off = (min(o + (ln >> 2), last) - first) * p.groups;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                // columns past the last row repeat it and are not stored
-                row[nt] = s_list[wv][min(nt * kTile + g.r, n - 1u)];
-                const size_t xr = row[nt] / p.x_div;
-                g.x_row[nt] = static_cast<const char*>(p.x) + xr * p.in_features * (FP8X ? 1u : 2u);
-                g.xs_row[nt] = static_cast<const char*>(p.x_scales) + xr * p.x_groups * (p.x_kind == kXFp8F32 ? 4u : 1u);
-                g.acc[nt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-            }
-            const uint32_t ntiles = (n + kTile - 1) / kTile;
-            if (o0 < p.out_features) {
-                uint32_t b = ks * p.steps_wave;
-                const uint32_t end = min(b + p.steps_wave, p.steps);
-                for (; b + 4 <= end; b += 4)
-                    g.template steps<4>(b, ntiles);
-                if (b + 2 <= end) {
-                    g.template steps<2>(b, ntiles);
-                    b += 2;
+            for (uint32_t i = 0; i < kMaxStage / 4; ++i)
+                sreg[i] = *reinterpret_cast<const uint2*>(
+                    base + (off + 8u * min(b0 + t0 + 4u * i + (ln & 3u), p.steps - 1u)));
+        }
+    };
+    auto put_scales = [&](uint32_t j, uint32_t t0, uint32_t cnt) {
+        const uint32_t ln = here(lane);
+        char* const to = s_ws + (ln >> 2) * kScalePitch;
+        if constexpr (FAST) {
+#pragma unroll
+            for (uint32_t i = 0; i < kMaxStage / 4; ++i)
+                *reinterpret_cast<uint2*>(to + 8u * (4u * i + (ln & 3u))) = sreg[i];
+        } else if constexpr (PART == 2) { // or an fp32 one for 128
+            for (uint32_t h = ln & 3u; h < 2u * cnt; h += 4u)
+                *reinterpret_cast<float*>(to + 4u * h) = static_cast<const float*>(
+                    p.scales)[scale_row(j) +
+                              divide(min(2u * (b0 + t0) + h, (p.in_features - 1u) / 128u), p.group_magic128)];
+        } else {
+            for (uint32_t i = ln & 3u; i < 8u * cnt; i += 4u)
+                to[i] = (char)static_cast<const uint8_t*>(
+                    p.scales)[scale_row(j) + divide(min(8u * (b0 + t0) + i, p.in_features / 32u - 1u), p.group_magic)];
+        }
+    };
+
+    while (true) {
+        // ---- the next rows of this expert, at most pass_rows
+        uint32_t n = 0;
+        while (next < p.rows && n < pass_rows) {
+            const uint32_t base = next & ~(uint32_t)(kWaveSize - 1), row = base + lane;
+            const bool hit = row >= next && row < p.rows && (!p.idx || (uint32_t)p.idx[row] == e);
+            const uint64_t mask = __builtin_amdgcn_ballot_w64(hit);
+            const uint32_t rank = n + (uint32_t)__builtin_popcountll(mask & below);
+            if (hit && rank < pass_rows)
+                s_list[wv][rank] = row;
+            const uint64_t left = __builtin_amdgcn_ballot_w64(hit && rank >= pass_rows);
+            next = left ? base + (uint32_t)__builtin_ctzll(left) : base + kWaveSize;
+            n = left ? pass_rows : n + (uint32_t)__builtin_popcountll(mask);
+        }
+        if (n == 0)
+            break; // the same for every wave of the workgroup
+        Tile cur = tile(0);
+        wave_exchange();
+
+        // steps staged at a time: all of a wave's share when they fit, else a multiple of kAhead
+        const uint32_t room = min(kMaxStage, (p.lds_x / (p.ks * n) - kRowPad) / kStepBytes) & ~(uint32_t)(kAhead - 1);
+        const uint32_t cs = min(room, (p.steps_wave + kAhead - 1) & ~(uint32_t)(kAhead - 1));
+        const uint32_t stride = cs * kStepBytes + kRowPad;
+        const uint32_t ntiles = (n + kTile - 1) / kTile;
+        uint32_t row[NT], x_off[NT];
+        float x_scale[NT];
+        v4f acc[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            // columns past the last row repeat it and are not stored
+            const uint32_t i = min(nt * kTile + r, n - 1u);
+            row[nt] = s_list[wv][i];
+            x_off[nt] = (ks * n + i) * stride + 64u * q;
+            x_scale[nt] = 1.0f;
+            if (XK == kXFp8F32 && p.x_groups == 1) // one scale a row
+                x_scale[nt] = static_cast<const float*>(p.x_scales)[row[nt] / p.x_div];
+        }
+
+        for (uint32_t j = 0; j < p.tiles; ++j) {
+            const uint32_t o0 = o_first + j * o_next;
+            const Tile nxt = tile(min(j + 1u, p.tiles - 1u));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                acc[nt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            for (uint32_t c0 = 0; c0 < p.steps_wave; c0 += cs) {
+                const uint32_t end = share > c0 ? min(cs, share - c0) : 0u; // the wave's steps of this part
+                if (j == 0 || cs < p.steps_wave) { // the x rows stay when they all fit
+                    __syncthreads(); // those before are done with
+                    const uint32_t cols = min(cs, p.steps_wave - c0) * kStep;
+                    const uint32_t pieces = cols / 8u; // of 8 columns, a row
+                    const uint32_t per_piece = magic(pieces);
+#pragma unroll 4
+                    for (uint32_t i = here(threadIdx.x); i < p.ks * n * pieces; i += kThreads) {
+                        const uint32_t pr = divide(i, per_piece), c = (i - pr * pieces) * 8u; // a wave's part of a row
+                        const uint32_t pk = pr / n, xr = s_list[wv][pr - pk * n] / p.x_div;
+                        const uint32_t col = (pk * p.steps_wave + c0) * kStep + c;
+                        const bool in = col < p.in_features;
+                        const size_t at = (size_t)xr * p.in_features + (in ? col : 0u);
+                        uint4 v;
+                        if constexpr (XK != kXBf16) {
+                            const uint2 x8 = *reinterpret_cast<const uint2*>(static_cast<const char*>(p.x) + at);
+                            uint32_t sc = 127u;
+                            if constexpr (XK == kXFp8E8) {
+                                const uint32_t g = divide((in ? col : 0u) / 32u, p.x_group_magic);
+                                sc = static_cast<const uint8_t*>(p.x_scales)[(size_t)xr * p.x_groups + g];
+                            }
+                            const float sx = as_float(sc << 23);
+                            v.x = fp8_to_bf16<false>(x8.x, sx);
+                            v.y = fp8_to_bf16<true>(x8.x, sx);
+                            v.z = fp8_to_bf16<false>(x8.y, sx);
+                            v.w = fp8_to_bf16<true>(x8.y, sx);
+                        } else {
+                            v = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.x) + 2u * at);
+                        }
+                        if (!in)
+                            v = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(s_x + pr * stride + 2u * c) = v;
+                    }
+                    if (x_part) {
+                        for (uint32_t i = here(threadIdx.x); i < p.ks * n * (cols / 128u); i += kThreads) {
+                            const uint32_t pr = i / (cols / 128u), h = i - pr * (cols / 128u);
+                            const uint32_t pk = pr / n, xr = s_list[wv][pr - pk * n] / p.x_div;
+                            const uint32_t first = (pk * p.steps_wave + c0) * (kStep / 128);
+                            s_sx[pr * 2u * cs + h] = static_cast<const float*>(
+                                p.x_scales)[(size_t)xr * p.x_groups +
+                                            divide(min(first + h, (p.in_features - 1u) / 128u), p.x_group_magic128)];
+                        }
+                    }
                 }
-                if constexpr (WS != 0)
-                    if (b < end)
-                        g.template steps<1>(b, ntiles);
+                if (j == 0 && c0 == 0) {
+                    // Past a wave's share, here and below, its last step again, unused: a condition around the loads
+                    // would leave the compiler unsure how many are in flight, and it would wait for all of them at
+                    // every step.
+                    for_slots<kAhead>([&](auto u) { fetch(u, cur, min((uint32_t)u.value, last_step)); });
+                    fetch_scales(0, 0);
+                }
+                put_scales(j, c0, end); // read by this wave alone
+                if (c0 + cs < p.steps_wave)
+                    fetch_scales(j, c0 + cs);
+                else
+                    fetch_scales(min(j + 1u, p.tiles - 1u), 0);
+                if (j == 0 || cs < p.steps_wave)
+                    __syncthreads();
+                else
+                    wave_exchange();
+
+                auto step = [&](auto slot, uint32_t t) { // step c0 + t, from slot u, whose next step is then fetched
+                    constexpr int u = decltype(slot)::value;
+                    // steps (and their halves) apart: interleaved, their operands would not fit 128 registers
+                    __builtin_amdgcn_sched_barrier(0);
+                    *w_put = w0[u];
+                    *w_put8 = w1[u];
+                    wave_exchange();
+                    const bool in = c0 + t + kAhead < share;
+                    const Tile from = {in ? cur.base : nxt.base, in ? cur.off : nxt.off, in ? cur.off8 : nxt.off8};
+                    fetch(slot, from, in ? c0 + t + kAhead : min((uint32_t)u, last_step));
+                    const uint2 sb2 = PART == 2 ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu)
+                                                : *reinterpret_cast<const uint2*>(s_ws + r * kScalePitch + 8u * t);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h)
+                            __builtin_amdgcn_sched_barrier(0);
+                        // only the exponent is looked at: 0 is 2^-127, 255 NaN
+                        const float s = as_float((((h ? sb2.y : sb2.x) >> (8u * q)) & 255u) << 23);
+                        const v4u wh = h ? *w_get4 : *w_get;
+                        const uint32_t w4[4] = {wh.x, wh.y, wh.z, wh.w};
+                        v8b A[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const v2b a0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w4[i], s, 0);
+                            const v2b a1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w4[i], s, 1);
+                            const v2b a2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w4[i], s, 2);
+                            const v2b a3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w4[i], s, 3);
+                            A[i] = v8b{a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (NT > 1 && (uint32_t)nt >= ntiles)
+                                break;
+                            v4f c = PART ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[nt];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const v8b B = *reinterpret_cast<const v8b*>(s_x + x_off[nt] + t * kStepBytes +
+                                                                            256u * h + 16u * i);
+                                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[i], B, c, 0, 0, 0);
+                            }
+                            if constexpr (PART) {
+                                const uint32_t pr = ks * n + min(nt * kTile + r, n - 1u);
+                                const float sx = x_part ? s_sx[(pr * cs + t) * 2u + h] : 1.0f;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    float f = sx;
+                                    if constexpr (PART == 2)
+                                        f *= *reinterpret_cast<const float*>(s_ws + (4u * q + i) * kScalePitch +
+                                                                             8u * t + 4u * h);
+                                    acc[nt][i] = __builtin_fmaf(c[i], f, acc[nt][i]);
+                                }
+                            } else {
+                                acc[nt] = c;
+                            }
+                        }
+                    }
+                };
+                uint32_t t = 0;
+                for (; t + kAhead <= end; t += kAhead)
+                    for_slots<kAhead>([&](auto u) { step(u, t + u.value); });
+                for_slots<kAhead>([&](auto u) {
+                    if (t + u.value < end)
+                        step(u, t + u.value);
+                });
             }
+
+            cur = nxt;
             // ---- the waves' sums over the columns meet, in their order
             if (p.ks > 1) {
-                __syncthreads();
+                __syncthreads(); // the sums before are done with
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    s_acc[wv][nt][lane] = g.acc[nt];
+                    s_acc[wv][nt][lane] = acc[nt];
                 __syncthreads();
                 if (ks != 0)
                     continue;
@@ -296,26 +446,22 @@ __global__ __launch_bounds__(kThreads) void gemv_fp4_kernel(GemvParams p)
                     for (uint32_t i = 1; i < p.ks; ++i) {
                         const v4f a = s_acc[wv + i][nt][lane];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            g.acc[nt][j] += a[j];
+                        for (int k = 0; k < 4; ++k)
+                            acc[nt][k] += a[k];
                     }
             }
-            // ---- scales of whole rows, and the results
+            // ---- the activations' scales of whole rows, and the results
+            const uint32_t ln = here(lane);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                if (nt * kTile + g.r >= n)
+                if (nt * kTile + (ln & 15u) >= n)
                     continue;
-                float sx = 1.0f;
-                if (FP8X && p.x_kind == kXFp8F32 && p.x_groups == 1)
-                    sx = *static_cast<const float*>(g.xs_row[nt]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t o = o0 + 4u * g.q + i;
+                    const uint32_t o = o0 + 4u * (ln >> 4) + i;
                     if (o >= p.out_features)
                         continue;
-                    float v = g.acc[nt][i] * sx;
-                    if (!p.scale_u8 && p.groups == 1)
-                        v *= static_cast<const float*>(p.scales)[g.tile_row + 4u * g.q + i];
+                    const float v = acc[nt][i] * x_scale[nt];
                     const size_t at = (size_t)row[nt] * p.out_features + o;
                     if (p.out_bf16)
                         static_cast<__bf16*>(p.out)[at] = (__bf16)v;
@@ -327,30 +473,24 @@ __global__ __launch_bounds__(kThreads) void gemv_fp4_kernel(GemvParams p)
     }
 }
 
-template <bool FP8X, bool PART, int NT>
-void launch_gemv(int ws, const GemvParams& p, dim3 grid, hipStream_t s)
+template <int XK, int PART, int NT>
+void launch_gemv(bool fast, const GemvParams& p, dim3 grid, hipStream_t s)
 {
-    if (ws == 0)
-        hipLaunchKernelGGL((gemv_fp4_kernel<FP8X, PART, NT, 0>), grid, dim3(kThreads), 0, s, p);
-    else if (ws == 1)
-        hipLaunchKernelGGL((gemv_fp4_kernel<FP8X, PART, NT, 1>), grid, dim3(kThreads), 0, s, p);
+    const uint32_t lds = p.lds_x + p.lds_x / kStepBytes * 8u;
+    if (PART != 2 && fast)
+        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, NT, PART != 2>), grid, dim3(kThreads), lds, s, p);
     else
-        hipLaunchKernelGGL((gemv_fp4_kernel<FP8X, PART, NT, 2>), grid, dim3(kThreads), 0, s, p);
+        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, NT, false>), grid, dim3(kThreads), lds, s, p);
 }
 
-template <bool FP8X, bool PART>
-void launch_gemv_nt(int nt, int ws, const GemvParams& p, dim3 grid, hipStream_t s)
+template <int XK, int PART>
+void launch_gemv_nt(int nt, bool fast, const GemvParams& p, dim3 grid, hipStream_t s)
 {
     if (nt == 1)
-        launch_gemv<FP8X, PART, 1>(ws, p, grid, s);
-    else if (nt == 2)
-        launch_gemv<FP8X, PART, 2>(ws, p, grid, s);
+        launch_gemv<XK, PART, 1>(fast, p, grid, s);
     else
-        launch_gemv<FP8X, PART, 4>(ws, p, grid, s);
+        launch_gemv<XK, PART, 2>(fast, p, grid, s);
 }
-
-// ceil(2^32 / d), by which divide() is exact for q * d < 2^32; 0 stands for d = 1.
-uint32_t magic(uint32_t d) { return d <= 1 ? 0u : (uint32_t)(((1ull << 32) + d - 1) / d); }
 
 // A group width's columns a scale; 0 when the kernels do not take it.
 int64_t group_columns(int64_t group, int64_t in, bool u8)
@@ -380,7 +520,7 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     if (tokens < 0 || k <= 0 || tokens >= (int64_t)INT_MAX || k >= (int64_t)INT_MAX || tokens * k >= (int64_t)INT_MAX ||
         (x_slots != 0 && x_slots != 1) || (!topk_idx && k != 1))
         return TK_ERR_INVALID_ARG;
-    if (experts <= 0 || experts > (1 << 20) || out_features <= 0 || out_features > (1 << 24) || in_features <= 0 ||
+    if (experts <= 0 || experts > 32768 || out_features <= 0 || out_features > (1 << 24) || in_features <= 0 ||
         in_features > (1 << 20) || in_features % 32 != 0)
         return TK_ERR_INVALID_ARG;
     if (group_size < 0 || (group_size != 0 && in_features % group_size != 0) ||
@@ -434,31 +574,46 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     hipStream_t s = static_cast<hipStream_t>(stream);
     p.group_magic = magic(p.group / 32u);
     p.x_group_magic = magic(p.x_group / 32u);
-    p.group_magic128 = magic(p.group / kBlock);
-    p.x_group_magic128 = magic(p.x_group / kBlock);
-    p.steps = (p.in_features + kBlock - 1) / kBlock;
+    p.group_magic128 = magic(p.group / 128u);
+    p.x_group_magic128 = magic(p.x_group / 128u);
+    p.steps = (p.in_features + kStep - 1) / kStep;
     // Columns are split over waves by the sizes alone, never by the number of
     // tokens, so that a row's sum has one order.
     const uint64_t waves = (uint64_t)p.k * ((p.out_features + kTile - 1) / kTile);
-    p.ks = waves >= 4096 ? 1u : waves >= 2048 ? 2u : 4u;
-    while (p.ks > 1 && p.steps < 2 * p.ks)
+    p.ks = waves >= 3072 ? 1u : waves >= 1536 ? 2u : 4u;
+    while (p.ks > p.steps)
         p.ks >>= 1;
     p.steps_wave = (p.steps + p.ks - 1) / p.ks;
-    p.steps_wave += p.steps_wave & 1u; // whole pairs
     p.by_row = topk_idx && rows <= experts;
-    p.grid_y = !topk_idx ? 1u : p.by_row ? p.rows : p.experts + 1u;
-    const bool part = (fp8 && !xu8 && p.x_groups > 1) || (!u8 && p.groups > 1);
-    const int ws = p.in_features % kBlock != 0                                      ? 2
-                   : u8 && group == 32 && in_features % 256 == 0 && aligned(scales, 8) ? 0
-                                                                                     : 1;
+    const int part = !u8 ? 2 : fp8 && !xu8 && p.x_groups > 1 ? 1 : 0;
+    const bool fast = u8 && group == 32 && in_features % kStep == 0 && aligned(scales, 8);
     // x tiles of a pass by the rows an expert has on average
     const uint64_t load = topk_idx ? (uint64_t)rows / (uint64_t)experts : (uint64_t)rows;
-    const int nt = tokens <= kTile || load <= 8 ? 1 : tokens <= 2 * kTile || load <= 24 ? 2 : 4;
+    const int nt = tokens <= kTile || load <= 8 ? 1 : 2;
+    // Staged x rows: room for kAhead steps of every row of a full pass when
+    // experts have that many, else of a few more than they have on average
+    // (a more crowded one takes further passes)
+    const uint32_t want = topk_idx ? (uint32_t)(2 * load + 4) : (uint32_t)rows;
+    const uint32_t most = (uint32_t)(kTile * nt);
+    const uint32_t row_bytes = p.ks * (kAhead * kStepBytes + kRowPad);
+    p.lds_x = row_bytes * (want < most ? want : most);
+    p.lds_x = p.lds_x < 16448u ? 16448u : p.lds_x > 66560u ? 66560u : p.lds_x;
+    // Several tiles a wave where that leaves four workgroups a CU: the x rows are then staged once for all of them
+    // and a tile's first weights are on their way during the one before (2048 -> 7168, 16 tokens top-8 of 64:
+    // 96.4 us with one tile, 95.2 with two, 94.0 with four, 99.8 with seven).
+    const uint64_t active = topk_idx ? (uint64_t)(rows < experts ? rows : experts) : 1u;
     const uint32_t tiles_wg = kThreads / kWaveSize / p.ks;
-    const dim3 grid((p.out_features + kTile * tiles_wg - 1) / (kTile * tiles_wg), p.grid_y < 65535u ? p.grid_y : 65535u);
-    if (fp8)
-        part ? launch_gemv_nt<true, true>(nt, ws, p, grid, s) : launch_gemv_nt<true, false>(nt, ws, p, grid, s);
+    const uint64_t wgs = active * ((p.out_features + kTile * tiles_wg - 1) / (kTile * tiles_wg));
+    p.tiles = wgs >= 4096 ? 4u : wgs >= 2048 ? 2u : 1u;
+    const uint32_t wg_rows = kTile * tiles_wg * p.tiles;
+    const dim3 grid((p.out_features + wg_rows - 1) / wg_rows, !topk_idx ? 1u : p.by_row ? p.rows : p.experts + 1u);
+    if (p.x_kind == kXBf16)
+        part == 2 ? launch_gemv_nt<kXBf16, 2>(nt, fast, p, grid, s) : launch_gemv_nt<kXBf16, 0>(nt, fast, p, grid, s);
+    else if (p.x_kind == kXFp8E8)
+        part == 2 ? launch_gemv_nt<kXFp8E8, 2>(nt, fast, p, grid, s) : launch_gemv_nt<kXFp8E8, 0>(nt, fast, p, grid, s);
     else
-        part ? launch_gemv_nt<false, true>(nt, ws, p, grid, s) : launch_gemv_nt<false, false>(nt, ws, p, grid, s);
+        part == 2   ? launch_gemv_nt<kXFp8F32, 2>(nt, fast, p, grid, s)
+        : part == 1 ? launch_gemv_nt<kXFp8F32, 1>(nt, fast, p, grid, s)
+                    : launch_gemv_nt<kXFp8F32, 0>(nt, fast, p, grid, s);
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }

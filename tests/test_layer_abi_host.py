@@ -141,7 +141,7 @@ def gemv(**kw):
 
 @pytest.mark.parametrize("kw", [
     dict(x_dtype=1), dict(x_dtype=3), dict(out_dtype=2), dict(scale_fmt=5), dict(scale_fmt=-1), dict(x_scale_fmt=9),
-    dict(tokens=-1), dict(k=0), dict(tokens=2 ** 28), dict(topk_idx=None), dict(experts=0), dict(experts=2 ** 20 + 1),
+    dict(tokens=-1), dict(k=0), dict(tokens=2 ** 28), dict(topk_idx=None), dict(experts=0), dict(experts=32769),
     dict(out_features=0), dict(out_features=2 ** 24 + 1), dict(in_features=0), dict(in_features=1040), dict(in_features=-32),
     dict(group_size=-32), dict(group_size=96), dict(x_group=-128), dict(x_group=384), dict(x=None), dict(x_scales=None),
     dict(codes=None), dict(scales=None), dict(out=None), dict(x=A + 8), dict(codes=D + 8), dict(topk_idx=C + 2),
