@@ -4,7 +4,16 @@
 //
 // Scores are computed in 64 bits and rounded once, so that the order of two
 // experts is that of their exact scores rounded to fp32 (plus the bias), and
-// does not hang on how an fp32 exponential was built.
+// does not hang on how an fp32 exponential was built.  gfx950 runs fp64
+// additions, products and FMAs at the rate of fp32's (4.8 cycles a wave against
+// 4.6, measured), so the 22 of a sigmoid cost about 3 us at 16384 tokens x 256
+// experts.
+//
+// route_row_kernel (k <= 16; no groups, or 2, 4, 8 or 16 groups of whole
+// lanes): four tokens per wave, one per 16-lane row, a lane holding
+// consecutive experts as lists of eight sorted scores; k rounds take the
+// largest list head of each row.  route_kernel takes what is left: one wave
+// per token, the largest key searched anew each round.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -13,8 +22,11 @@
 
 #include "tk.h"
 #include "tk_layer.h"
+#include "tk_select.h"
 
 namespace {
+
+using namespace tk_select;
 
 constexpr int kWave = 64;
 constexpr int kThreads = 256;
@@ -22,9 +34,6 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxK = 64;
 constexpr int64_t kMaxBlocks = 1 << 20; // a launch holds fewer than 2^32 work-items; tokens past the grid loop
-
-__device__ __forceinline__ uint32_t fbits(float f) { return __builtin_bit_cast(uint32_t, f); }
-__device__ __forceinline__ float ffrom(uint32_t u) { return __builtin_bit_cast(float, u); }
 
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* base, size_t i)
@@ -34,15 +43,6 @@ __device__ __forceinline__ float load_logit(const void* base, size_t i)
     else
         return static_cast<const float*>(base)[i];
 }
-
-// Order-preserving map of a (non-NaN) float to uint32; -0 and +0 map alike, and
-// 0 is below every value.
-__device__ __forceinline__ uint32_t ordered(float f)
-{
-    const uint32_t b = fbits(f + 0.0f);
-    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t h) { return ffrom((h & 0x80000000u) ? (h & 0x7FFFFFFFu) : ~h); }
 
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v)
 {
@@ -67,12 +67,49 @@ __device__ __forceinline__ T wave_sum(T v)
     return v;
 }
 
-__device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
+// e^x for a number x <= 0 to about 2^-49 (x below -1100 as -1100, which gives 0): 2^n
+// 2^f, n the nearest whole number to x log2(e), 2^f by the polynomial that
+// meets it at the 11 Chebyshev nodes of [-1/2, 1/2] (relative error 4.5e-16).
+__device__ __forceinline__ double exp64(double x)
+{
+    constexpr double kLog2e = 0x1.71547652b82fep+0;
+    x = __builtin_fmax(x, -1100.0);
+    const double n = __builtin_rint(x * kLog2e);
+    const double f = __builtin_fma(x, kLog2e, -n);
+    double r = 0x1.e60638d3aabfep-28;
+    r = __builtin_fma(r, f, 0x1.b675bc9694c29p-24);
+    r = __builtin_fma(r, f, 0x1.62bfd47c2b6d0p-20);
+    r = __builtin_fma(r, f, 0x1.ffcb5406453b3p-17);
+    r = __builtin_fma(r, f, 0x1.430913096ce36p-13);
+    r = __builtin_fma(r, f, 0x1.5d87fe9d7a4ffp-10);
+    r = __builtin_fma(r, f, 0x1.3b2ab6fba1df9p-7);
+    r = __builtin_fma(r, f, 0x1.c6b08d703ce49p-5);
+    r = __builtin_fma(r, f, 0x1.ebfbdff82c598p-3);
+    r = __builtin_fma(r, f, 0x1.62e42fefa3a19p-1);
+    r = __builtin_fma(r, f, 1.0);
+    return __builtin_ldexp(r, (int)n);
+}
+
+// 1/d for d in [1, 2]: the hardware's estimate and one Newton step
+__device__ __forceinline__ double reciprocal64(double d)
+{
+    const double r = __builtin_amdgcn_rcp(d);
+    return __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+}
+
+// 1 / (1 + e^-l) of a number l without overflow: with t = e^-|l|, 1 / (1 + t) or t / (1 + t)
+__device__ __forceinline__ double sigmoid64(float l)
+{
+    const double t = exp64(-(double)fabsf(l)), r = reciprocal64(1.0 + t);
+    return l >= 0.0f ? r : t * r;
+}
 
 struct RouteParams {
     const void* logits;
     const float* bias; // or null
     uint32_t tokens, experts, k, n_group, topk_group;
+    uint32_t lane_experts; // route_row_kernel: experts a lane holds
+    uint32_t gl_log2;      // ... and lanes a group, as a power of two
     int softmax, normalise;
     double scale;
     int32_t* idx;
@@ -106,11 +143,11 @@ __device__ __forceinline__ void route_token(const RouteParams& p, uint32_t t, ui
         double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < C; ++j)
-            sum += exp((double)l[j] - (double)top);
+            sum += exp64((double)l[j] - (double)top);
         sum = wave_sum(sum);
         inv_sum = sum > 0.0 ? 1.0 / sum : 0.0;
     }
-    auto score = [&](float x) { return p.softmax ? exp((double)x - (double)top) * inv_sum : sigmoid64(x); };
+    auto score = [&](float x) { return p.softmax ? exp64((double)x - (double)top) * inv_sum : sigmoid64(x); };
 
     uint32_t key[C];
     const bool by_score = p.bias || p.n_group > 1;
@@ -213,6 +250,277 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteParams p)
         route_token<BF16, C>(p, t, lane, s_key[wv], s_group[wv]);
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+    return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// sum / maximum over each 16-lane row, in every lane of it
+__device__ __forceinline__ double row_sum(double v)
+{
+    v = dpp_add<0xB1>(v);    // quad_perm [1,0,3,2]
+    v = dpp_add<0x4E>(v);    // quad_perm [2,3,0,1]
+    v = dpp_add<0x141>(v);   // row_half_mirror
+    return dpp_add<0x140>(v); // row_mirror
+}
+__device__ __forceinline__ uint32_t row_umax(uint32_t v)
+{
+    v = dpp_umax<0xB1>(v);
+    v = dpp_umax<0x4E>(v);
+    v = dpp_umax<0x141>(v);
+    return dpp_umax<0x140>(v);
+}
+
+// N consecutive logits as fp32.
+template <bool BF16, int N>
+__device__ __forceinline__ void load_logits(const void* base, size_t i, float* x)
+{
+    if constexpr (BF16) {
+        static_assert(N % 2 == 0, "whole words");
+        struct __attribute__((packed, aligned(2))) Words {
+            uint32_t w[N / 2];
+        };
+        const Words v = *reinterpret_cast<const Words*>(static_cast<const uint16_t*>(base) + i);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            x[2 * j] = ffrom(v.w[j] << 16);
+            x[2 * j + 1] = ffrom(v.w[j] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            x[j] = static_cast<const float*>(base)[i + j];
+    }
+}
+
+constexpr uint32_t kMasked = 0x007FFFFFu; // ordered(-inf): the key of a masked or absent expert
+
+// Four tokens per wave: lane q of row r holds experts q * C .. + C - 1 of token
+// t0 + r, C = FC (experts == 16 * FC) or p.lane_experts, in L lists of eight
+// (slots past the last expert hold -inf, as masked experts do).  The keys
+// order as the gating's do: score, then the smaller index.
+template <bool BF16, int L, int FC, bool K8>
+__global__ __launch_bounds__(kThreads, L <= 2 ? 4 : 2) void route_row_kernel(RouteParams p)
+{
+    constexpr int M = 8 * L;
+    constexpr bool FULL = FC > 0;
+    __shared__ uint2 s_pick[kWaves][kWave];                             // [row * 16 + round]: (expert, key)
+    __shared__ float s_in[FULL ? 1 : kWaves][FULL ? 1 : 4][FULL ? 1 : 16 * M]; // the rows, to be read in lane order
+    const uint32_t lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
+    const uint32_t q = lane & 15u, row = lane >> 4;
+    const uint32_t C = FULL ? (uint32_t)FC : p.lane_experts;
+    const bool by_score = p.bias || p.n_group > 1;
+    const uint32_t first = 4u * __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + wv);
+
+    for (uint32_t t0 = first; t0 < p.tokens; t0 += gridDim.x * (4u * kWaves)) {
+        // a wave past the last token repeats it in its other rows and stores nothing from them
+        const uint32_t t = t0 + row;
+        const size_t at = (size_t)min(t, p.tokens - 1u) * p.experts;
+        float x[M];
+        if constexpr (FULL) {
+            load_logits<BF16, FULL ? FC : 2>(p.logits, at + q * FC, x);
+#pragma unroll
+            for (int j = FC; j < M; ++j)
+                x[j] = -INFINITY;
+        } else {
+            for (uint32_t e = q; e < p.experts; e += 16u)
+                s_in[wv][row][e] = load_logit<BF16>(p.logits, at + e);
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+            for (int j = 0; j < M; ++j) {
+                const uint32_t e = q * C + j;
+                x[j] = (uint32_t)j < C && e < p.experts ? s_in[wv][row][min(e, 16u * M - 1u)] : -INFINITY;
+            }
+        }
+
+        // ---- keys: the logits, or the scores (and the bias) with the masked at -inf
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < M; j += 2)
+            bad |= __builtin_isunordered(x[j], x[j + 1]);
+        double top = 0.0, inv_sum = 1.0; // softmax: the row's largest logit, and one over the sum
+        if (p.softmax) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < M; ++j)
+                m = fmaxf(m, x[j]);
+            m = unordered(row_umax(ordered(m)));
+            bad |= m == INFINITY;
+            top = m == -INFINITY ? 0.0 : (double)m; // every expert masked: no inf - inf
+        }
+        auto shifted = [&](float l) { return exp64((double)l - top); };
+        if (by_score) {
+            if (p.softmax) {
+                double e[M], sum = 0.0;
+#pragma unroll
+                for (int j = 0; j < M; ++j) {
+                    e[j] = 0.0;
+                    if (FULL ? j < FC : (uint32_t)j < C) {
+                        e[j] = shifted(x[j]);
+                        sum += e[j];
+                    }
+                }
+                sum = row_sum(sum);
+                inv_sum = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+                for (int j = 0; j < M; ++j)
+                    if (FULL ? j < FC : (uint32_t)j < C)
+                        x[j] = x[j] > -INFINITY ? (float)(e[j] * inv_sum) : -INFINITY;
+            } else {
+#pragma unroll
+                for (int j = 0; j < M; ++j)
+                    if (FULL ? j < FC : (uint32_t)j < C)
+                        x[j] = x[j] > -INFINITY ? (float)sigmoid64(x[j]) : -INFINITY;
+            }
+            if (p.bias) {
+                float b[M];
+#pragma unroll
+                for (int j = 0; j < M; ++j)
+                    b[j] = (FULL ? j < FC : (uint32_t)j < C) ? p.bias[min(q * C + j, p.experts - 1u)] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < M; ++j)
+                    x[j] = x[j] > -INFINITY ? x[j] + b[j] : -INFINITY;
+#pragma unroll
+                for (int j = 0; j < M; j += 2)
+                    bad |= __builtin_isunordered(x[j], x[j + 1]);
+            }
+        } else if (p.softmax && !p.normalise) {
+            double sum = 0.0;
+#pragma unroll
+            for (int j = 0; j < M; ++j)
+                if (FULL ? j < FC : (uint32_t)j < C)
+                    sum += shifted(x[j]);
+            sum = row_sum(sum);
+            inv_sum = sum > 0.0 ? 1.0 / sum : 0.0;
+        }
+        const uint64_t bad_lanes = __builtin_amdgcn_ballot_w64(bad);
+        const bool poisoned = (uint32_t)(bad_lanes >> (lane & 48u)) & 0xFFFFu;
+        if (bad_lanes != 0) { // a poisoned row still has to sort
+#pragma unroll
+            for (int j = 0; j < M; ++j)
+                x[j] = x[j] == x[j] ? x[j] : -INFINITY;
+        }
+
+        // ---- groups: the lanes of those that are not among the best hold nothing any more
+        if (p.n_group > 1) {
+            const float pinf = opaque_inf(false);
+            float a1 = fmax2(x[0], x[1], pinf), a2 = fmin2(x[0], x[1], opaque_inf(true));
+#pragma unroll
+            for (int j = 2; j < M; ++j) {
+                a2 = __builtin_amdgcn_fmed3f(a1, a2, x[j]);
+                a1 = fmax2(a1, x[j], pinf);
+            }
+            if (p.gl_log2 >= 1)
+                merge_top2f<0xB1>(a1, a2, pinf); // quad_perm [1,0,3,2]
+            if (p.gl_log2 >= 2)
+                merge_top2f<0x4E>(a1, a2, pinf); // quad_perm [2,3,0,1]
+            if (p.gl_log2 >= 3)
+                merge_top2f<0x141>(a1, a2, pinf); // row_half_mirror
+            const float value = a1 + (a2 > -INFINITY ? a2 : 0.0f); // one expert left counts alone
+            const uint32_t gkey = ordered(value == value ? value : -INFINITY);
+            uint32_t rank = 0;
+            switch (p.gl_log2) {
+            case 0: row_group_rank<0>(gkey, gkey - 1u, rank); break;
+            case 1: row_group_rank<1>(gkey, gkey - 1u, rank); break;
+            case 2: row_group_rank<2>(gkey, gkey - 1u, rank); break;
+            default: row_group_rank<3>(gkey, gkey - 1u, rank); break;
+            }
+#pragma unroll
+            for (int j = 0; j < M; ++j)
+                x[j] = rank < p.topk_group ? x[j] : -INFINITY;
+        }
+
+        // ---- the lane's lists, best first, their slots 3 bits each with the head's lowest
+        uint32_t key[L][8], slots[L];
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            uint32_t id[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                key[l][j] = fbits(x[8 * l + j]);
+            sort_lane_raw8(key[l], id);
+            slots[l] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                slots[l] |= id[j] << (3 * j);
+            slots[l] ^= 0xFFFFFFu;
+        }
+
+        // ---- k rounds, four tokens at once; depth: the picks left, this one included
+        uint2* const pick_row = &s_pick[wv][row << 4];
+        auto round = [&](uint32_t it, uint32_t depth) {
+            uint32_t h = key[0][0];
+#pragma unroll
+            for (int l = 1; l < L; ++l)
+                h = max(h, key[l][0]);
+            const uint32_t m = row_umax(h);
+            const uint64_t hit = __builtin_amdgcn_ballot_w64(h == m);
+            // the lowest set bit of each row's 16 bits (every row has one)
+            const uint64_t win = hit & ~(hit - 0x0001000100010001ull);
+            const bool mine = __builtin_amdgcn_inverse_ballot_w64(win);
+            bool taken = false;
+            uint32_t pick = 0;
+            bool pop[L];
+#pragma unroll
+            for (int l = 0; l < L; ++l) { // the first list that holds it: its experts have the smaller indices
+                const bool here = !taken && key[l][0] == h;
+                pick = here ? q * C + 8 * l + (slots[l] & 7u) : pick;
+                taken = taken || here;
+                pop[l] = mine && here;
+            }
+#pragma unroll
+            for (int l = 0; l < L; ++l) {
+#pragma unroll
+                for (int j = 0; j + 1 < 8; ++j)
+                    if (j + 1u < depth)
+                        key[l][j] = pop[l] ? key[l][j + 1] : key[l][j];
+                if (depth > 8u)
+                    key[l][7] = pop[l] ? 0u : key[l][7];
+                slots[l] = pop[l] ? slots[l] >> 3 : slots[l];
+            }
+            if (mine)
+                pick_row[it] = make_uint2(pick, h);
+        };
+        if constexpr (K8) {
+#pragma unroll
+            for (uint32_t it = 0; it < 8; ++it)
+                round(it, 8u - it);
+        } else {
+            for (uint32_t it = 0; it < p.k; ++it)
+                round(it, 64u);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+
+        // ---- pick q of the row, its weight from its own logit again in 64 bits
+        const uint2 got = s_pick[wv][lane];
+        const bool out = q < p.k;
+        const bool present = out && got.y > kMasked && !poisoned;
+        double s = 0.0;
+        if (present) {
+            const float l = load_logit<BF16>(p.logits, at + got.x);
+            s = p.softmax ? shifted(l) * inv_sum : sigmoid64(l);
+        }
+        if (p.normalise) {
+            const double sum = row_sum(s);
+            if (sum != 0.0)
+                s /= sum;
+        }
+        if (out && t < p.tokens) {
+            p.idx[(size_t)t * p.k + q] = poisoned ? (int32_t)q : present ? (int32_t)got.x : -1;
+            p.weight[(size_t)t * p.k + q] = poisoned ? ffrom(0x7FC00000u) : (float)(s * p.scale);
+        }
+        __builtin_amdgcn_wave_barrier(); // s_pick and s_in are written again
+    }
+}
+
 struct RouteBwdParams {
     const float* dweight;
     const int32_t* idx;
@@ -281,9 +589,9 @@ __device__ __forceinline__ void route_backward_token(const RouteBwdParams& p, ui
         inv_sum = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
         s = live ? expf(l - top) * inv_sum : 0.0f;
     } else if (live) {
-        s64 = sigmoid64(l);
+        s64 = l == l ? sigmoid64(l) : (double)l;
         s = (float)s64;
-        slope = (float)(1.0 / (1.0 + exp((double)l)));
+        slope = (float)sigmoid64(-l);
     }
     float ds = live ? d : 0.0f;
     float grad;
@@ -334,6 +642,33 @@ bool overlaps(const void* a, size_t an, const void* b, size_t bn)
 }
 
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
+
+template <bool BF16, int L, int FC>
+void launch_route_k(const RouteParams& p, dim3 grid, hipStream_t s)
+{
+    if (p.k == 8)
+        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, true>), grid, dim3(kThreads), 0, s, p);
+    else
+        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, false>), grid, dim3(kThreads), 0, s, p);
+}
+
+// by the lists of eight a lane needs, the usual expert counts with their count compiled in
+template <bool BF16>
+void launch_route_row(const RouteParams& p, dim3 grid, hipStream_t s)
+{
+    switch (p.experts) {
+    case 64: return launch_route_k<BF16, 1, 4>(p, grid, s);
+    case 128: return launch_route_k<BF16, 1, 8>(p, grid, s);
+    case 256: return launch_route_k<BF16, 2, 16>(p, grid, s);
+    case 512: return launch_route_k<BF16, 4, 32>(p, grid, s);
+    }
+    switch ((p.lane_experts + 7) / 8) {
+    case 1: return launch_route_k<BF16, 1, 0>(p, grid, s);
+    case 2: return launch_route_k<BF16, 2, 0>(p, grid, s);
+    case 3: return launch_route_k<BF16, 3, 0>(p, grid, s);
+    default: return launch_route_k<BF16, 4, 0>(p, grid, s);
+    }
+}
 
 // what both directions check alike
 bool route_sizes_ok(int in_dtype, int64_t tokens, int64_t experts, int64_t k, int scoring, int normalise, float scale)
@@ -388,6 +723,19 @@ tk_status tk_route(const void* logits, tk_dtype in_dtype, const float* bias, int
     p.idx = topk_idx;
     p.weight = topk_weight;
     hipStream_t s = static_cast<hipStream_t>(stream);
+    // four tokens per wave; with groups, each of them has to be whole lanes
+    const bool lanes = experts % 16 == 0 && (n_group == 2 || n_group == 4 || n_group == 8 || n_group == 16);
+    if (k <= 16 && (n_group == 1 || lanes)) {
+        p.lane_experts = (uint32_t)((experts + 15) / 16);
+        p.gl_log2 = (uint32_t)__builtin_ctzll((unsigned long long)(16 / n_group));
+        const int64_t rblocks = (tokens + 4 * kWaves - 1) / (4 * kWaves);
+        const dim3 rgrid((uint32_t)(rblocks < kMaxBlocks ? rblocks : kMaxBlocks));
+        if (bf16)
+            launch_route_row<true>(p, rgrid, s);
+        else
+            launch_route_row<false>(p, rgrid, s);
+        return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
+    }
     const int64_t blocks = (tokens + kWaves - 1) / kWaves;
     const dim3 grid((uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks));
 #define TK_ROUTE(CC)                                                                        \
