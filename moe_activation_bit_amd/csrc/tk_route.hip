@@ -67,15 +67,15 @@ __device__ __forceinline__ T wave_sum(T v)
     return v;
 }
 
-// e^x for a number x <= 0 to about 2^-49 (x below -1100 as -1100, which gives 0): 2^n
-// 2^f, n the nearest whole number to x log2(e), 2^f by the polynomial that
-// meets it at the 11 Chebyshev nodes of [-1/2, 1/2] (relative error 4.5e-16).
+// e^x for a number x, |x| <= 1100, to about 2^-49: 2^n 2^f, n the nearest whole
+// number to x log2(e) (taken by adding and subtracting 1.5 * 2^52, whose low
+// word then holds n), 2^f by the polynomial that meets it at the 11 Chebyshev
+// nodes of [-1/2, 1/2] (relative error 4.5e-16).
 __device__ __forceinline__ double exp64(double x)
 {
-    constexpr double kLog2e = 0x1.71547652b82fep+0;
-    x = __builtin_fmax(x, -1100.0);
-    const double n = __builtin_rint(x * kLog2e);
-    const double f = __builtin_fma(x, kLog2e, -n);
+    constexpr double kLog2e = 0x1.71547652b82fep+0, kWhole = 0x1.8p+52;
+    const double tn = __builtin_fma(x, kLog2e, kWhole);
+    const double f = __builtin_fma(x, kLog2e, -(tn - kWhole));
     double r = 0x1.e60638d3aabfep-28;
     r = __builtin_fma(r, f, 0x1.b675bc9694c29p-24);
     r = __builtin_fma(r, f, 0x1.62bfd47c2b6d0p-20);
@@ -87,10 +87,12 @@ __device__ __forceinline__ double exp64(double x)
     r = __builtin_fma(r, f, 0x1.ebfbdff82c598p-3);
     r = __builtin_fma(r, f, 0x1.62e42fefa3a19p-1);
     r = __builtin_fma(r, f, 1.0);
-    return __builtin_ldexp(r, (int)n);
+    return __builtin_ldexp(r, (int)(uint32_t)__builtin_bit_cast(uint64_t, tn));
 }
+// ... for a number x <= 0 of any size: below -1100 it gives 0 as there
+__device__ __forceinline__ double exp64_neg(double x) { return exp64(__builtin_fmax(x, -1100.0)); }
 
-// 1/d for d in [1, 2]: the hardware's estimate and one Newton step
+// 1/d for a normal d whose reciprocal is normal: the hardware's estimate and one Newton step
 __device__ __forceinline__ double reciprocal64(double d)
 {
     const double r = __builtin_amdgcn_rcp(d);
@@ -100,8 +102,20 @@ __device__ __forceinline__ double reciprocal64(double d)
 // 1 / (1 + e^-l) of a number l without overflow: with t = e^-|l|, 1 / (1 + t) or t / (1 + t)
 __device__ __forceinline__ double sigmoid64(float l)
 {
-    const double t = exp64(-(double)fabsf(l)), r = reciprocal64(1.0 + t);
+    const double t = exp64_neg(-(double)fabsf(l)), r = reciprocal64(1.0 + t);
     return l >= 0.0f ? r : t * r;
+}
+
+// Two sigmoids rounded to fp32, with one reciprocal between them: 1/a = b/(ab).
+// Logits past +-340 count as that, whose scores round to 0 and 1 too (e^340
+// squared is still a double).
+__device__ __forceinline__ void sigmoid_pair(float& l0, float& l1)
+{
+    const double a = 1.0 + exp64(-(double)__builtin_amdgcn_fmed3f(l0, -340.0f, 340.0f));
+    const double b = 1.0 + exp64(-(double)__builtin_amdgcn_fmed3f(l1, -340.0f, 340.0f));
+    const double r = reciprocal64(a * b);
+    l0 = (float)(r * b);
+    l1 = (float)(r * a);
 }
 
 struct RouteParams {
@@ -143,11 +157,11 @@ __device__ __forceinline__ void route_token(const RouteParams& p, uint32_t t, ui
         double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < C; ++j)
-            sum += exp64((double)l[j] - (double)top);
+            sum += exp64_neg((double)l[j] - (double)top);
         sum = wave_sum(sum);
         inv_sum = sum > 0.0 ? 1.0 / sum : 0.0;
     }
-    auto score = [&](float x) { return p.softmax ? exp64((double)x - (double)top) * inv_sum : sigmoid64(x); };
+    auto score = [&](float x) { return p.softmax ? exp64_neg((double)x - (double)top) * inv_sum : sigmoid64(x); };
 
     uint32_t key[C];
     const bool by_score = p.bias || p.n_group > 1;
@@ -300,16 +314,28 @@ __device__ __forceinline__ void load_logits(const void* base, size_t i, float* x
 constexpr uint32_t kMasked = 0x007FFFFFu; // ordered(-inf): the key of a masked or absent expert
 
 // Four tokens per wave: lane q of row r holds experts q * C .. + C - 1 of token
-// t0 + r, C = FC (experts == 16 * FC) or p.lane_experts, in L lists of eight
+// t0 + r, C = FC (experts == 16 * FC) or p.lane_experts, in L lists of N
 // (slots past the last expert hold -inf, as masked experts do).  The keys
 // order as the gating's do: score, then the smaller index.
-template <bool BF16, int L, int FC, bool K8>
-__global__ __launch_bounds__(kThreads, L <= 2 ? 4 : 2) void route_row_kernel(RouteParams p)
+// MOVE (FC = 16, kept groups within 8 lanes): once the groups are ranked, each
+// kept lane's halves go to two lanes of the row, in order, so that every lane
+// sorts one list.
+// Bound by its fp64 and selection arithmetic: 926 vector instructions a wave at
+// 256 experts in 8 groups, top-8, some 7.4 us of the 10.4 us that 16384 tokens
+// take (1379 and 15.7 us before MOVE, the paired reciprocals and the masks
+// looked for at once).
+template <bool BF16, int L, int FC, bool K8, bool MOVE>
+__global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_kernel(RouteParams p)
 {
-    constexpr int M = 8 * L;
+    constexpr int N = FC == 4 ? 4 : 8;
+    constexpr int M = N * L;
+    constexpr int S = MOVE ? 1 : L; // lists to sort
     constexpr bool FULL = FC > 0;
+    static_assert(!MOVE || (FC == 16 && L == 2), "two halves of eight");
     __shared__ uint2 s_pick[kWaves][kWave];                             // [row * 16 + round]: (expert, key)
     __shared__ float s_in[FULL ? 1 : kWaves][FULL ? 1 : 4][FULL ? 1 : 16 * M]; // the rows, to be read in lane order
+    __shared__ uint4 s_move[MOVE ? kWaves : 1][2][MOVE ? kWave : 1];
+    __shared__ uint32_t s_src[MOVE ? kWaves : 1][MOVE ? kWave : 1];
     const uint32_t lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
     const uint32_t q = lane & 15u, row = lane >> 4;
     const uint32_t C = FULL ? (uint32_t)FC : p.lane_experts;
@@ -340,6 +366,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 ? 4 : 2) void route_row_kernel(Rou
         }
 
         // ---- keys: the logits, or the scores (and the bias) with the masked at -inf
+        auto held = [&](int j) { return FULL ? j < FC : (uint32_t)j < C; };
         bool bad = false;
 #pragma unroll
         for (int j = 0; j < M; j += 2)
@@ -354,14 +381,24 @@ __global__ __launch_bounds__(kThreads, L <= 2 ? 4 : 2) void route_row_kernel(Rou
             bad |= m == INFINITY;
             top = m == -INFINITY ? 0.0 : (double)m; // every expert masked: no inf - inf
         }
-        auto shifted = [&](float l) { return exp64((double)l - top); };
+        auto shifted = [&](float l) { return exp64_neg((double)l - top); };
         if (by_score) {
+            uint32_t masked = 0; // looked for at once: most waves have none
+            float least = x[0];
+#pragma unroll
+            for (int j = 1; j < M; ++j)
+                least = held(j) ? fminf(least, x[j]) : least;
+            if (__builtin_amdgcn_ballot_w64(least == -INFINITY) != 0) {
+#pragma unroll
+                for (int j = 0; j < M; ++j)
+                    masked |= x[j] == -INFINITY ? 1u << j : 0u;
+            }
             if (p.softmax) {
                 double e[M], sum = 0.0;
 #pragma unroll
                 for (int j = 0; j < M; ++j) {
                     e[j] = 0.0;
-                    if (FULL ? j < FC : (uint32_t)j < C) {
+                    if (held(j)) {
                         e[j] = shifted(x[j]);
                         sum += e[j];
                     }
@@ -370,31 +407,47 @@ __global__ __launch_bounds__(kThreads, L <= 2 ? 4 : 2) void route_row_kernel(Rou
                 inv_sum = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
                 for (int j = 0; j < M; ++j)
-                    if (FULL ? j < FC : (uint32_t)j < C)
-                        x[j] = x[j] > -INFINITY ? (float)(e[j] * inv_sum) : -INFINITY;
+                    x[j] = held(j) ? (float)(e[j] * inv_sum) : x[j];
             } else {
 #pragma unroll
-                for (int j = 0; j < M; ++j)
-                    if (FULL ? j < FC : (uint32_t)j < C)
-                        x[j] = x[j] > -INFINITY ? (float)sigmoid64(x[j]) : -INFINITY;
+                for (int j = 0; j < M; j += 2) {
+                    if (held(j)) {
+                        float s0 = x[j], s1 = x[j + 1];
+                        sigmoid_pair(s0, s1);
+                        x[j] = s0;
+                        x[j + 1] = held(j + 1) ? s1 : x[j + 1];
+                    }
+                }
             }
             if (p.bias) {
                 float b[M];
 #pragma unroll
                 for (int j = 0; j < M; ++j)
-                    b[j] = (FULL ? j < FC : (uint32_t)j < C) ? p.bias[min(q * C + j, p.experts - 1u)] : 0.0f;
+                    b[j] = held(j) ? p.bias[FULL ? q * FC + j : min(q * C + j, p.experts - 1u)] : 0.0f;
 #pragma unroll
                 for (int j = 0; j < M; ++j)
-                    x[j] = x[j] > -INFINITY ? x[j] + b[j] : -INFINITY;
+                    x[j] += b[j];
+            }
+            if (__builtin_amdgcn_ballot_w64(masked != 0) != 0) {
+#pragma unroll
+                for (int j = 0; j < M; ++j)
+                    x[j] = (masked >> j) & 1u ? -INFINITY : x[j];
+            }
+            if (p.bias) {
 #pragma unroll
                 for (int j = 0; j < M; j += 2)
                     bad |= __builtin_isunordered(x[j], x[j + 1]);
+            }
+            if constexpr (!FULL) { // the last lane's slots past the last expert
+#pragma unroll
+                for (int j = 0; j < M; ++j)
+                    x[j] = q * C + j < p.experts ? x[j] : -INFINITY;
             }
         } else if (p.softmax && !p.normalise) {
             double sum = 0.0;
 #pragma unroll
             for (int j = 0; j < M; ++j)
-                if (FULL ? j < FC : (uint32_t)j < C)
+                if (held(j))
                     sum += shifted(x[j]);
             sum = row_sum(sum);
             inv_sum = sum > 0.0 ? 1.0 / sum : 0.0;
@@ -408,6 +461,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 ? 4 : 2) void route_row_kernel(Rou
         }
 
         // ---- groups: the lanes of those that are not among the best hold nothing any more
+        uint32_t base0 = q * C; // the expert of the lane's first slot
         if (p.n_group > 1) {
             const float pinf = opaque_inf(false);
             float a1 = fmax2(x[0], x[1], pinf), a2 = fmin2(x[0], x[1], opaque_inf(true));
@@ -431,23 +485,55 @@ __global__ __launch_bounds__(kThreads, L <= 2 ? 4 : 2) void route_row_kernel(Rou
             case 2: row_group_rank<2>(gkey, gkey - 1u, rank); break;
             default: row_group_rank<3>(gkey, gkey - 1u, rank); break;
             }
+            const bool kept = rank < p.topk_group;
+            if constexpr (MOVE) {
+                // kept groups below this lane's own in its row, counted by their last lanes
+                const uint32_t gmask = (1u << p.gl_log2) - 1u;
+                const uint64_t last = __builtin_amdgcn_ballot_w64(kept && (q & gmask) == gmask);
+                const uint32_t mine = (uint32_t)(last >> (lane & 48u)) & ((1u << q) - 1u);
+                if (kept) {
+                    const uint32_t d = (row << 4) + 2u * (((uint32_t)__builtin_popcount(mine) << p.gl_log2) | (q & gmask));
 #pragma unroll
-            for (int j = 0; j < M; ++j)
-                x[j] = rank < p.topk_group ? x[j] : -INFINITY;
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int w = 0; w < 2; ++w)
+                            s_move[wv][w][d + h] = make_uint4(fbits(x[8 * h + 4 * w]), fbits(x[8 * h + 4 * w + 1]),
+                                                              fbits(x[8 * h + 4 * w + 2]), fbits(x[8 * h + 4 * w + 3]));
+                        s_src[wv][d + h] = q * C + 8 * h;
+                    }
+                }
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                const bool filled = q < 2u * (p.topk_group << p.gl_log2);
+                const uint4 v0 = s_move[wv][0][lane], v1 = s_move[wv][1][lane];
+                const uint32_t v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                base0 = s_src[wv][lane];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[j] = filled ? ffrom(v[j]) : -INFINITY;
+            } else {
+#pragma unroll
+                for (int j = 0; j < M; ++j)
+                    x[j] = kept ? x[j] : -INFINITY;
+            }
         }
 
         // ---- the lane's lists, best first, their slots 3 bits each with the head's lowest
-        uint32_t key[L][8], slots[L];
+        uint32_t key[S][N], slots[S];
 #pragma unroll
-        for (int l = 0; l < L; ++l) {
-            uint32_t id[8];
+        for (int l = 0; l < S; ++l) {
+            uint32_t id[N];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                key[l][j] = fbits(x[8 * l + j]);
-            sort_lane_raw8(key[l], id);
+            for (int j = 0; j < N; ++j)
+                key[l][j] = fbits(x[N * l + j]);
+            if constexpr (N == 4)
+                sort_lane_raw4(key[l], id);
+            else
+                sort_lane_raw8(key[l], id);
             slots[l] = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < N; ++j)
                 slots[l] |= id[j] << (3 * j);
             slots[l] ^= 0xFFFFFFu;
         }
@@ -457,31 +543,44 @@ __global__ __launch_bounds__(kThreads, L <= 2 ? 4 : 2) void route_row_kernel(Rou
         auto round = [&](uint32_t it, uint32_t depth) {
             uint32_t h = key[0][0];
 #pragma unroll
-            for (int l = 1; l < L; ++l)
+            for (int l = 1; l < S; ++l)
                 h = max(h, key[l][0]);
             const uint32_t m = row_umax(h);
             const uint64_t hit = __builtin_amdgcn_ballot_w64(h == m);
             // the lowest set bit of each row's 16 bits (every row has one)
             const uint64_t win = hit & ~(hit - 0x0001000100010001ull);
             const bool mine = __builtin_amdgcn_inverse_ballot_w64(win);
+            if constexpr (S == 1) {
+                if (mine) {
+                    pick_row[it] = make_uint2(base0 + (slots[0] & 7u), h);
+#pragma unroll
+                    for (int j = 0; j + 1 < N; ++j)
+                        if (j + 1u < depth)
+                            key[0][j] = key[0][j + 1];
+                    if (depth > (uint32_t)N)
+                        key[0][N - 1] = 0u;
+                    slots[0] >>= 3;
+                }
+                return;
+            }
             bool taken = false;
             uint32_t pick = 0;
-            bool pop[L];
+            bool pop[S];
 #pragma unroll
-            for (int l = 0; l < L; ++l) { // the first list that holds it: its experts have the smaller indices
+            for (int l = 0; l < S; ++l) { // the first list that holds it: its experts have the smaller indices
                 const bool here = !taken && key[l][0] == h;
-                pick = here ? q * C + 8 * l + (slots[l] & 7u) : pick;
+                pick = here ? base0 + N * l + (slots[l] & 7u) : pick;
                 taken = taken || here;
                 pop[l] = mine && here;
             }
 #pragma unroll
-            for (int l = 0; l < L; ++l) {
+            for (int l = 0; l < S; ++l) {
 #pragma unroll
-                for (int j = 0; j + 1 < 8; ++j)
+                for (int j = 0; j + 1 < N; ++j)
                     if (j + 1u < depth)
                         key[l][j] = pop[l] ? key[l][j + 1] : key[l][j];
-                if (depth > 8u)
-                    key[l][7] = pop[l] ? 0u : key[l][7];
+                if (depth > (uint32_t)N)
+                    key[l][N - 1] = pop[l] ? 0u : key[l][N - 1];
                 slots[l] = pop[l] ? slots[l] >> 3 : slots[l];
             }
             if (mine)
@@ -517,7 +616,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 ? 4 : 2) void route_row_kernel(Rou
             p.idx[(size_t)t * p.k + q] = poisoned ? (int32_t)q : present ? (int32_t)got.x : -1;
             p.weight[(size_t)t * p.k + q] = poisoned ? ffrom(0x7FC00000u) : (float)(s * p.scale);
         }
-        __builtin_amdgcn_wave_barrier(); // s_pick and s_in are written again
+        __builtin_amdgcn_wave_barrier(); // the LDS is written again
     }
 }
 
@@ -643,13 +742,13 @@ bool overlaps(const void* a, size_t an, const void* b, size_t bn)
 
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
-template <bool BF16, int L, int FC>
+template <bool BF16, int L, int FC, bool MOVE = false>
 void launch_route_k(const RouteParams& p, dim3 grid, hipStream_t s)
 {
     if (p.k == 8)
-        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, true>), grid, dim3(kThreads), 0, s, p);
+        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, true, MOVE>), grid, dim3(kThreads), 0, s, p);
     else
-        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, false>), grid, dim3(kThreads), 0, s, p);
+        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, false, MOVE>), grid, dim3(kThreads), 0, s, p);
 }
 
 // by the lists of eight a lane needs, the usual expert counts with their count compiled in
@@ -659,7 +758,13 @@ void launch_route_row(const RouteParams& p, dim3 grid, hipStream_t s)
     switch (p.experts) {
     case 64: return launch_route_k<BF16, 1, 4>(p, grid, s);
     case 128: return launch_route_k<BF16, 1, 8>(p, grid, s);
-    case 256: return launch_route_k<BF16, 2, 16>(p, grid, s);
+    case 256:
+        if (p.n_group > 1 && (p.topk_group << p.gl_log2) <= 8)
+            return launch_route_k<BF16, 2, 16, true>(p, grid, s);
+        return launch_route_k<BF16, 2, 16>(p, grid, s);
+    case 160: return launch_route_k<BF16, 2, 10>(p, grid, s);
+    case 192: return launch_route_k<BF16, 2, 12>(p, grid, s);
+    case 384: return launch_route_k<BF16, 3, 24>(p, grid, s);
     case 512: return launch_route_k<BF16, 4, 32>(p, grid, s);
     }
     switch ((p.lane_experts + 7) / 8) {

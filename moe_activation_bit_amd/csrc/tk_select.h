@@ -114,6 +114,33 @@ __device__ __forceinline__ void sort_lane_raw8(uint32_t (&key)[8], uint32_t (&id
     }
 }
 
+// The same for four scores: idx[j] = 7 - slot of entry j.
+__device__ __forceinline__ void sort_lane_raw4(uint32_t (&key)[4], uint32_t (&idx)[4])
+{
+    double x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t h = fbits(ffrom(key[j]) + 0.0f); // -0 + +0 = +0
+        const uint32_t l = (uint32_t)(7 - j) ^ ((uint32_t)((int32_t)h >> 31) & 7u);
+        x[j] = __builtin_bit_cast(double, ((uint64_t)h << 32) | l);
+    }
+    constexpr int net[5][2] = {{0, 2}, {1, 3}, {0, 1}, {2, 3}, {1, 2}};
+#pragma unroll
+    for (int c = 0; c < 5; ++c) {
+        const double a = x[net[c][0]], b = x[net[c][1]];
+        x[net[c][0]] = dmax(a, b);
+        x[net[c][1]] = dmin(a, b);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x[j]);
+        const uint32_t h = (uint32_t)(u >> 32);
+        const uint32_t s = (uint32_t)((int32_t)h >> 31);
+        key[j] = h ^ (s | 0x80000000u);
+        idx[j] = (uint32_t)u ^ (s & 7u);
+    }
+}
+
 // Group ranks within 16-lane rows (one token per row, 16 >> GL groups of
 // 2^GL lanes): group H's sum, as an order-preserving key, reaches every lane
 // of the row by row_newbcast from the group's first lane, and a lane counts
