@@ -39,26 +39,49 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// The lane slot's 8 columns as fp32.
+// The lane slot's 8 columns as they lie in memory, and as fp32.
+template <bool F32>
+struct Slot {
+    uint4 raw[F32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const void* base, size_t slot)
+    {
+        const uint4* p = static_cast<const uint4*>(base) + (F32 ? 2 : 1) * slot;
+        raw[0] = load16(p);
+        if constexpr (F32)
+            raw[F32 ? 1 : 0] = load16(p + 1);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        if constexpr (F32) {
+            const uint4 a = raw[0], b = raw[F32 ? 1 : 0];
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = as_float(w[j]);
+        } else {
+            const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = bf16_lo(w[j]);
+                v[2 * j + 1] = bf16_hi(w[j]);
+            }
+        }
+    }
+};
+__device__ __forceinline__ void load_weight(const float* weight, uint32_t slot, float (&w)[8])
+{
+    const float4* const p = reinterpret_cast<const float4*>(weight) + 2 * slot;
+    const float4 a = p[0], b = p[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
 template <bool F32>
 __device__ __forceinline__ void load_slot(const void* base, size_t slot, float (&v)[8])
 {
-    if constexpr (F32) {
-        const uint4* p = static_cast<const uint4*>(base) + 2 * slot;
-        const uint4 a = load16(p), b = load16(p + 1);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = as_float(w[j]);
-    } else {
-        const uint4 a = load16(static_cast<const uint4*>(base) + slot);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = bf16_lo(w[j]);
-            v[2 * j + 1] = bf16_hi(w[j]);
-        }
-    }
+    Slot<F32> s;
+    s.load(base, slot);
+    s.get(v);
 }
 
 // ... and the 8 columns written, rounded to the type.
@@ -175,10 +198,7 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_cast_kernel(NormParams p)
                 v[s][j] = 0.0f, w[s][j] = 0.0f;
             if (valid && slot < slots) {
                 load_slot<F32>(p.x, row_slot + slot, v[s]);
-                const float4* wp = reinterpret_cast<const float4*>(p.weight) + 2 * slot;
-                const float4 a = wp[0], b = wp[1];
-                w[s][0] = a.x, w[s][1] = a.y, w[s][2] = a.z, w[s][3] = a.w;
-                w[s][4] = b.x, w[s][5] = b.y, w[s][6] = b.z, w[s][7] = b.w;
+                load_weight(p.weight, slot, w[s]);
                 if (p.residual) {
                     float r[8];
                     load_slot<F32>(p.residual, row_slot + slot, r);
@@ -324,49 +344,81 @@ struct NormBwdParams {
     float inv_hidden;
 };
 
-// One row per pass of a workgroup, rows blockIdx.x, + gridDim.x, ...; the
-// weight and the rows' dy * a sums stay in registers.
-template <bool F32, int S, int MAXT>
+// One row per pass of a workgroup, rows blockIdx.x, + gridDim.x, ...; the rows'
+// dy * a sums stay in registers.  Rows of up to 16 steps (S = 1) keep the
+// weight there too and have the next row's dy, h and dresidual on their way
+// while the waves' parts of a row's dot meet; longer ones have no registers for
+// either.  Bound by the bytes of the rows.
+template <bool F32, int S, bool SKIP, int MAXT>
 __global__ __launch_bounds__(MAXT) void rmsnorm_backward_kernel(NormBwdParams p)
 {
+    constexpr bool AHEAD = S == 1;
     __shared__ float part_dot[2][16];
     const uint32_t lane = threadIdx.x & (kWaveSize - 1);
     const uint32_t wib = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
     const uint32_t waves = blockDim.x / kWaveSize;
-    float w[S][8], dw[S][8];
-    uint32_t slot[S];
-    bool in[S];
+    float w[AHEAD ? S : 1][8], dw[S][8];
+    uint32_t slot[S]; // lanes past the row's end read its last slot and add nothing to the dot
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         slot[s] = ((uint32_t)s * waves + wib) * kWaveSize + lane;
-        in[s] = slot[s] < p.slots;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            w[s][j] = in[s] ? p.weight[8 * slot[s] + j] : 0.0f, dw[s][j] = 0.0f;
+            dw[s][j] = 0.0f;
+        if constexpr (AHEAD)
+            load_weight(p.weight, min(slot[s], p.slots - 1u), w[s]);
     }
+    Slot<F32> dy[S], h[S], skip[SKIP ? S : 1];
+    float rstd = 0.0f;
+    auto fetch_skip = [&](uint32_t row) {
+        if constexpr (SKIP) {
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                skip[s].load(p.dresidual, (size_t)row * p.slots + min(slot[s], p.slots - 1u));
+        }
+    };
+    auto fetch = [&](uint32_t row) {
+        rstd = p.rstd[row];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const size_t at = (size_t)row * p.slots + min(slot[s], p.slots - 1u);
+            dy[s].load(p.dy, at);
+            h[s].load(p.h, at);
+        }
+        if constexpr (AHEAD)
+            fetch_skip(row);
+    };
+    if constexpr (AHEAD)
+        fetch(blockIdx.x); // the grid has at most a workgroup a row
     uint32_t parity = 0;
     for (uint32_t row = blockIdx.x; row < p.n; row += gridDim.x, parity ^= 1u) {
-        const size_t row_slot = (size_t)row * p.slots;
-        const float rstd = p.rstd[row];
-        float a[S][8], g[S][8];
+        if constexpr (!AHEAD)
+            fetch(row);
+        const float r = rstd;
+        float a[S][8], g[S][8], d[AHEAD && SKIP ? S : 1][8];
         float dot = 0.0f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                a[s][j] = 0.0f, g[s][j] = 0.0f;
-            if (in[s]) {
-                load_slot<F32>(p.dy, row_slot + slot[s], g[s]);
-                load_slot<F32>(p.h, row_slot + slot[s], a[s]);
-            }
+            dy[s].get(g[s]);
+            h[s].get(a[s]);
+            if constexpr (AHEAD && SKIP)
+                skip[s].get(d[s]);
+            if constexpr (!AHEAD)
+                load_weight(p.weight, min(slot[s], p.slots - 1u), w[0]);
+            float part = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                a[s][j] *= rstd;
+                a[s][j] *= r;
                 dw[s][j] += g[s][j] * a[s][j];
-                g[s][j] *= w[s][j];
-                dot += g[s][j] * a[s][j];
+                g[s][j] *= w[AHEAD ? s : 0][j];
+                part += g[s][j] * a[s][j];
             }
+            dot += slot[s] < p.slots ? part : 0.0f;
         }
+        if constexpr (AHEAD)
+            fetch(row + gridDim.x < p.n ? row + gridDim.x : row);
+        else
+            fetch_skip(row);
         dot = wave_sum(dot);
         if (waves > 1) {
             if (lane == 0)
@@ -379,26 +431,23 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_backward_kernel(NormBwdParams p)
         const float mean = dot * p.inv_hidden;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            if (in[s]) {
-                float d[8];
+            float e[8];
+            if constexpr (!AHEAD && SKIP)
+                skip[s].get(e);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    d[j] = rstd * (g[s][j] - a[s][j] * mean);
-                if (p.dresidual) {
-                    float r[8];
-                    load_slot<F32>(p.dresidual, row_slot + slot[s], r);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        d[j] += r[j];
-                }
-                store_slot<F32>(p.dx, row_slot + slot[s], d);
+            for (int j = 0; j < 8; ++j) {
+                g[s][j] = r * (g[s][j] - a[s][j] * mean);
+                if constexpr (SKIP)
+                    g[s][j] += AHEAD ? d[AHEAD ? s : 0][j] : e[j];
             }
+            if (slot[s] < p.slots)
+                store_slot<F32>(p.dx, (size_t)row * p.slots + slot[s], g[s]);
         }
     }
     if (p.partial) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            if (in[s]) {
+            if (slot[s] < p.slots) {
                 float4* o = reinterpret_cast<float4*>(p.partial + ((size_t)blockIdx.x * p.slots + slot[s]) * 8u);
                 o[0] = make_float4(dw[s][0], dw[s][1], dw[s][2], dw[s][3]);
                 o[1] = make_float4(dw[s][4], dw[s][5], dw[s][6], dw[s][7]);
@@ -408,18 +457,26 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_backward_kernel(NormBwdParams p)
 }
 
 // dweight[c] = the partial rows' sum: 16 waves of a workgroup share 64 columns,
-// wave w taking partial rows w, w + 16, ..., then their sums in wave order.
-// parts == 0 writes zeros.
+// wave w taking partial rows w, w + 16, ... (16 of them in flight), then their
+// sums in wave order.  parts == 0 writes zeros.
 __global__ __launch_bounds__(1024) void rmsnorm_dweight_kernel(const float* __restrict__ partial, uint32_t parts,
                                                               uint32_t hidden, float* __restrict__ dweight)
 {
+    constexpr uint32_t kBatch = 16;
     __shared__ float sums[16][kWaveSize];
     const uint32_t lane = threadIdx.x & (kWaveSize - 1), wv = threadIdx.x / kWaveSize;
     const uint32_t c = blockIdx.x * kWaveSize + lane;
+    const float* const at = partial + min(c, hidden - 1u);
     float s = 0.0f;
-    if (c < hidden)
-        for (uint32_t i = wv; i < parts; i += 16)
-            s += partial[(size_t)i * hidden + c];
+    for (uint32_t i = wv; i < parts; i += 16 * kBatch) {
+        float v[kBatch];
+#pragma unroll
+        for (uint32_t k = 0; k < kBatch; ++k)
+            v[k] = at[(size_t)min(i + 16 * k, parts - 1u) * hidden];
+#pragma unroll
+        for (uint32_t k = 0; k < kBatch; ++k)
+            s += i + 16 * k < parts ? v[k] : 0.0f;
+    }
     sums[wv][lane] = s;
     __syncthreads();
     if (wv == 0 && c < hidden) {
@@ -449,6 +506,15 @@ void launch_norm_gm(int gm, int sfmt, const NormParams& p, dim3 grid, dim3 block
         launch_norm<F32, S, MAXT, kGroupLanes>(sfmt, p, grid, block, 0, s);
     else
         launch_norm<F32, S, MAXT, kGroupLds>(sfmt, p, grid, block, lds, s);
+}
+
+template <bool F32, int S>
+void launch_norm_backward(bool skip, const NormBwdParams& p, dim3 grid, dim3 block, hipStream_t s)
+{
+    if (skip)
+        hipLaunchKernelGGL((rmsnorm_backward_kernel<F32, S, true, 1024>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((rmsnorm_backward_kernel<F32, S, false, 1024>), grid, block, 0, s, p);
 }
 
 // The steps a lane holds of a row of `steps` 512-column steps: `pref`, more
@@ -620,12 +686,10 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
         const uint32_t steps = (p.slots + kWaveSize - 1) / kWaveSize;
         const uint32_t S = steps_per_wave(steps, 1u);
         const dim3 grid(parts), block((steps + S - 1) / S * kWaveSize);
-#define TK_NORM_BWD(SS)                                                                                        \
-    case SS:                                                                                                   \
-        if (f32)                                                                                               \
-            hipLaunchKernelGGL((rmsnorm_backward_kernel<true, SS, 1024>), grid, block, 0, s, p);               \
-        else                                                                                                   \
-            hipLaunchKernelGGL((rmsnorm_backward_kernel<false, SS, 1024>), grid, block, 0, s, p);              \
+#define TK_NORM_BWD(SS)                                                      \
+    case SS:                                                                 \
+        f32 ? launch_norm_backward<true, SS>(dresidual != nullptr, p, grid, block, s)  \
+            : launch_norm_backward<false, SS>(dresidual != nullptr, p, grid, block, s); \
         break;
         switch (S) {
             TK_NORM_BWD(1)

@@ -19,6 +19,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "tk.h"
 #include "tk_layer.h"
@@ -732,6 +733,162 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteBwdParams
         route_backward_token<BF16>(p, t, lane, s_row[wv]);
 }
 
+// e of lane I of its 16-lane row, for I = 0 .. 14 while I < k - 1: whether an
+// earlier lane names the same expert
+template <int I = 0>
+__device__ __forceinline__ bool named_before(int32_t e, uint32_t q, uint32_t k)
+{
+    if constexpr (I < 15) {
+        if (I + 1u >= k)
+            return false;
+        const int32_t o = __builtin_amdgcn_mov_dpp(e, 0x150 + I, 0xF, 0xF, false); // row_newbcast
+        const bool mine = q > (uint32_t)I && o == e;
+        const bool later = named_before<I + 1>(e, q, k);
+        return mine || later;
+    } else {
+        return false;
+    }
+}
+
+__device__ __forceinline__ float row_sum(float v)
+{
+    auto add = [](float a, auto ctrl) {
+        return a + ffrom((uint32_t)__builtin_amdgcn_update_dpp(0, (int)fbits(a), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    v = add(v, std::integral_constant<int, 0xB1>{});
+    v = add(v, std::integral_constant<int, 0x4E>{});
+    v = add(v, std::integral_constant<int, 0x141>{});
+    return add(v, std::integral_constant<int, 0x140>{});
+}
+
+// Four tokens per wave, one per 16-lane row (k <= 16): lane q < k of a row holds
+// the token's slot q.  The four rows, consecutive in memory, are put together
+// in LDS and written as one run; VEC: 16 bytes a lane (the rows' bytes and
+// their addresses are multiples of 16).  DENSE: softmax over all experts, whose
+// logits pass through the same LDS.
+// Bound by the bytes written at large sizes.
+template <bool BF16, bool DENSE, bool VEC>
+__global__ __launch_bounds__(kThreads) void route_backward_row_kernel(RouteBwdParams p)
+{
+    constexpr uint32_t kPer = VEC ? (BF16 ? 8 : 4) : 1; // elements a lane moves at a time
+    extern __shared__ float4 s_rows4[];
+    const uint32_t lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
+    const uint32_t q = lane & 15u, row = lane >> 4;
+    float* const s_rows = reinterpret_cast<float*>(s_rows4) + (size_t)wv * 4u * p.experts;
+    const uint32_t first = 4u * __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + wv);
+    auto exchange = [] {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
+
+    for (uint32_t t0 = first; t0 < p.tokens; t0 += gridDim.x * (4u * kWaves)) {
+        const uint32_t t = min(t0 + row, p.tokens - 1u); // rows past the last token repeat it and are not written
+        const uint32_t count = min(4u, p.tokens - t0) * p.experts;
+        const size_t at = (size_t)t * p.experts, run = (size_t)t0 * p.experts;
+        int32_t e = -1;
+        float d = 0.0f;
+        if (q < p.k) {
+            e = p.idx[(size_t)t * p.k + q];
+            d = p.scale * p.dweight[(size_t)t * p.k + q];
+        }
+        const bool again = named_before(e, q, p.k);
+        const bool live = (uint32_t)e < p.experts && !again;
+        const float l = live ? load_logit<BF16>(p.logits, at + (uint32_t)e) : -INFINITY;
+        d = live ? d : 0.0f;
+
+        // the rows before the chosen experts' gradients: zeros, or the logits
+        if constexpr (DENSE) {
+            for (uint32_t i = lane * kPer; i < count; i += kWave * kPer) {
+                float x[kPer < 2 ? 2 : kPer];
+                if constexpr (VEC)
+                    load_logits<BF16, kPer < 2 ? 2 : kPer>(p.logits, run + i, x);
+                else
+                    x[0] = load_logit<BF16>(p.logits, run + i);
+#pragma unroll
+                for (uint32_t j = 0; j < kPer; ++j)
+                    s_rows[i + j] = x[j];
+            }
+        } else {
+            for (uint32_t i = lane * kPer; i < count; i += kWave * kPer) {
+#pragma unroll
+                for (uint32_t j = 0; j < kPer; ++j)
+                    s_rows[i + j] = 0.0f;
+            }
+        }
+        exchange();
+
+        float grad;
+        if (p.softmax) { // over the whole row, or, normalised, over the chosen experts alone
+            float* const mine = s_rows + (DENSE ? (t - t0) * p.experts : 0u);
+            float top = l;
+            if constexpr (DENSE)
+                for (uint32_t i = q; i < p.experts; i += 16u)
+                    top = fmaxf(top, mine[i]);
+            top = unordered(row_umax(ordered(top)));
+            if (top == -INFINITY)
+                top = 0.0f;
+            double sum = 0.0;
+            if constexpr (DENSE) {
+                for (uint32_t i = q; i < p.experts; i += 16u) {
+                    const float v = expf(mine[i] - top);
+                    sum += (double)v;
+                    if (t0 + row < p.tokens)
+                        mine[i] = v;
+                }
+            } else {
+                sum = live ? (double)expf(l - top) : 0.0;
+            }
+            const float total = (float)row_sum(sum);
+            const float inv_sum = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+            const float s = live ? expf(l - top) * inv_sum : 0.0f;
+            const float dot = row_sum(d * s);
+            grad = s * (d - dot);
+            if constexpr (DENSE) {
+                if (t0 + row < p.tokens)
+                    for (uint32_t i = q; i < p.experts; i += 16u)
+                        mine[i] = -(mine[i] * inv_sum) * dot;
+            }
+        } else {
+            // s and 1 - s from one exponential, in 64 bits: scores too small for 32 still share the weight
+            const double x = exp64_neg(-(double)fabsf(l)), one = reciprocal64(1.0 + x);
+            double s64 = live ? (l >= 0.0f ? one : x * one) : 0.0;
+            const float slope = (float)(l >= 0.0f ? x * one : one);
+            if (l != l)
+                s64 = (double)l;
+            float s = (float)s64, ds = d;
+            if (p.normalise) {
+                const double total = row_sum(s64);
+                if (total != 0.0) {
+                    s = (float)(s64 / total);
+                    ds = d - row_sum(d * s);
+                }
+            }
+            grad = ds * s * slope;
+        }
+        exchange();
+        if (live && t0 + row < p.tokens)
+            s_rows[row * p.experts + (uint32_t)e] = grad;
+        exchange();
+        for (uint32_t i = lane * kPer; i < count; i += kWave * kPer) {
+            if constexpr (!VEC) {
+                store_grad<BF16>(p.dlogits, run + i, s_rows[i]);
+            } else if constexpr (BF16) {
+                typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+                bf16x8 v;
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    v[j] = (__bf16)s_rows[i + j];
+                *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(p.dlogits) + run + i) = v;
+            } else {
+                *reinterpret_cast<float4*>(static_cast<float*>(p.dlogits) + run + i) =
+                    *reinterpret_cast<const float4*>(s_rows + i);
+            }
+        }
+        exchange(); // the LDS is written again
+    }
+}
+
 bool overlaps(const void* a, size_t an, const void* b, size_t bn)
 {
     if (!a || !b || an == 0 || bn == 0)
@@ -773,6 +930,20 @@ void launch_route_row(const RouteParams& p, dim3 grid, hipStream_t s)
     case 3: return launch_route_k<BF16, 3, 0>(p, grid, s);
     default: return launch_route_k<BF16, 4, 0>(p, grid, s);
     }
+}
+
+template <bool BF16>
+void launch_backward_row(bool dense, bool vec, const RouteBwdParams& p, dim3 grid, hipStream_t s)
+{
+    const size_t lds = (size_t)kWaves * 4u * p.experts * 4u; // 32 KiB at 512 experts
+    if (dense && vec)
+        hipLaunchKernelGGL((route_backward_row_kernel<BF16, true, true>), grid, dim3(kThreads), lds, s, p);
+    else if (dense)
+        hipLaunchKernelGGL((route_backward_row_kernel<BF16, true, false>), grid, dim3(kThreads), lds, s, p);
+    else if (vec)
+        hipLaunchKernelGGL((route_backward_row_kernel<BF16, false, true>), grid, dim3(kThreads), lds, s, p);
+    else
+        hipLaunchKernelGGL((route_backward_row_kernel<BF16, false, false>), grid, dim3(kThreads), lds, s, p);
 }
 
 // what both directions check alike
@@ -897,6 +1068,17 @@ tk_status tk_route_backward(const float* dweight, const int32_t* topk_idx, const
     p.scale = scale;
     p.dlogits = dlogits;
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (k <= 16) { // four tokens per wave
+        const size_t row_bytes = (size_t)experts * (bf16 ? 2u : 4u);
+        const bool vec = row_bytes % 16 == 0 && !misaligned(dlogits, 16);
+        const int64_t rblocks = (tokens + 4 * kWaves - 1) / (4 * kWaves);
+        const dim3 rgrid((uint32_t)(rblocks < kMaxBlocks ? rblocks : kMaxBlocks));
+        if (bf16)
+            launch_backward_row<true>(p.softmax && !p.normalise, vec, p, rgrid, s);
+        else
+            launch_backward_row<false>(p.softmax && !p.normalise, vec, p, rgrid, s);
+        return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
+    }
     const int64_t blocks = (tokens + kWaves - 1) / kWaves;
     const dim3 grid((uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks));
     if (bf16)
