@@ -179,8 +179,9 @@ tk_status tk_route_backward(const float* dweight, const int32_t* topk_idx, const
  * with 4-bit weights: W[e][o][c] = codes * scale, as tk_cast_fp4 writes them
  * from bf16 or fp32 rows [experts*out_features, in_features] with a row-major
  * scale_fmt.  Products and sums in fp32 (each weight and activation enters
- * exactly), rounded once to out_dtype.  Each chosen expert's weights are read
- * once for up to 16 of its rows.
+ * exactly), rounded once to out_dtype.  A chosen expert's weights are read once
+ * for its rows together, up to 16 at a time: made for a step of decoding, a few
+ * rows an expert.
  *
  *  x            [tokens, in_features], or [tokens*k, in_features] when x_slots;
  *               TK_DTYPE_BF16 elements, or TK_DTYPE_FP8 codes with x_scales.

@@ -24,18 +24,17 @@ struct GemvParams {
     const void* scales;
     void* out;
     uint32_t rows;       // tokens * k
-    uint32_t k;
     uint32_t x_div;      // out row r reads x row r / x_div
     uint32_t experts;
     uint32_t out_features;
     uint32_t in_features;
-    uint32_t group, groups;     // weights: columns a scale, scales a row
-    uint32_t x_group, x_groups;
-    int x_kind, scale_u8, out_bf16;
+    uint32_t groups, x_groups; // scales a row
+    int out_bf16;
     uint32_t group_magic, x_group_magic;       // of the groups' width in blocks of 32 columns
     uint32_t group_magic128, x_group_magic128; // ... in steps of 128
     uint32_t steps;      // of kStep columns, the last part-filled when in_features is no multiple
     uint32_t steps_wave; // a wave's share of them
+    uint32_t steps_part; // ... summed in parts of so many, whose sums are then added in order
     uint32_t ks;         // waves that share a tile's columns: 1, 2 or 4
     uint32_t tiles;      // tiles of 16 weight rows a wave goes through
     uint32_t lds_x;      // bytes for staged rows
@@ -91,10 +90,14 @@ constexpr int kAhead = 2;            // steps of weights in flight
 constexpr uint32_t kMaxStage = 16;   // steps staged at a time at most
 constexpr uint32_t kStepBytes = 512; // a staged x row's bytes a step
 constexpr uint32_t kRowPad = 16;     // between staged x rows, which would else share their LDS banks
+constexpr uint32_t kCus = 256, kCuLds = 160 * 1024;
 constexpr uint32_t kScalePitch = 8 * kMaxStage + 8; // bytes of a weight row's staged scales
 
-// Matrix instructions on 16 weight rows at a time, for up to 16 * NT of the
-// rows that chose the expert.  Codes and FP8 activations become bf16 in
+// LDS of a workgroup beside the staged x rows: the row lists, a step of weights and the scales of each wave
+constexpr uint32_t kOwnLds = kThreads / kWaveSize * (kTile * 8 + kTile * 128 + kTile * kScalePitch);
+
+// Matrix instructions on 16 weight rows at a time, for up to 16 of the rows that
+// chose the expert.  Codes and FP8 activations become bf16 in
 // registers, with their UE8M0 scales on the way: both are exact (two and four
 // significant bits), and the products and sums of the 16x16x32 bf16
 // instructions are those of fp32.  (The E2M1 x E4M3 instruction would take the
@@ -102,8 +105,12 @@ constexpr uint32_t kScalePitch = 8 * kMaxStage + 8; // bytes of a weight row's s
 // step: random E4M3 bytes gave sums off by up to 7.7e-5 of their terms'
 // magnitude, where the bf16 instructions were exact.)
 //
-// What bounds it is the weights' bytes, so everything else keeps out of their
-// way.  A wave reads a step's 16 x 128 bytes with two instructions of eight
+// What bounds it is the weights' bytes (7168 -> 4096, top-8 of 8 experts for one
+// token: 26.9 us, 4.7 TB/s; 2048 -> 7168 for 16 tokens' top-8 of 64: 93.5 us, 4.7
+// TB/s; one row of a single expert, 7168 -> 4096: 8 us, a launch and the row's
+// staging), so everything else keeps out of their way.  For many rows of one
+// expert it is the staging of the rows, once for every pass and workgroup (64
+// rows of 7168 -> 4096: 54 us; 32 rows a pass instead of 16: 52).  A wave reads a step's 16 x 128 bytes with two instructions of eight
 // whole lines (lane l: row l / 8, 16 bytes l % 8), kAhead steps before their
 // use, and passes them through 2 KiB of LDS of its own into the instruction's
 // layout, lane (r, q) = (l & 15, l >> 4): weight row r, columns 32q.. of each
@@ -117,14 +124,13 @@ constexpr uint32_t kScalePitch = 8 * kMaxStage + 8; // bytes of a weight row's s
 // activations' alone; 2: the weights' too).
 // A result's column n (x row) is lane & 15, its rows 4q .. 4q + 3.
 //   FAST: UE8M0 weight scales of 32 columns and whole steps; else any.
-template <int XK, int PART, int NT, bool FAST>
-__global__ __launch_bounds__(kThreads, PART == 2 || NT == 2 ? 3 : 4) void gemv_fp4_kernel(GemvParams p)
+template <int XK, int PART, bool FAST>
+__global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(GemvParams p)
 {
-    constexpr uint32_t kWaves = kThreads / kWaveSize, kRows = kTile * NT;
-    __shared__ uint32_t s_list[kWaves][kRows];
+    constexpr uint32_t kWaves = kThreads / kWaveSize;
+    __shared__ uint2 s_list[kWaves][kTile]; // an output row and its x row
     __shared__ v4u s_w4[kWaves][kTile * 8];
     __shared__ uint2 s_ws2[kWaves][kTile * kScalePitch / 8];
-    __shared__ v4f s_acc[kWaves][NT][kWaveSize];
     extern __shared__ uint4 s_x4[]; // the staged rows, then their fp32 scales
     char* const s_x = reinterpret_cast<char*>(s_x4);
     float* const s_sx = reinterpret_cast<float*>(s_x + p.lds_x);
@@ -142,7 +148,7 @@ __global__ __launch_bounds__(kThreads, PART == 2 || NT == 2 ? 3 : 4) void gemv_f
     const uint64_t below = (1ull << lane) - 1u;
     const bool x_part = PART != 0 && XK == kXFp8F32 && p.x_groups > 1;
     // x rows of a pass: what leaves room for kAhead steps of each
-    const uint32_t pass_rows = min(kRows, p.lds_x / (p.ks * (kAhead * kStepBytes + kRowPad)));
+    const uint32_t pass_rows = min((uint32_t)kTile, p.lds_x / (p.ks * (kAhead * kStepBytes + kRowPad)));
     // LDS slots of this lane's weights: row r keeps columns 32p.. in slot p ^ (r / 2), so that neither the
     // writes nor the reads of 16 rows meet in a bank
     const uint32_t lrow = lane >> 3, lpiece = lane & 7u;
@@ -173,19 +179,24 @@ __global__ __launch_bounds__(kThreads, PART == 2 || NT == 2 ? 3 : 4) void gemv_f
             e = y;
         }
     }
+    auto zero_row = [&](uint32_t row) {
+        for (uint32_t i = threadIdx.x; i < p.tiles * o_next; i += kThreads) {
+            const uint32_t o = blockIdx.x * p.tiles * o_next + i;
+            if (o >= p.out_features)
+                break;
+            if (p.out_bf16)
+                static_cast<uint16_t*>(p.out)[(size_t)row * p.out_features + o] = 0;
+            else
+                static_cast<float*>(p.out)[(size_t)row * p.out_features + o] = 0.0f;
+        }
+    };
     if (e >= p.experts) { // absent rows: this one, or all of them
-        for (uint32_t row = p.by_row ? y : 0u; row < (p.by_row ? y + 1u : p.rows); ++row) {
-            if ((uint32_t)p.idx[row] < p.experts)
-                continue;
-            for (uint32_t i = threadIdx.x; i < p.tiles * o_next; i += kThreads) {
-                const uint32_t o = blockIdx.x * p.tiles * o_next + i;
-                if (o >= p.out_features)
-                    break;
-                if (p.out_bf16)
-                    static_cast<uint16_t*>(p.out)[(size_t)row * p.out_features + o] = 0;
-                else
-                    static_cast<float*>(p.out)[(size_t)row * p.out_features + o] = 0.0f;
-            }
+        for (uint32_t base = p.by_row ? y & ~(uint32_t)(kWaveSize - 1) : 0u; base < (p.by_row ? y + 1u : p.rows);
+             base += kWaveSize) {
+            const uint32_t mine = base + lane;
+            const bool hit = p.by_row ? mine == y : mine < p.rows && (uint32_t)p.idx[mine] >= p.experts;
+            for (uint64_t mask = __builtin_amdgcn_ballot_w64(hit); mask; mask &= mask - 1u)
+                zero_row(base + (uint32_t)__builtin_ctzll(mask));
         }
         return;
     }
@@ -268,7 +279,7 @@ __global__ __launch_bounds__(kThreads, PART == 2 || NT == 2 ? 3 : 4) void gemv_f
             const uint64_t mask = __builtin_amdgcn_ballot_w64(hit);
             const uint32_t rank = n + (uint32_t)__builtin_popcountll(mask & below);
             if (hit && rank < pass_rows)
-                s_list[wv][rank] = row;
+                s_list[wv][rank] = make_uint2(row, row / p.x_div);
             const uint64_t left = __builtin_amdgcn_ballot_w64(hit && rank >= pass_rows);
             next = left ? base + (uint32_t)__builtin_ctzll(left) : base + kWaveSize;
             n = left ? pass_rows : n + (uint32_t)__builtin_popcountll(mask);
@@ -282,65 +293,69 @@ __global__ __launch_bounds__(kThreads, PART == 2 || NT == 2 ? 3 : 4) void gemv_f
         const uint32_t room = min(kMaxStage, (p.lds_x / (p.ks * n) - kRowPad) / kStepBytes) & ~(uint32_t)(kAhead - 1);
         const uint32_t cs = min(room, (p.steps_wave + kAhead - 1) & ~(uint32_t)(kAhead - 1));
         const uint32_t stride = cs * kStepBytes + kRowPad;
-        const uint32_t ntiles = (n + kTile - 1) / kTile;
-        uint32_t row[NT], x_off[NT];
-        float x_scale[NT];
-        v4f acc[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            // columns past the last row repeat it and are not stored
-            const uint32_t i = min(nt * kTile + r, n - 1u);
-            row[nt] = s_list[wv][i];
-            x_off[nt] = (ks * n + i) * stride + 64u * q;
-            x_scale[nt] = 1.0f;
-            if (XK == kXFp8F32 && p.x_groups == 1) // one scale a row
-                x_scale[nt] = static_cast<const float*>(p.x_scales)[row[nt] / p.x_div];
-        }
+        // result columns past the last row repeat it and are not stored
+        const uint32_t pr = ks * n + min(r, n - 1u), x_off = pr * stride + 64u * q;
+        const uint2 mine = s_list[wv][min(r, n - 1u)];
+        float x_scale = 1.0f;
+        if (XK == kXFp8F32 && p.x_groups == 1) // one scale a row
+            x_scale = static_cast<const float*>(p.x_scales)[mine.y];
 
         for (uint32_t j = 0; j < p.tiles; ++j) {
             const uint32_t o0 = o_first + j * o_next;
             const Tile nxt = tile(min(j + 1u, p.tiles - 1u));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                acc[nt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            v4f acc = {0.0f, 0.0f, 0.0f, 0.0f}, total = acc; // of the part, and of the parts before it
+            uint32_t part_end = p.steps_part;
             for (uint32_t c0 = 0; c0 < p.steps_wave; c0 += cs) {
                 const uint32_t end = share > c0 ? min(cs, share - c0) : 0u; // the wave's steps of this part
                 if (j == 0 || cs < p.steps_wave) { // the x rows stay when they all fit
                     __syncthreads(); // those before are done with
                     const uint32_t cols = min(cs, p.steps_wave - c0) * kStep;
                     const uint32_t pieces = cols / 8u; // of 8 columns, a row
-                    const uint32_t per_piece = magic(pieces);
-#pragma unroll 4
-                    for (uint32_t i = here(threadIdx.x); i < p.ks * n * pieces; i += kThreads) {
-                        const uint32_t pr = divide(i, per_piece), c = (i - pr * pieces) * 8u; // a wave's part of a row
-                        const uint32_t pk = pr / n, xr = s_list[wv][pr - pk * n] / p.x_div;
-                        const uint32_t col = (pk * p.steps_wave + c0) * kStep + c;
-                        const bool in = col < p.in_features;
-                        const size_t at = (size_t)xr * p.in_features + (in ? col : 0u);
-                        uint4 v;
-                        if constexpr (XK != kXBf16) {
-                            const uint2 x8 = *reinterpret_cast<const uint2*>(static_cast<const char*>(p.x) + at);
-                            uint32_t sc = 127u;
-                            if constexpr (XK == kXFp8E8) {
-                                const uint32_t g = divide((in ? col : 0u) / 32u, p.x_group_magic);
-                                sc = static_cast<const uint8_t*>(p.x_scales)[(size_t)xr * p.x_groups + g];
+                    const uint32_t per_piece = magic(pieces), per_n = magic(n);
+                    // Pieces in flight a thread: one at a time, 64 tokens of one 7168 -> 4096 product took 93 us
+                    // instead of 49, and of a top-8 of 64 experts 143 instead of 134 (147 with eight, of FP8).
+                    constexpr int kBatch = XK == kXBf16 ? 8 : 4;
+                    const uint32_t all = p.ks * n * pieces;
+                    for (uint32_t i0 = here(threadIdx.x); i0 < all; i0 += kBatch * kThreads) {
+                        uint4 v[kBatch]; // FP8: the codes' two words, then their scale's byte
+                        uint32_t to[kBatch];
+#pragma unroll
+                        for (int m = 0; m < kBatch; ++m) { // every load first (past the end the last piece again)
+                            const uint32_t i = min(i0 + m * kThreads, all - 1u);
+                            const uint32_t pr = divide(i, per_piece), c = (i - pr * pieces) * 8u; // a wave's part of a row
+                            const uint32_t pk = divide(pr, per_n), xr = s_list[wv][pr - pk * n].y;
+                            const uint32_t col = (pk * p.steps_wave + c0) * kStep + c;
+                            const bool in = col < p.in_features;
+                            const size_t at = (size_t)xr * p.in_features + (in ? col : 0u);
+                            to[m] = (pr * stride + 2u * c) | (in ? 1u : 0u);
+                            if constexpr (XK != kXBf16) {
+                                const uint2 x8 = *reinterpret_cast<const uint2*>(static_cast<const char*>(p.x) + at);
+                                v[m] = make_uint4(x8.x, x8.y, 127u, 0u);
+                                if constexpr (XK == kXFp8E8) {
+                                    const uint32_t g = divide((in ? col : 0u) / 32u, p.x_group_magic);
+                                    v[m].z = static_cast<const uint8_t*>(p.x_scales)[(size_t)xr * p.x_groups + g];
+                                }
+                            } else {
+                                v[m] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.x) + 2u * at);
                             }
-                            const float sx = as_float(sc << 23);
-                            v.x = fp8_to_bf16<false>(x8.x, sx);
-                            v.y = fp8_to_bf16<true>(x8.x, sx);
-                            v.z = fp8_to_bf16<false>(x8.y, sx);
-                            v.w = fp8_to_bf16<true>(x8.y, sx);
-                        } else {
-                            v = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.x) + 2u * at);
                         }
-                        if (!in)
-                            v = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(s_x + pr * stride + 2u * c) = v;
+#pragma unroll
+                        for (int m = 0; m < kBatch; ++m) {
+                            if constexpr (XK != kXBf16) {
+                                const float sx = as_float(v[m].z << 23);
+                                v[m] = make_uint4(fp8_to_bf16<false>(v[m].x, sx), fp8_to_bf16<true>(v[m].x, sx),
+                                                  fp8_to_bf16<false>(v[m].y, sx), fp8_to_bf16<true>(v[m].y, sx));
+                            }
+                            if (!(to[m] & 1u))
+                                v[m] = make_uint4(0, 0, 0, 0);
+                            if (i0 + m * kThreads < all)
+                                *reinterpret_cast<uint4*>(s_x + (to[m] & ~1u)) = v[m];
+                        }
                     }
                     if (x_part) {
                         for (uint32_t i = here(threadIdx.x); i < p.ks * n * (cols / 128u); i += kThreads) {
                             const uint32_t pr = i / (cols / 128u), h = i - pr * (cols / 128u);
-                            const uint32_t pk = pr / n, xr = s_list[wv][pr - pk * n] / p.x_div;
+                            const uint32_t pk = divide(pr, per_n), xr = s_list[wv][pr - pk * n].y;
                             const uint32_t first = (pk * p.steps_wave + c0) * (kStep / 128);
                             s_sx[pr * 2u * cs + h] = static_cast<const float*>(
                                 p.x_scales)[(size_t)xr * p.x_groups +
@@ -367,6 +382,11 @@ __global__ __launch_bounds__(kThreads, PART == 2 || NT == 2 ? 3 : 4) void gemv_f
 
                 auto step = [&](auto slot, uint32_t t) { // step c0 + t, from slot u, whose next step is then fetched
                     constexpr int u = decltype(slot)::value;
+                    if (c0 + t == part_end) { // wave-uniform
+                        part_end += p.steps_part;
+                        total += acc;
+                        acc = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
                     // steps (and their halves) apart: interleaved, their operands would not fit 128 registers
                     __builtin_amdgcn_sched_barrier(0);
                     *w_put = w0[u];
@@ -394,31 +414,25 @@ __global__ __launch_bounds__(kThreads, PART == 2 || NT == 2 ? 3 : 4) void gemv_f
                             const v2b a3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w4[i], s, 3);
                             A[i] = v8b{a0[0], a0[1], a1[0], a1[1], a2[0], a2[1], a3[0], a3[1]};
                         }
+                        v4f c = PART ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if (NT > 1 && (uint32_t)nt >= ntiles)
-                                break;
-                            v4f c = PART ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[nt];
+                        for (int i = 0; i < 4; ++i) {
+                            const v8b B = *reinterpret_cast<const v8b*>(s_x + x_off + t * kStepBytes + 256u * h +
+                                                                        16u * i);
+                            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[i], B, c, 0, 0, 0);
+                        }
+                        if constexpr (PART) {
+                            const float sx = x_part ? s_sx[(pr * cs + t) * 2u + h] : 1.0f;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const v8b B = *reinterpret_cast<const v8b*>(s_x + x_off[nt] + t * kStepBytes +
-                                                                            256u * h + 16u * i);
-                                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[i], B, c, 0, 0, 0);
+                                float f = sx;
+                                if constexpr (PART == 2)
+                                    f *= *reinterpret_cast<const float*>(s_ws + (4u * q + i) * kScalePitch + 8u * t +
+                                                                         4u * h);
+                                acc[i] = __builtin_fmaf(c[i], f, acc[i]);
                             }
-                            if constexpr (PART) {
-                                const uint32_t pr = ks * n + min(nt * kTile + r, n - 1u);
-                                const float sx = x_part ? s_sx[(pr * cs + t) * 2u + h] : 1.0f;
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    float f = sx;
-                                    if constexpr (PART == 2)
-                                        f *= *reinterpret_cast<const float*>(s_ws + (4u * q + i) * kScalePitch +
-                                                                             8u * t + 4u * h);
-                                    acc[nt][i] = __builtin_fmaf(c[i], f, acc[nt][i]);
-                                }
-                            } else {
-                                acc[nt] = c;
-                            }
+                        } else {
+                            acc = c;
                         }
                     }
                 };
@@ -432,64 +446,50 @@ __global__ __launch_bounds__(kThreads, PART == 2 || NT == 2 ? 3 : 4) void gemv_f
             }
 
             cur = nxt;
-            // ---- the waves' sums over the columns meet, in their order
+            // ---- the parts' sums meet, in their order, through the weights' LDS
             if (p.ks > 1) {
-                __syncthreads(); // the sums before are done with
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    s_acc[wv][nt][lane] = acc[nt];
+                s_w4[wv][lane] = __builtin_bit_cast(v4u, total);
+                s_w4[wv][kWaveSize + lane] = __builtin_bit_cast(v4u, acc);
+                __syncthreads();
+            }
+            acc = total + acc;
+            if (p.ks > 1) {
+                if (ks == 0)
+                    for (uint32_t i = 1; i < p.ks; ++i) { // a wave has two parts at most when others share its tile
+                        acc += __builtin_bit_cast(v4f, s_w4[wv + i][lane]);
+                        acc += __builtin_bit_cast(v4f, s_w4[wv + i][kWaveSize + lane]);
+                    }
                 __syncthreads();
                 if (ks != 0)
                     continue;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    for (uint32_t i = 1; i < p.ks; ++i) {
-                        const v4f a = s_acc[wv + i][nt][lane];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            acc[nt][k] += a[k];
-                    }
             }
             // ---- the activations' scales of whole rows, and the results
-            const uint32_t ln = here(lane);
+            if (r >= n)
+                continue;
+            const uint32_t o = o0 + 4u * (here(lane) >> 4);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (nt * kTile + (ln & 15u) >= n)
+            for (uint32_t i = 0; i < 4; ++i) {
+                if (o + i >= p.out_features)
                     continue;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t o = o0 + 4u * (ln >> 4) + i;
-                    if (o >= p.out_features)
-                        continue;
-                    const float v = acc[nt][i] * x_scale[nt];
-                    const size_t at = (size_t)row[nt] * p.out_features + o;
-                    if (p.out_bf16)
-                        static_cast<__bf16*>(p.out)[at] = (__bf16)v;
-                    else
-                        static_cast<float*>(p.out)[at] = v;
-                }
+                const float v = acc[i] * x_scale;
+                const size_t at = (size_t)mine.x * p.out_features + o + i;
+                if (p.out_bf16)
+                    static_cast<__bf16*>(p.out)[at] = (__bf16)v;
+                else
+                    static_cast<float*>(p.out)[at] = v;
             }
         }
     }
 }
 
-template <int XK, int PART, int NT>
+template <int XK, int PART>
 void launch_gemv(bool fast, const GemvParams& p, dim3 grid, hipStream_t s)
 {
     const uint32_t lds = p.lds_x + p.lds_x / kStepBytes * 8u;
     if (PART != 2 && fast)
-        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, NT, PART != 2>), grid, dim3(kThreads), lds, s, p);
+        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, PART != 2>), grid, dim3(kThreads), lds, s, p);
     else
-        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, NT, false>), grid, dim3(kThreads), lds, s, p);
-}
-
-template <int XK, int PART>
-void launch_gemv_nt(int nt, bool fast, const GemvParams& p, dim3 grid, hipStream_t s)
-{
-    if (nt == 1)
-        launch_gemv<XK, PART, 1>(fast, p, grid, s);
-    else
-        launch_gemv<XK, PART, 2>(fast, p, grid, s);
+        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, false>), grid, dim3(kThreads), lds, s, p);
 }
 
 // A group width's columns a scale; 0 when the kernels do not take it.
@@ -559,61 +559,70 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     p.scales = scales;
     p.out = out;
     p.rows = (uint32_t)rows;
-    p.k = (uint32_t)k;
     p.x_div = x_slots ? 1u : (uint32_t)k;
     p.experts = (uint32_t)experts;
     p.out_features = (uint32_t)out_features;
     p.in_features = (uint32_t)in_features;
-    p.group = (uint32_t)group;
     p.groups = (uint32_t)(in_features / group);
-    p.x_group = (uint32_t)xgroup;
     p.x_groups = (uint32_t)(in_features / xgroup);
-    p.x_kind = fp8 ? (xu8 ? kXFp8E8 : kXFp8F32) : kXBf16;
-    p.scale_u8 = u8;
     p.out_bf16 = out_bf16;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    p.group_magic = magic(p.group / 32u);
-    p.x_group_magic = magic(p.x_group / 32u);
-    p.group_magic128 = magic(p.group / 128u);
-    p.x_group_magic128 = magic(p.x_group / 128u);
+    p.group_magic = magic((uint32_t)group / 32u);
+    p.x_group_magic = magic((uint32_t)xgroup / 32u);
+    p.group_magic128 = magic((uint32_t)group / 128u);
+    p.x_group_magic128 = magic((uint32_t)xgroup / 128u);
     p.steps = (p.in_features + kStep - 1) / kStep;
-    // Columns are split over waves by the sizes alone, never by the number of
-    // tokens, so that a row's sum has one order.
-    const uint64_t waves = (uint64_t)p.k * ((p.out_features + kTile - 1) / kTile);
-    p.ks = waves >= 3072 ? 1u : waves >= 1536 ? 2u : 4u;
-    while (p.ks > p.steps)
+    // The columns' parts go by the sizes alone, never by the number of tokens, so that a row's sum has one order;
+    // they are summed by as many waves (ks) as leave every CU the workgroups that its LDS has room for, with eight
+    // steps of each x row staged.  (7168 -> 4096 bf16, one row: 15.3 us by one wave, 9.7 by two, 8.0 by four; 8192
+    // -> 8192 with 32 rows: 44.8, 34.9, 58.6; 7168 -> 2048 with top-8 of 8 experts, 64 tokens: 99, 103, 276; 64
+    // experts, 16 tokens: 94, 110, 134.)
+    const uint64_t tiles = (uint64_t)((p.out_features + kTile - 1) / kTile), waves = (uint64_t)k * tiles;
+    const uint64_t active = topk_idx ? (uint64_t)(rows < experts ? rows : experts) : 1u;
+    const uint64_t load = topk_idx ? (uint64_t)(rows / experts) : (uint64_t)rows; // an expert's rows on average
+    const uint32_t pass = load < 1 ? 1u : load < kTile ? (uint32_t)load : (uint32_t)kTile;
+    uint32_t parts = waves >= 3072 ? 1u : waves >= 1536 ? 2u : 4u;
+    while (parts > p.steps)
+        parts >>= 1;
+    p.steps_part = (p.steps + parts - 1) / parts;
+    p.ks = parts;
+    auto workgroups = [&] { return active * ((tiles * p.ks + kThreads / kWaveSize - 1) / (kThreads / kWaveSize)); };
+    auto fit = [](uint32_t lds) { return lds > kCuLds / 2u ? 1u : lds > kCuLds / 4u ? kCuLds / lds : 4u; };
+    while (p.ks > 1 && workgroups() > kCus * fit(kOwnLds + p.ks * pass * 8u * kStepBytes))
         p.ks >>= 1;
-    p.steps_wave = (p.steps + p.ks - 1) / p.ks;
+    p.steps_wave = p.ks == 1 ? p.steps : p.steps_part * (parts / p.ks);
     p.by_row = topk_idx && rows <= experts;
     const int part = !u8 ? 2 : fp8 && !xu8 && p.x_groups > 1 ? 1 : 0;
     const bool fast = u8 && group == 32 && in_features % kStep == 0 && aligned(scales, 8);
-    // x tiles of a pass by the rows an expert has on average
-    const uint64_t load = topk_idx ? (uint64_t)rows / (uint64_t)experts : (uint64_t)rows;
-    const int nt = tokens <= kTile || load <= 8 ? 1 : 2;
-    // Staged x rows: room for kAhead steps of every row of a full pass when
-    // experts have that many, else of a few more than they have on average
-    // (a more crowded one takes further passes)
-    const uint32_t want = topk_idx ? (uint32_t)(2 * load + 4) : (uint32_t)rows;
-    const uint32_t most = (uint32_t)(kTile * nt);
-    const uint32_t row_bytes = p.ks * (kAhead * kStepBytes + kRowPad);
-    p.lds_x = row_bytes * (want < most ? want : most);
-    p.lds_x = p.lds_x < 16448u ? 16448u : p.lds_x > 66560u ? 66560u : p.lds_x;
+    const uint32_t tiles_wg = kThreads / kWaveSize / p.ks;
+    const uint64_t wgs = workgroups();
+    // Staged x rows: what the LDS leaves beside a workgroup's own, with as many workgroups a CU as there are, up to
+    // four; at most all the columns of a full pass, at least kAhead steps of a few rows more than an expert has on
+    // average (a more crowded one takes further passes)
+    const uint32_t want = p.ks * (topk_idx && 2 * load + 4 < kTile ? (uint32_t)(2 * load + 4)
+                                  : topk_idx || load >= kTile      ? (uint32_t)kTile
+                                                                   : (uint32_t)load);
+    const uint32_t per_cu = wgs >= 4 * kCus ? 4u : (uint32_t)((wgs + kCus - 1) / kCus);
+    const uint32_t room = (kCuLds / per_cu - kOwnLds) / 65u * 64u; // each 512 bytes with 8 of fp32 scales
+    const uint32_t stage = p.steps_wave < kMaxStage ? p.steps_wave + kAhead : kMaxStage;
+    const uint32_t all = want * (stage * kStepBytes + kRowPad), least = want * (kAhead * kStepBytes + kRowPad);
+    p.lds_x = all < room ? all : room;
+    p.lds_x = p.lds_x < least ? least : p.lds_x;
+    p.lds_x = p.lds_x < 16448u ? 16448u : p.lds_x > 131072u ? 131072u : p.lds_x;
+    p.lds_x &= ~15u;
     // Several tiles a wave where that leaves four workgroups a CU: the x rows are then staged once for all of them
     // and a tile's first weights are on their way during the one before (2048 -> 7168, 16 tokens top-8 of 64:
     // 96.4 us with one tile, 95.2 with two, 94.0 with four, 99.8 with seven).
-    const uint64_t active = topk_idx ? (uint64_t)(rows < experts ? rows : experts) : 1u;
-    const uint32_t tiles_wg = kThreads / kWaveSize / p.ks;
-    const uint64_t wgs = active * ((p.out_features + kTile * tiles_wg - 1) / (kTile * tiles_wg));
     p.tiles = wgs >= 4096 ? 4u : wgs >= 2048 ? 2u : 1u;
     const uint32_t wg_rows = kTile * tiles_wg * p.tiles;
     const dim3 grid((p.out_features + wg_rows - 1) / wg_rows, !topk_idx ? 1u : p.by_row ? p.rows : p.experts + 1u);
-    if (p.x_kind == kXBf16)
-        part == 2 ? launch_gemv_nt<kXBf16, 2>(nt, fast, p, grid, s) : launch_gemv_nt<kXBf16, 0>(nt, fast, p, grid, s);
-    else if (p.x_kind == kXFp8E8)
-        part == 2 ? launch_gemv_nt<kXFp8E8, 2>(nt, fast, p, grid, s) : launch_gemv_nt<kXFp8E8, 0>(nt, fast, p, grid, s);
+    if (!fp8)
+        part == 2 ? launch_gemv<kXBf16, 2>(fast, p, grid, s) : launch_gemv<kXBf16, 0>(fast, p, grid, s);
+    else if (xu8)
+        part == 2 ? launch_gemv<kXFp8E8, 2>(fast, p, grid, s) : launch_gemv<kXFp8E8, 0>(fast, p, grid, s);
     else
-        part == 2   ? launch_gemv_nt<kXFp8F32, 2>(nt, fast, p, grid, s)
-        : part == 1 ? launch_gemv_nt<kXFp8F32, 1>(nt, fast, p, grid, s)
-                    : launch_gemv_nt<kXFp8F32, 0>(nt, fast, p, grid, s);
+        part == 2   ? launch_gemv<kXFp8F32, 2>(fast, p, grid, s)
+        : part == 1 ? launch_gemv<kXFp8F32, 1>(fast, p, grid, s)
+                    : launch_gemv<kXFp8F32, 0>(fast, p, grid, s);
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
