@@ -569,8 +569,9 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     hipStream_t s = static_cast<hipStream_t>(stream);
     p.group_magic = magic((uint32_t)group / 32u);
     p.x_group_magic = magic((uint32_t)xgroup / 32u);
-    p.group_magic128 = magic((uint32_t)group / 128u);
-    p.x_group_magic128 = magic((uint32_t)xgroup / 128u);
+    // (one scale a row may span a part of a step of 128)
+    p.group_magic128 = magic(((uint32_t)group + 127u) / 128u);
+    p.x_group_magic128 = magic(((uint32_t)xgroup + 127u) / 128u);
     p.steps = (p.in_features + kStep - 1) / kStep;
     // The columns' parts go by the sizes alone, never by the number of tokens, so that a row's sum has one order;
     // they are summed by as many waves (ks) as leave every CU the workgroups that its LDS has room for, with eight

@@ -122,6 +122,18 @@ def test_dense(tokens, xk, xg, u8, group):
         check(run(xk, x, xs, xg, None, tokens, 1, 0, codes, scales, u8, group, False), False, want, mag, inner, exact)
 
 
+@pytest.mark.parametrize("inner", [32, 96, 160, 288, 992, 2016, 4128])
+@pytest.mark.parametrize("xk", ["bf16", "fp8", "fp8e"])
+@pytest.mark.parametrize("u8", [True, False])
+def test_one_scale_a_row_of_any_width(inner, xk, u8):
+    say("gemv one scale a row", inner, xk, u8)
+    tokens, k, E, out = 5, 2, 3, 37
+    for exact in (True, False):
+        x, xs, idx, codes, scales = make(inner, tokens, k, E, out, inner, xk, 0, 0, u8, 0, exact)
+        want, mag = ref.gemv(ref.x_values(x, xs, xk), idx, k, 0, ref.fp4_values(codes, scales, u8))
+        check(run(xk, x, xs, 0, idx, tokens, k, 0, codes, scales, u8, 0, False), False, want, mag, inner, exact)
+
+
 def test_absent_repeated_and_crowded():
     say("gemv routing")
     E, out, inner, k = 6, 34, 256, 4
