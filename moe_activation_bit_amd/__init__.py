@@ -121,6 +121,9 @@ _STATUS = tuple(TkStatus(i) for i in range(len(TkStatus)))
 
 def _current_stream() -> int:
     import torch
+    if torch.cuda.is_initialized():
+        # the handle alone: making torch's stream object around it takes 2.9 us of a small launch's 7
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(torch.cuda.current_stream().cuda_stream)
 
 
