@@ -100,8 +100,9 @@ tk_status tk_rmsnorm_cast_fp8(const void* x, const void* residual, tk_dtype in_d
  *             by itself (the skip connection); NULL: none.
  *  dx         [n, hidden] of in_dtype; may be the dy or the dresidual buffer.
  *  dweight    fp32 [hidden], overwritten (zeros for n == 0); NULL: not computed.
- *  workspace  fp32 [min(n, TK_RMSNORM_PARTS), hidden]: the rows' partial sums;
- *             unused (may be NULL) when dweight is NULL or n == 0.
+ *  workspace  fp32 [min(n, TK_RMSNORM_PARTS), hidden]: the rows' partial sums
+ *             (of many rows; not touched for few); may be NULL when dweight is
+ *             NULL or n == 0.
  * [n, hidden] buffers, weight, dweight and workspace 16-byte aligned, rstd
  * 4-byte.  hidden as in the forward.
  */

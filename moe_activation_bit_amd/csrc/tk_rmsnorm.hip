@@ -7,9 +7,10 @@
 // code tail of the casts (tk_quant.h).  A row is held in registers between its
 // sum and its cast, so every input is read and every output written once.
 // Backward: dx = rstd * (g - a * mean(g*a)) + dresidual with g = dy * weight and
-// a = rstd * h, and dweight = sum over the rows of dy * a, gathered by each
-// workgroup over its rows in registers, written as one partial row, and summed
-// over the partial rows by a second kernel in their order.
+// a = rstd * h, and dweight = sum over the rows of dy * a: of many rows gathered
+// by each workgroup over its own in registers, written as one partial row, and
+// summed over the partial rows by a second kernel in their order; of few rows by
+// workgroups of their own in the same launch.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -24,6 +25,9 @@ namespace {
 using namespace tk_detail;
 
 constexpr uint32_t kMaxBlocks = 1u << 20;
+// Rows of a gradient whose dweight is summed beside them: 970 x 8192 in bf16 18.8 us so and 24.0 by partial rows,
+// 1024 x 16384 33.8 / 40.0; 1600 x 7168 27.4 / 27.4, 2048 x 2048 23.9 / 13.6.
+constexpr int64_t kShortRows = 1024;
 constexpr int64_t kMaxHidden = 32768; // 16 waves of 4 steps of 512 columns
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -342,6 +346,12 @@ struct NormBwdParams {
     uint32_t n;
     uint32_t slots;
     float inv_hidden;
+    // the short form's
+    float* dweight;
+    uint32_t column_blocks; // workgroups that sum dweight, before those of the rows
+    uint32_t col_lanes_log2; // lanes that share a row's part in those, two columns each
+    uint32_t waves;         // that share a row
+    uint32_t rows;          // of a workgroup
 };
 
 // One row per pass of a workgroup, rows blockIdx.x, + gridDim.x, ...; the rows'
@@ -488,6 +498,127 @@ __global__ __launch_bounds__(1024) void rmsnorm_dweight_kernel(const float* __re
     }
 }
 
+// Up to kShortRows rows: one launch for dx and dweight.  A partial row of
+// dweight for each row or two would be more bytes than the rows themselves, so
+// the first workgroups read dy and h again, from the caches, 32 or 64 columns
+// each: every 16 or 32 lanes take a row at a time, eight rows in flight, and
+// their sums meet in a fixed order.  The others take rows, as many as fit 16
+// waves.  Bound by a launch and two trips to memory, later by the caches: 3 x
+// 7168 in fp32 3.7 us (6.1 with partial rows and a second launch), 333 x 1024
+// 4.4 (6.6), 356 x 8192 in bf16 9.4 (15.5), 512 x 32768 37 (111).
+template <bool F32, int S, bool SKIP>
+__global__ __launch_bounds__(1024) void rmsnorm_backward_short_kernel(NormBwdParams p)
+{
+    __shared__ float sums[16][kWaveSize];
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1);
+    const uint32_t wib = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
+    if (blockIdx.x < p.column_blocks) {
+        constexpr uint32_t kBatch = 8;
+        const uint32_t hidden = p.slots * kSlotCols, lanes = 1u << p.col_lanes_log2;
+        const uint32_t part = threadIdx.x >> p.col_lanes_log2, parts = 1024u >> p.col_lanes_log2;
+        const uint32_t c = min(2u * (blockIdx.x * lanes + (lane & (lanes - 1u))), hidden - 2u);
+        float s0 = 0.0f, s1 = 0.0f;
+        for (uint32_t base = part; base < p.n; base += parts * kBatch) {
+            float r[kBatch];
+            uint2 dy[kBatch], h[kBatch]; // bf16: a word of each
+#pragma unroll
+            for (uint32_t k = 0; k < kBatch; ++k) {
+                const uint32_t row = min(base + parts * k, p.n - 1u);
+                const size_t at = (size_t)row * hidden + c;
+                r[k] = p.rstd[row];
+                if constexpr (F32) {
+                    dy[k] = *reinterpret_cast<const uint2*>(static_cast<const float*>(p.dy) + at);
+                    h[k] = *reinterpret_cast<const uint2*>(static_cast<const float*>(p.h) + at);
+                } else {
+                    dy[k].x = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.dy) + at);
+                    h[k].x = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.h) + at);
+                }
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < kBatch; ++k) {
+                const bool in = base + parts * k < p.n;
+                const float g0 = F32 ? as_float(dy[k].x) : bf16_lo(dy[k].x), a0 = F32 ? as_float(h[k].x) : bf16_lo(h[k].x);
+                const float g1 = F32 ? as_float(dy[k].y) : bf16_hi(dy[k].x), a1 = F32 ? as_float(h[k].y) : bf16_hi(h[k].x);
+                s0 = in ? s0 + g0 * (a0 * r[k]) : s0;
+                s1 = in ? s1 + g1 * (a1 * r[k]) : s1;
+            }
+        }
+        for (uint32_t x = lanes; x < kWaveSize; x <<= 1) {
+            s0 += __shfl_xor(s0, x);
+            s1 += __shfl_xor(s1, x);
+        }
+        if (lane < lanes) {
+            sums[wib][2u * lane] = s0;
+            sums[wib][2u * lane + 1u] = s1;
+        }
+        __syncthreads();
+        const uint32_t o = 2u * blockIdx.x * lanes + lane;
+        if (threadIdx.x < 2u * lanes && o < hidden) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s += sums[i][lane];
+            p.dweight[o] = s;
+        }
+        return;
+    }
+    const uint32_t local = wib / p.waves, part = wib - local * p.waves;
+    const uint32_t mine = (blockIdx.x - p.column_blocks) * p.rows + local;
+    const bool valid = local < p.rows && mine < p.n;
+    const uint32_t row = min(mine, p.n - 1u);
+    uint32_t slot[S];
+    Slot<F32> dy[S], h[S], skip[SKIP ? S : 1];
+    const float r = p.rstd[row];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        slot[s] = ((uint32_t)s * p.waves + part) * kWaveSize + lane;
+        const size_t at = (size_t)row * p.slots + min(slot[s], p.slots - 1u);
+        dy[s].load(p.dy, at);
+        h[s].load(p.h, at);
+        if constexpr (SKIP)
+            skip[s].load(p.dresidual, at);
+    }
+    float a[S][8], g[S][8], dot = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        float w[8], sum = 0.0f;
+        dy[s].get(g[s]);
+        h[s].get(a[s]);
+        load_weight(p.weight, min(slot[s], p.slots - 1u), w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            a[s][j] *= r;
+            g[s][j] *= w[j];
+            sum += g[s][j] * a[s][j];
+        }
+        dot += slot[s] < p.slots ? sum : 0.0f;
+    }
+    dot = wave_sum(dot);
+    if (p.waves > 1) {
+        if (lane == 0)
+            sums[0][wib] = dot;
+        __syncthreads();
+        dot = 0.0f;
+        for (uint32_t i = 0; i < p.waves; ++i)
+            dot += sums[0][min(local * p.waves + i, 15u)];
+    }
+    const float mean = dot * p.inv_hidden;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        float d[8];
+        if constexpr (SKIP)
+            skip[s].get(d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            g[s][j] = r * (g[s][j] - a[s][j] * mean);
+            if constexpr (SKIP)
+                g[s][j] += d[j];
+        }
+        if (valid && slot[s] < p.slots)
+            store_slot<F32>(p.dx, (size_t)row * p.slots + slot[s], g[s]);
+    }
+}
+
 template <bool F32, int S, int MAXT, int GM>
 void launch_norm(int sfmt, const NormParams& p, dim3 grid, dim3 block, size_t lds, hipStream_t s)
 {
@@ -511,6 +642,13 @@ void launch_norm_gm(int gm, int sfmt, const NormParams& p, dim3 grid, dim3 block
 template <bool F32, int S>
 void launch_norm_backward(bool skip, const NormBwdParams& p, dim3 grid, dim3 block, hipStream_t s)
 {
+    if (p.dweight) {
+        if (skip)
+            hipLaunchKernelGGL((rmsnorm_backward_short_kernel<F32, S, true>), grid, block, 0, s, p);
+        else
+            hipLaunchKernelGGL((rmsnorm_backward_short_kernel<F32, S, false>), grid, block, 0, s, p);
+        return;
+    }
     if (skip)
         hipLaunchKernelGGL((rmsnorm_backward_kernel<F32, S, true, 1024>), grid, block, 0, s, p);
     else
@@ -685,7 +823,28 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
         p.inv_hidden = 1.0f / (float)hidden;
         const uint32_t steps = (p.slots + kWaveSize - 1) / kWaveSize;
         const uint32_t S = steps_per_wave(steps, 1u);
-        const dim3 grid(parts), block((steps + S - 1) / S * kWaveSize);
+        p.waves = (steps + S - 1) / S;
+        dim3 grid(parts), block(p.waves * kWaveSize);
+        const bool together = dweight && n <= kShortRows;
+        if (together) {
+            p.partial = nullptr;
+            p.dweight = dweight;
+            p.rows = 16u / p.waves;
+            // 32 columns or 64: fp32 333 x 1024 4.5 / 6.5 us, 1024 x 4096 19.5 / 24.0, 320 x 7168 15.9 / 14.7;
+            // bf16 1024 x 1024 4.9 / 6.4, 1024 x 4096 14.8 / 15.1, 320 x 7168 10.1 / 7.9
+            p.col_lanes_log2 = hidden <= 4096 ? 4u : 5u;
+            p.column_blocks = (uint32_t)(hidden + (2 << p.col_lanes_log2) - 1) >> (p.col_lanes_log2 + 1);
+            const uint32_t row_blocks = ((uint32_t)n + p.rows - 1u) / p.rows;
+            block = dim3(1024);
+            grid = dim3(p.column_blocks + row_blocks);
+            if (dx == dy) { // dweight first: it reads dy, which the rows write
+                grid = dim3(p.column_blocks);
+                f32 ? launch_norm_backward<true, 1>(false, p, grid, block, s)
+                    : launch_norm_backward<false, 1>(false, p, grid, block, s);
+                grid = dim3(row_blocks);
+                p.column_blocks = 0;
+            }
+        }
 #define TK_NORM_BWD(SS)                                                      \
     case SS:                                                                 \
         f32 ? launch_norm_backward<true, SS>(dresidual != nullptr, p, grid, block, s)  \
@@ -699,6 +858,8 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
 #undef TK_NORM_BWD
         if (hipGetLastError() != hipSuccess)
             return TK_ERR_HIP;
+        if (together)
+            return TK_OK;
     }
     if (dweight) {
         hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((uint32_t)((hidden + kWaveSize - 1) / kWaveSize)), dim3(1024),

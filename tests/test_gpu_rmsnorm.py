@@ -293,3 +293,33 @@ def test_backward_in_place_without_dweight_and_empty():
     dw = torch.full((2048,), 7.0, device=DEV)
     assert tk.tk_rmsnorm_backward(None, None, 0, None, None, None, 0, 2048, None, dw, None) == OK
     assert not dw.any()
+
+
+@pytest.mark.parametrize("hidden", [8, 512, 520, 1024, 4096, 8192, 8200, 16392, 32768])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_backward_rows_do_not_depend_on_their_number(hidden, bf16):
+    say("norm backward batch", hidden, bf16)
+    n = 1100
+    dy, dres, w = make(hidden, n, hidden, bf16, True)
+    h = make(hidden + 1, n, hidden, bf16, False, 4.0)[0]
+    rstd = ref.norm(value(h, bf16), w, 1e-6)[0].astype(np.float32)
+    for skip in (dres, None):
+        whole, _ = run_backward(dy, h, w, rstd, skip, bf16)
+        for rows in (slice(0, 1), slice(3, 40), slice(76, 1100)):
+            part, _ = run_backward(dy[rows], h[rows], w, rstd[rows], None if skip is None else skip[rows], bf16)
+            assert np.array_equal(whole[rows], part), rows
+
+
+@pytest.mark.parametrize("n,hidden", [(3, 8), (32, 64), (255, 1016), (257, 2048), (1023, 1024), (1024, 72), (1025, 72), (700, 7168),
+                                      (33, 16384), (64, 20480)])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_backward_of_few_rows(n, hidden, bf16):
+    say("norm backward few rows", n, hidden, bf16)
+    dy, dres, w = make(n * hidden, n, hidden, bf16, True)
+    h = make(n * hidden + 1, n, hidden, bf16, False, 4.0)[0]
+    rstd = ref.norm(value(h, bf16), w, 1e-6)[0].astype(np.float32)
+    dx, dw = run_backward(dy, h, w, rstd, dres, bf16)
+    check_backward(dy, h, w, rstd, dres, bf16, dx, dw)
+    for place in ("dy", "dres"):
+        dx2, dw2 = run_backward(dy, h, w, rstd, dres, bf16, place)
+        assert np.array_equal(dx, dx2) and np.array_equal(dw, dw2), place
