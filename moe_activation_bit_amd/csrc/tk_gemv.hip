@@ -110,7 +110,7 @@ constexpr uint32_t kOwnLds = kThreads / kWaveSize * (kTile * 8 + kTile * 128 + k
 // TB/s; one row of a single expert, 7168 -> 4096: 8 us, a launch and the row's
 // staging), so everything else keeps out of their way.  For many rows of one
 // expert it is the staging of the rows, once for every pass and workgroup (64
-// rows of 7168 -> 4096: 54 us; 32 rows a pass instead of 16: 52).  A wave reads a step's 16 x 128 bytes with two instructions of eight
+// rows of 7168 -> 4096: 23 us).  A wave reads a step's 16 x 128 bytes with two instructions of eight
 // whole lines (lane l: row l / 8, 16 bytes l % 8), kAhead steps before their
 // use, and passes them through 2 KiB of LDS of its own into the instruction's
 // layout, lane (r, q) = (l & 15, l >> 4): weight row r, columns 32q.. of each
@@ -160,12 +160,12 @@ __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(G
 
     // One workgroup: ks waves along the columns of each of kWaves / ks tiles of
     // 16 weight rows.  Its rows are those whose expert is e, in order,
-    // pass_rows at a time.  by_row: y is a row, and the first row of an expert
-    // does the work of all of them; else y is an expert, and the one past the
-    // last writes the absent rows' zeros.  Every branch around a barrier is the
+    // pass_rows at a time: z takes the passes z, z + gridDim.z, ...  by_row: y is
+    // a row, and the first row of an expert does the work of all of them; else y
+    // is an expert, and the one past the last writes the absent rows' zeros.  Every branch around a barrier is the
     // same for all waves.
     const uint32_t y = blockIdx.y;
-    uint32_t e = 0, next = 0;
+    uint32_t e = 0, next = 0, seen = 0, first = blockIdx.z * pass_rows; // of the expert's rows
     if (p.idx) {
         if (p.by_row) {
             next = y;
@@ -191,6 +191,8 @@ __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(G
         }
     };
     if (e >= p.experts) { // absent rows: this one, or all of them
+        if (blockIdx.z)
+            return;
         for (uint32_t base = p.by_row ? y & ~(uint32_t)(kWaveSize - 1) : 0u; base < (p.by_row ? y + 1u : p.rows);
              base += kWaveSize) {
             const uint32_t mine = base + lane;
@@ -271,21 +273,23 @@ __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(G
     };
 
     while (true) {
-        // ---- the next rows of this expert, at most pass_rows
+        // ---- this workgroup's next rows of the expert: those numbered first, first + 1, ..., at most pass_rows
         uint32_t n = 0;
         while (next < p.rows && n < pass_rows) {
             const uint32_t base = next & ~(uint32_t)(kWaveSize - 1), row = base + lane;
             const bool hit = row >= next && row < p.rows && (!p.idx || (uint32_t)p.idx[row] == e);
             const uint64_t mask = __builtin_amdgcn_ballot_w64(hit);
-            const uint32_t rank = n + (uint32_t)__builtin_popcountll(mask & below);
-            if (hit && rank < pass_rows)
-                s_list[wv][rank] = make_uint2(row, row / p.x_div);
-            const uint64_t left = __builtin_amdgcn_ballot_w64(hit && rank >= pass_rows);
+            const uint32_t rank = seen + (uint32_t)__builtin_popcountll(mask & below);
+            if (hit && rank >= first && rank < first + pass_rows)
+                s_list[wv][rank - first] = make_uint2(row, row / p.x_div);
+            const uint64_t left = __builtin_amdgcn_ballot_w64(hit && rank >= first + pass_rows);
             next = left ? base + (uint32_t)__builtin_ctzll(left) : base + kWaveSize;
-            n = left ? pass_rows : n + (uint32_t)__builtin_popcountll(mask);
+            seen = left ? first + pass_rows : seen + (uint32_t)__builtin_popcountll(mask);
+            n = seen > first ? seen - first : 0u;
         }
         if (n == 0)
             break; // the same for every wave of the workgroup
+        first += gridDim.z * pass_rows;
         Tile cur = tile(0);
         wave_exchange();
 
@@ -573,21 +577,26 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     p.group_magic128 = magic(((uint32_t)group + 127u) / 128u);
     p.x_group_magic128 = magic(((uint32_t)xgroup + 127u) / 128u);
     p.steps = (p.in_features + kStep - 1) / kStep;
+    // Workgroups side by side for an expert's passes of kTile rows, as many as an expert has on average (64 rows of
+    // 7168 -> 4096: 54 us when one workgroup takes them all, 23 so; 512 rows of 4096 -> 4096 255 / 66; 64 tokens'
+    // top-8 of 8 experts 7168 -> 2048 99 / 60).
+    const uint64_t load = topk_idx ? (uint64_t)(rows / experts) : (uint64_t)rows; // an expert's rows on average
+    const uint32_t passes = load <= kTile ? 1u : load < 256u * kTile ? (uint32_t)((load + kTile - 1) / kTile) : 256u;
     // The columns' parts go by the sizes alone, never by the number of tokens, so that a row's sum has one order;
     // they are summed by as many waves (ks) as leave every CU the workgroups that its LDS has room for, with eight
-    // steps of each x row staged.  (7168 -> 4096 bf16, one row: 15.3 us by one wave, 9.7 by two, 8.0 by four; 8192
-    // -> 8192 with 32 rows: 44.8, 34.9, 58.6; 7168 -> 2048 with top-8 of 8 experts, 64 tokens: 99, 103, 276; 64
-    // experts, 16 tokens: 94, 110, 134.)
+    // steps of each x row staged.  (7168 -> 4096 bf16, one row: 15.3 us by one wave, 9.7 by two, 8.0 by four, 64 rows:
+    // 23 by one, 57 by four; 7168 -> 2048 for 16 tokens' top-8 of 64 experts: 94, 110, 134.)
     const uint64_t tiles = (uint64_t)((p.out_features + kTile - 1) / kTile), waves = (uint64_t)k * tiles;
     const uint64_t active = topk_idx ? (uint64_t)(rows < experts ? rows : experts) : 1u;
-    const uint64_t load = topk_idx ? (uint64_t)(rows / experts) : (uint64_t)rows; // an expert's rows on average
     const uint32_t pass = load < 1 ? 1u : load < kTile ? (uint32_t)load : (uint32_t)kTile;
     uint32_t parts = waves >= 3072 ? 1u : waves >= 1536 ? 2u : 4u;
     while (parts > p.steps)
         parts >>= 1;
     p.steps_part = (p.steps + parts - 1) / parts;
     p.ks = parts;
-    auto workgroups = [&] { return active * ((tiles * p.ks + kThreads / kWaveSize - 1) / (kThreads / kWaveSize)); };
+    auto workgroups = [&] {
+        return passes * active * ((tiles * p.ks + kThreads / kWaveSize - 1) / (kThreads / kWaveSize));
+    };
     auto fit = [](uint32_t lds) { return lds > kCuLds / 2u ? 1u : lds > kCuLds / 4u ? kCuLds / lds : 4u; };
     while (p.ks > 1 && workgroups() > kCus * fit(kOwnLds + p.ks * pass * 8u * kStepBytes))
         p.ks >>= 1;
@@ -616,7 +625,7 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     // 96.4 us with one tile, 95.2 with two, 94.0 with four, 99.8 with seven).
     p.tiles = wgs >= 4096 ? 4u : wgs >= 2048 ? 2u : 1u;
     const uint32_t wg_rows = kTile * tiles_wg * p.tiles;
-    const dim3 grid((p.out_features + wg_rows - 1) / wg_rows, !topk_idx ? 1u : p.by_row ? p.rows : p.experts + 1u);
+    const dim3 grid((p.out_features + wg_rows - 1) / wg_rows, !topk_idx ? 1u : p.by_row ? p.rows : p.experts + 1u, passes);
     if (!fp8)
         part == 2 ? launch_gemv<kXBf16, 2>(fast, p, grid, s) : launch_gemv<kXBf16, 0>(fast, p, grid, s);
     else if (xu8)
