@@ -74,6 +74,14 @@ __device__ __forceinline__ void wave_exchange()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// 16 bytes of weights, past the caches when nothing reads them again
+template <bool STREAM>
+__device__ __forceinline__ v4u load_weights(const char* at)
+{
+    const v4u* const p = reinterpret_cast<const v4u*>(at);
+    return STREAM ? __builtin_nontemporal_load(p) : *p;
+}
+
 // f(0), f(1), ... f(N - 1), each with its number as a constant
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void for_slots(F&& f)
@@ -106,7 +114,7 @@ constexpr uint32_t kOwnLds = kThreads / kWaveSize * (kTile * 8 + kTile * 128 + k
 // magnitude, where the bf16 instructions were exact.)
 //
 // What bounds it is the weights' bytes (7168 -> 4096, top-8 of 8 experts for one
-// token: 26.9 us, 4.7 TB/s; 2048 -> 7168 for 16 tokens' top-8 of 64: 93.5 us, 4.7
+// token: 24.8 us, 5.0 TB/s; 2048 -> 7168 for 16 tokens' top-8 of 64: 85.2 us, 5.2
 // TB/s; one row of a single expert, 7168 -> 4096: 8 us, a launch and the row's
 // staging), so everything else keeps out of their way.  For many rows of one
 // expert it is the staging of the rows, once for every pass and workgroup (64
@@ -124,7 +132,8 @@ constexpr uint32_t kOwnLds = kThreads / kWaveSize * (kTile * 8 + kTile * 128 + k
 // activations' alone; 2: the weights' too).
 // A result's column n (x row) is lane & 15, its rows 4q .. 4q + 3.
 //   FAST: UE8M0 weight scales of 32 columns and whole steps; else any.
-template <int XK, int PART, bool FAST>
+//   STREAM: weights past the caches.
+template <int XK, int PART, bool FAST, bool STREAM>
 __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(GemvParams p)
 {
     constexpr uint32_t kWaves = kThreads / kWaveSize;
@@ -224,13 +233,13 @@ __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(G
         const uint32_t b = b0 + t;
         if constexpr (FAST) {
             const char* const at = from.base + (size_t)b * (kStep / 2);
-            w0[u] = *reinterpret_cast<const v4u*>(at + from.off);
-            w1[u] = *reinterpret_cast<const v4u*>(at + from.off8);
+            w0[u] = load_weights<STREAM>(at + from.off);
+            w1[u] = load_weights<STREAM>(at + from.off8);
         } else { // columns past the row's end: its first ones, made zero
             const bool in = b * kStep + 32u * lpiece < p.in_features;
             const uint32_t at = in ? b * (kStep / 2) : 0u - 16u * lpiece;
-            const v4u v0 = *reinterpret_cast<const v4u*>(from.base + (from.off + at));
-            const v4u v1 = *reinterpret_cast<const v4u*>(from.base + (from.off8 + at));
+            const v4u v0 = load_weights<STREAM>(from.base + (from.off + at));
+            const v4u v1 = load_weights<STREAM>(from.base + (from.off8 + at));
             const uint32_t keep = in ? ~0u : 0u;
             w0[u] = v0 & keep;
             w1[u] = v1 & keep;
@@ -307,6 +316,7 @@ __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(G
         for (uint32_t j = 0; j < p.tiles; ++j) {
             const uint32_t o0 = o_first + j * o_next;
             const Tile nxt = tile(min(j + 1u, p.tiles - 1u));
+            const uint32_t after = !FAST || j + 1u < p.tiles ? 0u : last_step; // (no register for it in the others)
             v4f acc = {0.0f, 0.0f, 0.0f, 0.0f}, total = acc; // of the part, and of the parts before it
             uint32_t part_end = p.steps_part;
             for (uint32_t c0 = 0; c0 < p.steps_wave; c0 += cs) {
@@ -398,7 +408,9 @@ __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(G
                     wave_exchange();
                     const bool in = c0 + t + kAhead < share;
                     const Tile from = {in ? cur.base : nxt.base, in ? cur.off : nxt.off, in ? cur.off8 : nxt.off8};
-                    fetch(slot, from, in ? c0 + t + kAhead : min((uint32_t)u, last_step));
+                    // (after the last tile that tile's last step, which is on its way or in the cache: its first ones,
+                    // long evicted, were 13% more bytes with 14 steps a wave)
+                    fetch(slot, from, in ? c0 + t + kAhead : max(min((uint32_t)u, last_step), after));
                     const uint2 sb2 = PART == 2 ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu)
                                                 : *reinterpret_cast<const uint2*>(s_ws + r * kScalePitch + 8u * t);
 #pragma unroll
@@ -486,14 +498,23 @@ __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(G
     }
 }
 
-template <int XK, int PART>
-void launch_gemv(bool fast, const GemvParams& p, dim3 grid, hipStream_t s)
+template <int XK, int PART, bool FAST>
+void launch_gemv_stream(bool stream, const GemvParams& p, dim3 grid, hipStream_t s)
 {
     const uint32_t lds = p.lds_x + p.lds_x / kStepBytes * 8u;
-    if (PART != 2 && fast)
-        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, PART != 2>), grid, dim3(kThreads), lds, s, p);
+    if (stream)
+        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, FAST, true>), grid, dim3(kThreads), lds, s, p);
     else
-        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, false>), grid, dim3(kThreads), lds, s, p);
+        hipLaunchKernelGGL((gemv_fp4_kernel<XK, PART, FAST, false>), grid, dim3(kThreads), lds, s, p);
+}
+
+template <int XK, int PART>
+void launch_gemv(bool fast, bool stream, const GemvParams& p, dim3 grid, hipStream_t s)
+{
+    if (PART != 2 && fast)
+        launch_gemv_stream<XK, PART, PART != 2>(stream, p, grid, s);
+    else
+        launch_gemv_stream<XK, PART, false>(stream, p, grid, s);
 }
 
 // A group width's columns a scale; 0 when the kernels do not take it.
@@ -603,6 +624,10 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     p.steps_wave = p.ks == 1 ? p.steps : p.steps_part * (parts / p.ks);
     p.by_row = topk_idx && rows <= experts;
     const int part = !u8 ? 2 : fp8 && !xu8 && p.x_groups > 1 ? 1 : 0;
+    // Weights that as a rule one pass reads, in whole lines, go past the caches: 2048 -> 7168 for 16 tokens' top-8 of
+    // 64 experts 85.2 us, through them 94.0; 64 tokens 7168 -> 2048 122 / 129; but with several passes (64 tokens'
+    // top-8 of 16 experts, 7168 -> 4096) 154 / 136 and with lines that two rows share (2016 -> 2048) 42.3 / 37.0.
+    const bool once = passes == 1 && in_features % kStep == 0 && aligned(codes, 128);
     const bool fast = u8 && group == 32 && in_features % kStep == 0 && aligned(scales, 8);
     const uint32_t tiles_wg = kThreads / kWaveSize / p.ks;
     const uint64_t wgs = workgroups();
@@ -622,17 +647,17 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     p.lds_x &= ~15u;
     // Several tiles a wave where that leaves four workgroups a CU: the x rows are then staged once for all of them
     // and a tile's first weights are on their way during the one before (2048 -> 7168, 16 tokens top-8 of 64:
-    // 96.4 us with one tile, 95.2 with two, 94.0 with four, 99.8 with seven).
+    // 90.6 us with one tile, 86.9 with two, 85.1 with four, 86.3 with eight).
     p.tiles = wgs >= 4096 ? 4u : wgs >= 2048 ? 2u : 1u;
     const uint32_t wg_rows = kTile * tiles_wg * p.tiles;
     const dim3 grid((p.out_features + wg_rows - 1) / wg_rows, !topk_idx ? 1u : p.by_row ? p.rows : p.experts + 1u, passes);
     if (!fp8)
-        part == 2 ? launch_gemv<kXBf16, 2>(fast, p, grid, s) : launch_gemv<kXBf16, 0>(fast, p, grid, s);
+        part == 2 ? launch_gemv<kXBf16, 2>(fast, once, p, grid, s) : launch_gemv<kXBf16, 0>(fast, once, p, grid, s);
     else if (xu8)
-        part == 2 ? launch_gemv<kXFp8E8, 2>(fast, p, grid, s) : launch_gemv<kXFp8E8, 0>(fast, p, grid, s);
+        part == 2 ? launch_gemv<kXFp8E8, 2>(fast, once, p, grid, s) : launch_gemv<kXFp8E8, 0>(fast, once, p, grid, s);
     else
-        part == 2   ? launch_gemv<kXFp8F32, 2>(fast, p, grid, s)
-        : part == 1 ? launch_gemv<kXFp8F32, 1>(fast, p, grid, s)
-                    : launch_gemv<kXFp8F32, 0>(fast, p, grid, s);
+        part == 2   ? launch_gemv<kXFp8F32, 2>(fast, once, p, grid, s)
+        : part == 1 ? launch_gemv<kXFp8F32, 1>(fast, once, p, grid, s)
+                    : launch_gemv<kXFp8F32, 0>(fast, once, p, grid, s);
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
