@@ -9,10 +9,9 @@
 // 4.6, measured), so the 22 of a sigmoid cost about 3 us at 16384 tokens x 256
 // experts.
 //
-// route_row_kernel (k <= 16; no groups, or 2, 4, 8 or 16 groups of whole
-// lanes): four tokens per wave, one per 16-lane row, a lane holding
-// consecutive experts as lists of eight sorted scores; k rounds take the
-// largest list head of each row.  route_kernel takes what is left: one wave
+// route_row_kernel (k <= 16, up to 16 groups): four tokens per wave, one per
+// 16-lane row, a lane holding consecutive experts of a group as lists of eight
+// sorted scores; k rounds take the largest list head of each row.  route_kernel takes what is left: one wave
 // per token, the largest key searched anew each round.
 #include <hip/hip_runtime.h>
 
@@ -125,6 +124,7 @@ struct RouteParams {
     uint32_t tokens, experts, k, n_group, topk_group;
     uint32_t lane_experts; // route_row_kernel: experts a lane holds
     uint32_t gl_log2;      // ... and lanes a group, as a power of two
+    uint32_t group_experts;
     int softmax, normalise;
     double scale;
     int32_t* idx;
@@ -315,8 +315,10 @@ __device__ __forceinline__ void load_logits(const void* base, size_t i, float* x
 constexpr uint32_t kMasked = 0x007FFFFFu; // ordered(-inf): the key of a masked or absent expert
 
 // Four tokens per wave: lane q of row r holds experts q * C .. + C - 1 of token
-// t0 + r, C = FC (experts == 16 * FC) or p.lane_experts, in L lists of N
-// (slots past the last expert hold -inf, as masked experts do).  The keys
+// t0 + r (FC > 0: experts == 16 * C, groups of whole lanes) or, with C =
+// p.lane_experts, up to C of group q >> p.gl_log2, in L lists of N (slots past
+// the last expert hold -inf, as masked experts do; so does a group past the
+// last, whose index is then the larger one).  The keys
 // order as the gating's do: score, then the smaller index.
 // MOVE (FC = 16, kept groups within 8 lanes): once the groups are ranked, each
 // kept lane's halves go to two lanes of the row, in order, so that every lane
@@ -340,6 +342,13 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
     const uint32_t lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
     const uint32_t q = lane & 15u, row = lane >> 4;
     const uint32_t C = FULL ? (uint32_t)FC : p.lane_experts;
+    // the lane's first expert, and how many it has
+    uint32_t from = q * C, own = C;
+    if constexpr (!FULL) {
+        const uint32_t g = q >> p.gl_log2, sub = (q & ((1u << p.gl_log2) - 1u)) * C, per = p.group_experts;
+        from = g * per + sub;
+        own = g < p.n_group && sub < per ? min(C, per - sub) : 0u;
+    }
     const bool by_score = p.bias || p.n_group > 1;
     const uint32_t first = 4u * __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + wv);
 
@@ -361,8 +370,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
             for (int j = 0; j < M; ++j) {
-                const uint32_t e = q * C + j;
-                x[j] = (uint32_t)j < C && e < p.experts ? s_in[wv][row][min(e, 16u * M - 1u)] : -INFINITY;
+                x[j] = (uint32_t)j < own ? s_in[wv][row][min(from + j, 16u * M - 1u)] : -INFINITY;
             }
         }
 
@@ -424,7 +432,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
                 float b[M];
 #pragma unroll
                 for (int j = 0; j < M; ++j)
-                    b[j] = held(j) ? p.bias[FULL ? q * FC + j : min(q * C + j, p.experts - 1u)] : 0.0f;
+                    b[j] = held(j) ? p.bias[FULL ? q * FC + j : min(from + j, p.experts - 1u)] : 0.0f;
 #pragma unroll
                 for (int j = 0; j < M; ++j)
                     x[j] += b[j];
@@ -439,10 +447,10 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
                 for (int j = 0; j < M; j += 2)
                     bad |= __builtin_isunordered(x[j], x[j + 1]);
             }
-            if constexpr (!FULL) { // the last lane's slots past the last expert
+            if constexpr (!FULL) { // slots past the lane's last expert
 #pragma unroll
                 for (int j = 0; j < M; ++j)
-                    x[j] = q * C + j < p.experts ? x[j] : -INFINITY;
+                    x[j] = (uint32_t)j < own ? x[j] : -INFINITY;
             }
         } else if (p.softmax && !p.normalise) {
             double sum = 0.0;
@@ -462,7 +470,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
         }
 
         // ---- groups: the lanes of those that are not among the best hold nothing any more
-        uint32_t base0 = q * C; // the expert of the lane's first slot
+        uint32_t base0 = from; // the expert of the lane's first slot
         if (p.n_group > 1) {
             const float pinf = opaque_inf(false);
             float a1 = fmax2(x[0], x[1], pinf), a2 = fmin2(x[0], x[1], opaque_inf(true));
@@ -912,7 +920,7 @@ void launch_route_k(const RouteParams& p, dim3 grid, hipStream_t s)
 template <bool BF16>
 void launch_route_row(const RouteParams& p, dim3 grid, hipStream_t s)
 {
-    switch (p.experts) {
+    switch ((p.n_group << p.gl_log2) == 16u && p.lane_experts * 16u == p.experts ? p.experts : 0u) {
     case 64: return launch_route_k<BF16, 1, 4>(p, grid, s);
     case 128: return launch_route_k<BF16, 1, 8>(p, grid, s);
     case 256:
@@ -999,11 +1007,13 @@ tk_status tk_route(const void* logits, tk_dtype in_dtype, const float* bias, int
     p.idx = topk_idx;
     p.weight = topk_weight;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    // four tokens per wave; with groups, each of them has to be whole lanes
-    const bool lanes = experts % 16 == 0 && (n_group == 2 || n_group == 4 || n_group == 8 || n_group == 16);
-    if (k <= 16 && (n_group == 1 || lanes)) {
-        p.lane_experts = (uint32_t)((experts + 15) / 16);
-        p.gl_log2 = (uint32_t)__builtin_ctzll((unsigned long long)(16 / n_group));
+    // four tokens per wave, a group to a power of two of a row's 16 lanes, 32 experts a lane at most
+    p.gl_log2 = 4;
+    while (p.gl_log2 > 0 && (n_group << p.gl_log2) > 16)
+        --p.gl_log2;
+    p.group_experts = (uint32_t)per;
+    p.lane_experts = (uint32_t)((per + (1 << p.gl_log2) - 1) >> p.gl_log2);
+    if (k <= 16 && n_group <= 16 && p.lane_experts <= 32) {
         const int64_t rblocks = (tokens + 4 * kWaves - 1) / (4 * kWaves);
         const dim3 rgrid((uint32_t)(rblocks < kMaxBlocks ? rblocks : kMaxBlocks));
         if (bf16)

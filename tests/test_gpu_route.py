@@ -75,6 +75,27 @@ def test_route(E, k, ng, tg, softmax):
         check_route(x, b, k, ng, tg, softmax, normalise, run_route(x, bf16, b, k, ng, tg, softmax, normalise))
 
 
+@pytest.mark.parametrize("E,k,ng,tg", [
+    (96, 4, 3, 2), (384, 8, 3, 2), (192, 8, 3, 1), (130, 6, 13, 5), (33, 4, 11, 4), (45, 5, 9, 3), (500, 8, 10, 4),
+    (30, 4, 15, 15), (12, 3, 6, 3), (510, 16, 15, 8), (496, 8, 16, 4), (40, 16, 5, 5), (306, 7, 6, 2), (62, 2, 2, 1),
+])
+@pytest.mark.parametrize("softmax", [False, True])
+def test_route_groups_of_any_size(E, k, ng, tg, softmax):
+    say("route any groups", E, k, ng, tg, softmax)
+    for n, (T, bf16, with_bias, normalise, masked) in enumerate([
+            (1, False, True, 1, 0.0), (41, False, False, 1, 0.0), (22, True, True, 0, 0.3), (9, False, True, 1, 0.97)]):
+        x, bias = make(E * 100 + k + n, T, E, bf16, masked)
+        b = bias if with_bias else None
+        check_route(x, b, k, ng, tg, softmax, normalise, run_route(x, bf16, b, k, ng, tg, softmax, normalise))
+    # every key equal, and whole groups masked
+    x = np.zeros((5, E), np.float32)
+    x[1, :E // ng] = -np.inf
+    x[2, E // ng:] = -np.inf
+    x[3] = -np.inf
+    x[4, ::2] = -np.inf
+    check_route(x, None, k, ng, tg, softmax, 1, run_route(x, False, None, k, ng, tg, softmax, 1))
+
+
 @pytest.mark.parametrize("E,k,ng,tg", [(256, 8, 8, 4), (64, 6, 1, 1), (512, 8, 16, 8), (160, 8, 8, 3)])
 def test_route_ties_extremes_and_masks(E, k, ng, tg):
     say("route values", E, k, ng, tg)
