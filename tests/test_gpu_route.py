@@ -96,6 +96,33 @@ def test_route_groups_of_any_size(E, k, ng, tg, softmax):
     check_route(x, None, k, ng, tg, softmax, 1, run_route(x, False, None, k, ng, tg, softmax, 1))
 
 
+@pytest.mark.parametrize("E,k,ng,tg", [(256, 8, 8, 4), (64, 6, 1, 1), (512, 8, 16, 8), (160, 6, 8, 3), (128, 8, 1, 1), (96, 4, 3, 2)])
+@pytest.mark.parametrize("spread", [0, 2.0 ** -25, 2.0 ** -23, 2.0 ** -21, 2.0 ** -19, 2.0 ** -16])
+@pytest.mark.parametrize("offset", [0.0, 1.0, -1000.0])
+def test_route_keys_that_nearly_tie(E, k, ng, tg, spread, offset):
+    """Scores that the bias brings to within a few units of each other's last place: an order that only exact scores
+    tell, or (offset) that the sum's rounding makes a tie."""
+    say("route near ties", E, k, ng, tg, spread, offset)
+    T = 48
+    rng = np.random.default_rng(E + k)
+    x = (3 * rng.standard_normal((T, E))).astype(np.float32)
+    x[:, 1:] = x[:1, 1:]  # one bias for all: the rows' other logits are equal
+    x[:, 0] += 8 * rng.random(T).astype(np.float32)
+    s = ref.scores(x[:1], False)[0]
+    bias = (offset + 0.7 - s + spread * rng.standard_normal(E)).astype(np.float32)
+    for T_ in (T, 3):
+        check_route(x[:T_], bias, k, ng, tg, False, 1, run_route(x[:T_], False, bias, k, ng, tg, False, 1))
+    # values of groups that cancel: keys of opposite signs
+    if ng > 1:
+        per = E // ng
+        b = bias.copy()
+        b[::per] += 500
+        b[1::per] -= 500
+        for g in range(ng):
+            b[g * per + 2:(g + 1) * per] -= 2000
+        check_route(x, b, min(k, 2 * tg), ng, tg, False, 1, run_route(x, False, b, min(k, 2 * tg), ng, tg, False, 1))
+
+
 @pytest.mark.parametrize("E,k,ng,tg", [(256, 8, 8, 4), (64, 6, 1, 1), (512, 8, 16, 8), (160, 8, 8, 3)])
 def test_route_ties_extremes_and_masks(E, k, ng, tg):
     say("route values", E, k, ng, tg)
