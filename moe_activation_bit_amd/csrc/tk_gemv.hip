@@ -37,6 +37,7 @@ struct GemvParams {
     uint32_t steps_part; // ... summed in parts of so many, whose sums are then added in order
     uint32_t ks;         // waves that share a tile's columns: 1, 2 or 4
     uint32_t tiles;      // tiles of 16 weight rows a wave goes through
+    uint32_t pass;       // x rows of a pass, at most
     uint32_t lds_x;      // bytes for staged rows
     int by_row;
 };
@@ -157,7 +158,7 @@ __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(G
     const uint64_t below = (1ull << lane) - 1u;
     const bool x_part = PART != 0 && XK == kXFp8F32 && p.x_groups > 1;
     // x rows of a pass: what leaves room for kAhead steps of each
-    const uint32_t pass_rows = min((uint32_t)kTile, p.lds_x / (p.ks * (kAhead * kStepBytes + kRowPad)));
+    const uint32_t pass_rows = min(p.pass, p.lds_x / (p.ks * (kAhead * kStepBytes + kRowPad)));
     // LDS slots of this lane's weights: row r keeps columns 32p.. in slot p ^ (r / 2), so that neither the
     // writes nor the reads of 16 rows meet in a bank
     const uint32_t lrow = lane >> 3, lpiece = lane & 7u;
@@ -598,18 +599,21 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     p.group_magic128 = magic(((uint32_t)group + 127u) / 128u);
     p.x_group_magic128 = magic(((uint32_t)xgroup + 127u) / 128u);
     p.steps = (p.in_features + kStep - 1) / kStep;
-    // Workgroups side by side for an expert's passes of kTile rows, as many as an expert has on average (64 rows of
-    // 7168 -> 4096: 54 us when one workgroup takes them all, 23 so; 512 rows of 4096 -> 4096 255 / 66; 64 tokens'
-    // top-8 of 8 experts 7168 -> 2048 99 / 60).
+    const uint64_t tiles = (uint64_t)((p.out_features + kTile - 1) / kTile), waves = (uint64_t)k * tiles;
+    const uint64_t active = topk_idx ? (uint64_t)(rows < experts ? rows : experts) : 1u;
     const uint64_t load = topk_idx ? (uint64_t)(rows / experts) : (uint64_t)rows; // an expert's rows on average
-    const uint32_t passes = load <= kTile ? 1u : load < 256u * kTile ? (uint32_t)((load + kTile - 1) / kTile) : 256u;
+    // Workgroups side by side for an expert's passes of 16 rows, as many as an expert has on average (64 rows of
+    // 7168 -> 4096: 54 us when one workgroup takes them all, 23 so; 512 rows of 4096 -> 4096 255 / 66; 64 tokens'
+    // top-8 of 8 experts 7168 -> 2048 99 / 60).  Passes of 8 while those leave CUs with less than two (20 rows of 8032
+    // -> 2048 in FP8 20.4 / 15.7 us, 15 of 4096 -> 1024 11.2 / 8.9; 32 of 7168 -> 4096 in bf16 18.3 / 19.1).
+    auto passes_of = [&](uint64_t n) { return load <= n ? 1u : load < 256u * n ? (uint32_t)((load + n - 1) / n) : 256u; };
+    p.pass = load > 8 && active * tiles * passes_of(kTile) < 2u * kCus ? 8u : (uint32_t)kTile;
+    const uint32_t passes = passes_of(p.pass);
     // The columns' parts go by the sizes alone, never by the number of tokens, so that a row's sum has one order;
     // they are summed by as many waves (ks) as leave every CU the workgroups that its LDS has room for, with eight
     // steps of each x row staged.  (7168 -> 4096 bf16, one row: 15.3 us by one wave, 9.7 by two, 8.0 by four, 64 rows:
     // 23 by one, 57 by four; 7168 -> 2048 for 16 tokens' top-8 of 64 experts: 94, 110, 134.)
-    const uint64_t tiles = (uint64_t)((p.out_features + kTile - 1) / kTile), waves = (uint64_t)k * tiles;
-    const uint64_t active = topk_idx ? (uint64_t)(rows < experts ? rows : experts) : 1u;
-    const uint32_t pass = load < 1 ? 1u : load < kTile ? (uint32_t)load : (uint32_t)kTile;
+    const uint32_t pass = load < 1 ? 1u : load < p.pass ? (uint32_t)load : p.pass;
     uint32_t parts = waves >= 3072 ? 1u : waves >= 1536 ? 2u : 4u;
     while (parts > p.steps)
         parts >>= 1;
@@ -619,7 +623,7 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
         return passes * active * ((tiles * p.ks + kThreads / kWaveSize - 1) / (kThreads / kWaveSize));
     };
     auto fit = [](uint32_t lds) { return lds > kCuLds / 2u ? 1u : lds > kCuLds / 4u ? kCuLds / lds : 4u; };
-    while (p.ks > 1 && workgroups() > kCus * fit(kOwnLds + p.ks * pass * 8u * kStepBytes))
+    while (p.ks > 1 && workgroups() > (p.pass < kTile ? 2u : 1u) * kCus * fit(kOwnLds + p.ks * pass * 8u * kStepBytes))
         p.ks >>= 1;
     p.steps_wave = p.ks == 1 ? p.steps : p.steps_part * (parts / p.ks);
     p.by_row = topk_idx && rows <= experts;
@@ -634,9 +638,9 @@ extern "C" tk_status tk_expert_gemv_fp4(const void* x, const void* x_scales, int
     // Staged x rows: what the LDS leaves beside a workgroup's own, with as many workgroups a CU as there are, up to
     // four; at most all the columns of a full pass, at least kAhead steps of a few rows more than an expert has on
     // average (a more crowded one takes further passes)
-    const uint32_t want = p.ks * (topk_idx && 2 * load + 4 < kTile ? (uint32_t)(2 * load + 4)
-                                  : topk_idx || load >= kTile      ? (uint32_t)kTile
-                                                                   : (uint32_t)load);
+    const uint32_t want = p.ks * (topk_idx && 2 * load + 4 < p.pass ? (uint32_t)(2 * load + 4)
+                                  : topk_idx || load >= p.pass      ? p.pass
+                                                                    : (uint32_t)load);
     const uint32_t per_cu = wgs >= 4 * kCus ? 4u : (uint32_t)((wgs + kCus - 1) / kCus);
     const uint32_t room = (kCuLds / per_cu - kOwnLds) / 65u * 64u; // each 512 bytes with 8 of fp32 scales
     const uint32_t stage = p.steps_wave < kMaxStage ? p.steps_wave + kAhead : kMaxStage;
