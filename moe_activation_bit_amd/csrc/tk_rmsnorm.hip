@@ -25,7 +25,8 @@ namespace {
 using namespace tk_detail;
 
 constexpr uint32_t kMaxBlocks = 1u << 20;
-// Rows of a gradient whose dweight is summed beside them: 970 x 8192 in bf16 18.8 us so and 24.0 by partial rows,
+// Rows of a gradient whose dweight is summed beside them (of more than 16384 columns always: a wave has no registers
+// left for their sums, 2048 x 32768 in bf16 133 us so and 326 with them spilled): 970 x 8192 in bf16 18.8 us so and 24.0 by partial rows,
 // 1024 x 16384 33.8 / 40.0; 1600 x 7168 27.4 / 27.4, 2048 x 2048 23.9 / 13.6.
 constexpr int64_t kShortRows = 1024;
 constexpr int64_t kMaxHidden = 32768; // 16 waves of 4 steps of 512 columns
@@ -355,18 +356,20 @@ struct NormBwdParams {
 };
 
 // One row per pass of a workgroup, rows blockIdx.x, + gridDim.x, ...; the rows'
-// dy * a sums stay in registers.  Rows of up to 16 steps (S = 1) keep the
+// dy * a sums stay in registers.  MANY: rows of up to two steps, p.rows of them
+// a pass, so that a CU has waves enough (16384 x 512 in bf16 28.0 -> 17.5 us, x 1024 34.8 -> 28.0).  Rows of up to 16 steps (S = 1) keep the
 // weight there too and have the next row's dy, h and dresidual on their way
 // while the waves' parts of a row's dot meet; longer ones have no registers for
 // either.  Bound by the bytes of the rows.
-template <bool F32, int S, bool SKIP, int MAXT>
-__global__ __launch_bounds__(MAXT) void rmsnorm_backward_kernel(NormBwdParams p)
+template <bool F32, int S, bool SKIP, bool MANY>
+__global__ __launch_bounds__(MANY ? 512 : 1024) void rmsnorm_backward_kernel(NormBwdParams p)
 {
     constexpr bool AHEAD = S == 1;
     __shared__ float part_dot[2][16];
     const uint32_t lane = threadIdx.x & (kWaveSize - 1);
-    const uint32_t wib = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
-    const uint32_t waves = blockDim.x / kWaveSize;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
+    const uint32_t waves = p.waves, rows = MANY ? p.rows : 1u;
+    const uint32_t local = MANY ? wave / waves : 0u, wib = wave - local * waves; // row of a pass, part of the row
     float w[AHEAD ? S : 1][8], dw[S][8];
     uint32_t slot[S]; // lanes past the row's end read its last slot and add nothing to the dot
 #pragma unroll
@@ -399,9 +402,11 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_backward_kernel(NormBwdParams p)
             fetch_skip(row);
     };
     if constexpr (AHEAD)
-        fetch(blockIdx.x); // the grid has at most a workgroup a row
+        fetch(min(blockIdx.x * rows + local, p.n - 1u));
     uint32_t parity = 0;
-    for (uint32_t row = blockIdx.x; row < p.n; row += gridDim.x, parity ^= 1u) {
+    for (uint32_t base = blockIdx.x * rows; base < p.n; base += gridDim.x * rows, parity ^= 1u) {
+        const uint32_t row = base + local;
+        const bool valid = !MANY || row < p.n; // else the last row again, unused
         if constexpr (!AHEAD)
             fetch(row);
         const float r = rstd;
@@ -419,24 +424,24 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_backward_kernel(NormBwdParams p)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 a[s][j] *= r;
-                dw[s][j] += g[s][j] * a[s][j];
+                dw[s][j] = valid ? dw[s][j] + g[s][j] * a[s][j] : dw[s][j];
                 g[s][j] *= w[AHEAD ? s : 0][j];
                 part += g[s][j] * a[s][j];
             }
             dot += slot[s] < p.slots ? part : 0.0f;
         }
         if constexpr (AHEAD)
-            fetch(row + gridDim.x < p.n ? row + gridDim.x : row);
+            fetch(min(row + gridDim.x * rows, p.n - 1u));
         else
             fetch_skip(row);
         dot = wave_sum(dot);
         if (waves > 1) {
             if (lane == 0)
-                part_dot[parity][wib] = dot;
+                part_dot[parity][wave] = dot;
             __syncthreads();
             dot = 0.0f;
             for (uint32_t i = 0; i < waves; ++i)
-                dot += part_dot[parity][i];
+                dot += part_dot[parity][wave - wib + i];
         }
         const float mean = dot * p.inv_hidden;
 #pragma unroll
@@ -450,8 +455,24 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_backward_kernel(NormBwdParams p)
                 if constexpr (SKIP)
                     g[s][j] += AHEAD ? d[AHEAD ? s : 0][j] : e[j];
             }
-            if (slot[s] < p.slots)
+            if (valid && slot[s] < p.slots)
                 store_slot<F32>(p.dx, (size_t)row * p.slots + slot[s], g[s]);
+        }
+    }
+    if constexpr (MANY) { // the rows' sums meet in their order
+        __shared__ float s_dw[8][kWaveSize * 8];
+        if (p.partial) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s_dw[wave][j * kWaveSize + lane] = dw[0][j];
+            __syncthreads();
+            if (local != 0)
+                return;
+            for (uint32_t i = 1; i < rows; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    dw[0][j] += s_dw[i * waves + wib][j * kWaveSize + lane];
+            }
         }
     }
     if (p.partial) {
@@ -534,14 +555,17 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_short_kernel(NormBwdPar
                     h[k].x = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.h) + at);
                 }
             }
+            float b0 = 0.0f, b1 = 0.0f; // a batch's own sums first: long columns then lose less
 #pragma unroll
             for (uint32_t k = 0; k < kBatch; ++k) {
                 const bool in = base + parts * k < p.n;
                 const float g0 = F32 ? as_float(dy[k].x) : bf16_lo(dy[k].x), a0 = F32 ? as_float(h[k].x) : bf16_lo(h[k].x);
                 const float g1 = F32 ? as_float(dy[k].y) : bf16_hi(dy[k].x), a1 = F32 ? as_float(h[k].y) : bf16_hi(h[k].x);
-                s0 = in ? s0 + g0 * (a0 * r[k]) : s0;
-                s1 = in ? s1 + g1 * (a1 * r[k]) : s1;
+                b0 = in ? b0 + g0 * (a0 * r[k]) : b0;
+                b1 = in ? b1 + g1 * (a1 * r[k]) : b1;
             }
+            s0 += b0;
+            s1 += b1;
         }
         for (uint32_t x = lanes; x < kWaveSize; x <<= 1) {
             s0 += __shfl_xor(s0, x);
@@ -640,19 +664,30 @@ void launch_norm_gm(int gm, int sfmt, const NormParams& p, dim3 grid, dim3 block
 }
 
 template <bool F32, int S>
-void launch_norm_backward(bool skip, const NormBwdParams& p, dim3 grid, dim3 block, hipStream_t s)
+void launch_norm_backward(bool together, bool skip, const NormBwdParams& p, dim3 grid, dim3 block, hipStream_t s)
 {
-    if (p.dweight) {
+    if (together) {
         if (skip)
             hipLaunchKernelGGL((rmsnorm_backward_short_kernel<F32, S, true>), grid, block, 0, s, p);
         else
             hipLaunchKernelGGL((rmsnorm_backward_short_kernel<F32, S, false>), grid, block, 0, s, p);
         return;
     }
-    if (skip)
-        hipLaunchKernelGGL((rmsnorm_backward_kernel<F32, S, true, 1024>), grid, block, 0, s, p);
-    else
-        hipLaunchKernelGGL((rmsnorm_backward_kernel<F32, S, false, 1024>), grid, block, 0, s, p);
+    if constexpr (S == 1) {
+        if (p.rows > 1) {
+            if (skip)
+                hipLaunchKernelGGL((rmsnorm_backward_kernel<F32, S, true, true>), grid, block, 0, s, p);
+            else
+                hipLaunchKernelGGL((rmsnorm_backward_kernel<F32, S, false, true>), grid, block, 0, s, p);
+            return;
+        }
+    }
+    if constexpr (S <= 2) {
+        if (skip)
+            hipLaunchKernelGGL((rmsnorm_backward_kernel<F32, S, true, false>), grid, block, 0, s, p);
+        else
+            hipLaunchKernelGGL((rmsnorm_backward_kernel<F32, S, false, false>), grid, block, 0, s, p);
+    }
 }
 
 // The steps a lane holds of a row of `steps` 512-column steps: `pref`, more
@@ -787,7 +822,7 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
         return TK_ERR_INVALID_ARG;
     const bool f32 = (int)in_dtype == TK_DTYPE_FP32;
     const size_t t_bytes = (size_t)n * (size_t)hidden * (f32 ? 4u : 2u), w_bytes = (size_t)hidden * 4u;
-    const uint32_t parts = (uint32_t)(n < TK_RMSNORM_PARTS ? n : TK_RMSNORM_PARTS);
+    uint32_t parts = (uint32_t)(n < TK_RMSNORM_PARTS ? n : TK_RMSNORM_PARTS);
     const size_t ws_bytes = dweight ? (size_t)parts * w_bytes : 0;
     {
         const void* in[] = {dy, h, dresidual, weight, rstd};
@@ -824,8 +859,11 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
         const uint32_t steps = (p.slots + kWaveSize - 1) / kWaveSize;
         const uint32_t S = steps_per_wave(steps, 1u);
         p.waves = (steps + S - 1) / S;
-        dim3 grid(parts), block(p.waves * kWaveSize);
-        const bool together = dweight && n <= kShortRows;
+        p.rows = p.waves <= 2 ? 8u / p.waves : 1u;
+        const uint32_t passes = ((uint32_t)n + p.rows - 1u) / p.rows;
+        parts = passes < TK_RMSNORM_PARTS ? passes : TK_RMSNORM_PARTS;
+        dim3 grid(parts), block(p.rows * p.waves * kWaveSize);
+        const bool together = (dweight && n <= kShortRows) || S == 4;
         if (together) {
             p.partial = nullptr;
             p.dweight = dweight;
@@ -833,22 +871,22 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
             // 32 columns or 64: fp32 333 x 1024 4.5 / 6.5 us, 1024 x 4096 19.5 / 24.0, 320 x 7168 15.9 / 14.7;
             // bf16 1024 x 1024 4.9 / 6.4, 1024 x 4096 14.8 / 15.1, 320 x 7168 10.1 / 7.9
             p.col_lanes_log2 = hidden <= 4096 ? 4u : 5u;
-            p.column_blocks = (uint32_t)(hidden + (2 << p.col_lanes_log2) - 1) >> (p.col_lanes_log2 + 1);
+            p.column_blocks = dweight ? (uint32_t)(hidden + (2 << p.col_lanes_log2) - 1) >> (p.col_lanes_log2 + 1) : 0u;
             const uint32_t row_blocks = ((uint32_t)n + p.rows - 1u) / p.rows;
             block = dim3(1024);
             grid = dim3(p.column_blocks + row_blocks);
-            if (dx == dy) { // dweight first: it reads dy, which the rows write
+            if (dweight && dx == dy) { // dweight first: it reads dy, which the rows write
                 grid = dim3(p.column_blocks);
-                f32 ? launch_norm_backward<true, 1>(false, p, grid, block, s)
-                    : launch_norm_backward<false, 1>(false, p, grid, block, s);
+                f32 ? launch_norm_backward<true, 1>(true, false, p, grid, block, s)
+                    : launch_norm_backward<false, 1>(true, false, p, grid, block, s);
                 grid = dim3(row_blocks);
                 p.column_blocks = 0;
             }
         }
 #define TK_NORM_BWD(SS)                                                      \
     case SS:                                                                 \
-        f32 ? launch_norm_backward<true, SS>(dresidual != nullptr, p, grid, block, s)  \
-            : launch_norm_backward<false, SS>(dresidual != nullptr, p, grid, block, s); \
+        f32 ? launch_norm_backward<true, SS>(together, dresidual != nullptr, p, grid, block, s)  \
+            : launch_norm_backward<false, SS>(together, dresidual != nullptr, p, grid, block, s); \
         break;
         switch (S) {
             TK_NORM_BWD(1)

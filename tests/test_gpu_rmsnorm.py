@@ -323,3 +323,30 @@ def test_backward_of_few_rows(n, hidden, bf16):
     for place in ("dy", "dres"):
         dx2, dw2 = run_backward(dy, h, w, rstd, dres, bf16, place)
         assert np.array_equal(dx, dx2) and np.array_equal(dw, dw2), place
+
+
+@pytest.mark.parametrize("n,hidden", [(1025, 8), (1031, 168), (4099, 504), (1030, 512), (1037, 520), (2500, 1016), (1100, 1024),
+                                      (1026, 1032), (1030, 16392), (1025, 32768)])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_backward_of_narrow_and_wide_rows(n, hidden, bf16):
+    say("norm backward narrow and wide", n, hidden, bf16)
+    dy, dres, w = make(n + hidden, n, hidden, bf16, True)
+    h = make(n + hidden + 1, n, hidden, bf16, False, 4.0)[0]
+    rstd = ref.norm(value(h, bf16), w, 1e-6)[0].astype(np.float32)
+    dx, dw = run_backward(dy, h, w, rstd, dres, bf16)
+    check_backward(dy, h, w, rstd, dres, bf16, dx, dw)
+    dx2, dw2 = run_backward(dy, h, w, rstd, dres, bf16, "dy")
+    assert np.array_equal(dx, dx2) and np.array_equal(dw, dw2)
+    few, _ = run_backward(dy[-9:], h[-9:], w, rstd[-9:], dres[-9:], bf16)
+    assert np.array_equal(dx[-9:], few)
+
+
+def test_backward_without_dweight_of_any_width():
+    say("norm backward without dweight")
+    for n, hidden in ((5, 32768), (1200, 24), (700, 1024), (3, 16392), (2000, 520)):
+        dy, dres, w = make(n, n, hidden, True, True)
+        h = make(n + 1, n, hidden, True, False, 4.0)[0]
+        rstd = ref.norm(value(h, True), w, 1e-6)[0].astype(np.float32)
+        want, _ = run_backward(dy, h, w, rstd, dres, True)
+        got, _ = run_backward(dy, h, w, rstd, dres, True, dweight=False)
+        assert np.array_equal(got, want), (n, hidden)
