@@ -39,7 +39,7 @@ extern "C" {
 #define TK_DTYPE_FP8 2
 
 /* Rows of tk_rmsnorm_backward's workspace. */
-#define TK_RMSNORM_PARTS 512
+#define TK_RMSNORM_PARTS 256
 
 typedef enum {
     TK_SCORE_SIGMOID = 0, /* 1 / (1 + e^-l) of each logit */

@@ -43,7 +43,7 @@ TK_DTYPE_FP32 = 1
 TK_DTYPE_FP8 = 2
 TK_SCORE_SIGMOID = 0
 TK_SCORE_SOFTMAX = 1
-TK_RMSNORM_PARTS = 512
+TK_RMSNORM_PARTS = 256
 
 
 class TkStatus(enum.IntEnum):

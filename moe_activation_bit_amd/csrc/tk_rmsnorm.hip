@@ -25,10 +25,6 @@ namespace {
 using namespace tk_detail;
 
 constexpr uint32_t kMaxBlocks = 1u << 20;
-// Rows of a gradient whose dweight is summed beside them (of more than 16384 columns always: a wave has no registers
-// left for their sums, 2048 x 32768 in bf16 133 us so and 326 with them spilled): 970 x 8192 in bf16 18.8 us so and 24.0 by partial rows,
-// 1024 x 16384 33.8 / 40.0; 1600 x 7168 27.4 / 27.4, 2048 x 2048 23.9 / 13.6.
-constexpr int64_t kShortRows = 1024;
 constexpr int64_t kMaxHidden = 32768; // 16 waves of 4 steps of 512 columns
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -356,11 +352,14 @@ struct NormBwdParams {
 };
 
 // One row per pass of a workgroup, rows blockIdx.x, + gridDim.x, ...; the rows'
-// dy * a sums stay in registers.  MANY: rows of up to two steps, p.rows of them
-// a pass, so that a CU has waves enough (16384 x 512 in bf16 28.0 -> 17.5 us, x 1024 34.8 -> 28.0).  Rows of up to 16 steps (S = 1) keep the
+// dy * a sums stay in registers.  Rows of up to 16 steps (S = 1) keep the
 // weight there too and have the next row's dy, h and dresidual on their way
 // while the waves' parts of a row's dot meet; longer ones have no registers for
-// either.  Bound by the bytes of the rows.
+// either.  MANY: rows of up to four steps, p.rows of them a pass, so that a CU
+// has waves enough (16384 x 512 in bf16 15.9 us instead of 28.0, x 1024 26.2
+// instead of 34.8, x 2048 47.2 instead of 59.5).  Bound by the bytes of the
+// rows: a workgroup a CU, since each writes a partial row (8192 x 4096 47.6 us
+// with 256 of them, 51.8 with 512).
 template <bool F32, int S, bool SKIP, bool MANY>
 __global__ __launch_bounds__(MANY ? 512 : 1024) void rmsnorm_backward_kernel(NormBwdParams p)
 {
@@ -519,14 +518,14 @@ __global__ __launch_bounds__(1024) void rmsnorm_dweight_kernel(const float* __re
     }
 }
 
-// Up to kShortRows rows: one launch for dx and dweight.  A partial row of
+// Few rows, or very long ones: one launch for dx and dweight.  A partial row of
 // dweight for each row or two would be more bytes than the rows themselves, so
 // the first workgroups read dy and h again, from the caches, 32 or 64 columns
 // each: every 16 or 32 lanes take a row at a time, eight rows in flight, and
 // their sums meet in a fixed order.  The others take rows, as many as fit 16
 // waves.  Bound by a launch and two trips to memory, later by the caches: 3 x
 // 7168 in fp32 3.7 us (6.1 with partial rows and a second launch), 333 x 1024
-// 4.4 (6.6), 356 x 8192 in bf16 9.4 (15.5), 512 x 32768 37 (111).
+// 4.4 (6.6), 356 x 8192 in bf16 9.4 (15.5).
 template <bool F32, int S, bool SKIP>
 __global__ __launch_bounds__(1024) void rmsnorm_backward_short_kernel(NormBwdParams p)
 {
@@ -859,11 +858,14 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
         const uint32_t steps = (p.slots + kWaveSize - 1) / kWaveSize;
         const uint32_t S = steps_per_wave(steps, 1u);
         p.waves = (steps + S - 1) / S;
-        p.rows = p.waves <= 2 ? 8u / p.waves : 1u;
+        p.rows = p.waves <= 4 ? 8u / p.waves : 1u;
         const uint32_t passes = ((uint32_t)n + p.rows - 1u) / p.rows;
         parts = passes < TK_RMSNORM_PARTS ? passes : TK_RMSNORM_PARTS;
         dim3 grid(parts), block(p.rows * p.waves * kWaveSize);
-        const bool together = (dweight && n <= kShortRows) || S == 4;
+        // Whether dweight is summed beside the rows.  In bf16, so and by partial rows: 1024 x 1024 4.9 / 6.6 us, 1024 x
+        // 4096 14.7 / 12.6, 500 x 4096 9.2 / 9.5, 300 x 16384 13.9 / 19.4, 500 x 12616 21.1 / 19.6.  Beyond 16384
+        // columns always: a wave has no registers left for their sums (2048 x 32768 133 us, with them spilled 326).
+        const bool together = (dweight && n <= 1024 && n * hidden <= (n <= 512 ? 5 << 20 : 2 << 20)) || S == 4;
         if (together) {
             p.partial = nullptr;
             p.dweight = dweight;
