@@ -830,14 +830,18 @@ __global__ __launch_bounds__(kThreads) void route_backward_row_kernel(RouteBwdPa
         if (p.softmax) { // over the whole row, or, normalised, over the chosen experts alone
             float* const mine = s_rows + (DENSE ? (t - t0) * p.experts : 0u);
             float top = l;
-            if constexpr (DENSE)
+            // (unrolled: 406 tokens x 512 experts 10.3 -> 6.9 us, 4096 x 160 5.6 -> 5.0)
+            if constexpr (DENSE) {
+#pragma unroll 8
                 for (uint32_t i = q; i < p.experts; i += 16u)
                     top = fmaxf(top, mine[i]);
+            }
             top = unordered(row_umax(ordered(top)));
             if (top == -INFINITY)
                 top = 0.0f;
             double sum = 0.0;
             if constexpr (DENSE) {
+#pragma unroll 8
                 for (uint32_t i = q; i < p.experts; i += 16u) {
                     const float v = expf(mine[i] - top);
                     sum += (double)v;
@@ -853,9 +857,11 @@ __global__ __launch_bounds__(kThreads) void route_backward_row_kernel(RouteBwdPa
             const float dot = row_sum(d * s);
             grad = s * (d - dot);
             if constexpr (DENSE) {
-                if (t0 + row < p.tokens)
+                if (t0 + row < p.tokens) {
+#pragma unroll 8
                     for (uint32_t i = q; i < p.experts; i += 16u)
                         mine[i] = -(mine[i] * inv_sum) * dot;
+                }
             }
         } else {
             // s and 1 - s from one exponential, in 64 bits: scores too small for 32 still share the weight
