@@ -413,7 +413,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
                     }
                 }
                 sum = row_sum(sum);
-                inv_sum = sum > 0.0 ? 1.0 / sum : 0.0;
+                inv_sum = sum > 0.0 ? reciprocal64(sum) : 0.0; // at least 1
 #pragma unroll
                 for (int j = 0; j < M; ++j)
                     x[j] = held(j) ? (float)(e[j] * inv_sum) : x[j];
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
                 if (held(j))
                     sum += shifted(x[j]);
             sum = row_sum(sum);
-            inv_sum = sum > 0.0 ? 1.0 / sum : 0.0;
+            inv_sum = sum > 0.0 ? reciprocal64(sum) : 0.0; // at least 1
         }
         const uint64_t bad_lanes = __builtin_amdgcn_ballot_w64(bad);
         const bool poisoned = (uint32_t)(bad_lanes >> (lane & 48u)) & 0xFFFFu;
@@ -613,7 +613,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
         const bool present = out && got.y > kMasked && !poisoned;
         double s = 0.0;
         if (present) {
-            const float l = load_logit<BF16>(p.logits, at + got.x);
+            const float l = by_score ? load_logit<BF16>(p.logits, at + got.x) : unordered(got.y); // else the key itself
             s = p.softmax ? shifted(l) * inv_sum : sigmoid64(l);
         }
         if (p.normalise) {
