@@ -887,16 +887,18 @@ __global__ __launch_bounds__(kThreads) void route_backward_row_kernel(RouteBwdPa
         for (uint32_t i = lane * kPer; i < count; i += kWave * kPer) {
             if constexpr (!VEC) {
                 store_grad<BF16>(p.dlogits, run + i, s_rows[i]);
-            } else if constexpr (BF16) {
+            } else if constexpr (BF16) { // past the caches: 16384 x 256 in fp32 5.7 us, through them 6.9
                 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
                 bf16x8 v;
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j)
                     v[j] = (__bf16)s_rows[i + j];
-                *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(p.dlogits) + run + i) = v;
+                __builtin_nontemporal_store(
+                    v, reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(p.dlogits) + run + i));
             } else {
-                *reinterpret_cast<float4*>(static_cast<float*>(p.dlogits) + run + i) =
-                    *reinterpret_cast<const float4*>(s_rows + i);
+                typedef float f32x4 __attribute__((ext_vector_type(4)));
+                __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(s_rows + i),
+                                            reinterpret_cast<f32x4*>(static_cast<float*>(p.dlogits) + run + i));
             }
         }
         exchange(); // the LDS is written again
