@@ -356,6 +356,7 @@ struct NormBwdParams {
     uint32_t col_lanes_log2; // lanes that share a row's part in those, two columns each
     uint32_t waves;         // that share a row
     uint32_t rows;          // of a workgroup
+    uint32_t first_row;     // of the launch
     int cached;             // the rows are read through the caches, as the columns are
 };
 
@@ -594,7 +595,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_backward_short_kernel(NormBwdPar
         return;
     }
     const uint32_t local = wib / p.waves, part = wib - local * p.waves;
-    const uint32_t mine = (blockIdx.x - p.column_blocks) * p.rows + local;
+    const uint32_t mine = p.first_row + (blockIdx.x - p.column_blocks) * p.rows + local;
     const bool valid = local < p.rows && mine < p.n;
     const uint32_t row = min(mine, p.n - 1u);
     uint32_t slot[S];
@@ -879,6 +880,18 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
         // 4096 14.7 / 12.6, 500 x 4096 9.2 / 9.5, 300 x 16384 13.9 / 19.4, 500 x 12616 21.1 / 19.6.  Beyond 16384
         // columns always: a wave has no registers left for their sums (2048 x 32768 133 us, with them spilled 326).
         const bool together = (dweight && n <= 1024 && n * hidden <= (n <= 512 ? 5 << 20 : 2 << 20)) || S == 4;
+#define TK_NORM_BWD(SS)                                                      \
+    case SS:                                                                 \
+        f32 ? launch_norm_backward<true, SS>(together, dresidual != nullptr, p, grid, block, s)  \
+            : launch_norm_backward<false, SS>(together, dresidual != nullptr, p, grid, block, s); \
+        break;
+        auto launch = [&] {
+            switch (S) {
+                TK_NORM_BWD(1)
+                TK_NORM_BWD(2)
+                TK_NORM_BWD(4)
+            }
+        };
         if (together) {
             p.partial = nullptr;
             p.dweight = dweight;
@@ -890,26 +903,23 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
             // bf16 1024 x 1024 4.9 / 6.4, 1024 x 4096 14.8 / 15.1, 320 x 7168 10.1 / 7.9
             p.col_lanes_log2 = hidden <= 4096 ? 4u : 5u;
             p.column_blocks = dweight ? (uint32_t)(hidden + (2 << p.col_lanes_log2) - 1) >> (p.col_lanes_log2 + 1) : 0u;
-            const uint32_t row_blocks = ((uint32_t)n + p.rows - 1u) / p.rows;
             block = dim3(1024);
-            grid = dim3(p.column_blocks + row_blocks);
             if (dweight && dx == dy) { // dweight first: it reads dy, which the rows write
                 grid = dim3(p.column_blocks);
-                f32 ? launch_norm_backward<true, 1>(true, false, p, grid, block, s)
-                    : launch_norm_backward<false, 1>(true, false, p, grid, block, s);
-                grid = dim3(row_blocks);
+                launch();
                 p.column_blocks = 0;
             }
-        }
-#define TK_NORM_BWD(SS)                                                      \
-    case SS:                                                                 \
-        f32 ? launch_norm_backward<true, SS>(together, dresidual != nullptr, p, grid, block, s)  \
-            : launch_norm_backward<false, SS>(together, dresidual != nullptr, p, grid, block, s); \
-        break;
-        switch (S) {
-            TK_NORM_BWD(1)
-            TK_NORM_BWD(2)
-            TK_NORM_BWD(4)
+            // a launch holds fewer than 2^32 work-items
+            for (uint32_t row_blocks = ((uint32_t)n + p.rows - 1u) / p.rows; row_blocks;) {
+                const uint32_t now = row_blocks < kMaxBlocks ? row_blocks : kMaxBlocks;
+                grid = dim3(p.column_blocks + now);
+                launch();
+                p.column_blocks = 0;
+                p.first_row += now * p.rows;
+                row_blocks -= now;
+            }
+        } else {
+            launch();
         }
 #undef TK_NORM_BWD
         if (hipGetLastError() != hipSuccess)
