@@ -274,20 +274,22 @@ __device__ __forceinline__ double dpp_add(double v)
     return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// sum / maximum over each 16-lane row, in every lane of it
+// sum / maximum over each row of 16 lanes, or of 8, in every lane of it
+template <int LANES = 16>
 __device__ __forceinline__ double row_sum(double v)
 {
-    v = dpp_add<0xB1>(v);    // quad_perm [1,0,3,2]
-    v = dpp_add<0x4E>(v);    // quad_perm [2,3,0,1]
-    v = dpp_add<0x141>(v);   // row_half_mirror
-    return dpp_add<0x140>(v); // row_mirror
+    v = dpp_add<0xB1>(v);  // quad_perm [1,0,3,2]
+    v = dpp_add<0x4E>(v);  // quad_perm [2,3,0,1]
+    v = dpp_add<0x141>(v); // row_half_mirror
+    return LANES == 16 ? dpp_add<0x140>(v) : v; // row_mirror
 }
+template <int LANES = 16>
 __device__ __forceinline__ uint32_t row_umax(uint32_t v)
 {
     v = dpp_umax<0xB1>(v);
     v = dpp_umax<0x4E>(v);
     v = dpp_umax<0x141>(v);
-    return dpp_umax<0x140>(v);
+    return LANES == 16 ? dpp_umax<0x140>(v) : v;
 }
 
 // N consecutive logits as fp32.
@@ -320,6 +322,7 @@ constexpr uint32_t kMasked = 0x007FFFFFu; // ordered(-inf): the key of a masked 
 // the last expert hold -inf, as masked experts do; so does a group past the
 // last, whose index is then the larger one).  The keys
 // order as the gating's do: score, then the smaller index.
+// RL = 8: eight tokens per wave in the same way, a row of 8 lanes each.
 // MOVE (FC = 16, kept groups within 8 lanes): once the groups are ranked, each
 // kept lane's halves go to two lanes of the row, in order, so that every lane
 // sorts one list.
@@ -327,7 +330,7 @@ constexpr uint32_t kMasked = 0x007FFFFFu; // ordered(-inf): the key of a masked 
 // 256 experts in 8 groups, top-8, some 7.4 us of the 10.4 us that 16384 tokens
 // take (1379 and 15.7 us before MOVE, the paired reciprocals and the masks
 // looked for at once).
-template <bool BF16, int L, int FC, bool K8, bool MOVE>
+template <bool BF16, int L, int FC, bool K8, bool MOVE, int RL>
 __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_kernel(RouteParams p)
 {
     constexpr int N = FC == 4 ? 4 : 8;
@@ -335,12 +338,14 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
     constexpr int S = MOVE ? 1 : L; // lists to sort
     constexpr bool FULL = FC > 0;
     static_assert(!MOVE || (FC == 16 && L == 2), "two halves of eight");
+    static_assert(RL == 16 || (FULL && !MOVE), "groups and other counts in rows of 16 lanes");
+    constexpr uint32_t TW = kWave / RL; // tokens of a wave
     __shared__ uint2 s_pick[kWaves][kWave];                             // [row * 16 + round]: (expert, key)
     __shared__ float s_in[FULL ? 1 : kWaves][FULL ? 1 : 4][FULL ? 1 : 16 * M]; // the rows, to be read in lane order
     __shared__ uint4 s_move[MOVE ? kWaves : 1][2][MOVE ? kWave : 1];
     __shared__ uint32_t s_src[MOVE ? kWaves : 1][MOVE ? kWave : 1];
     const uint32_t lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
-    const uint32_t q = lane & 15u, row = lane >> 4;
+    const uint32_t q = lane & (RL - 1u), row = lane / RL;
     const uint32_t C = FULL ? (uint32_t)FC : p.lane_experts;
     // the lane's first expert, and how many it has
     uint32_t from = q * C, own = C;
@@ -350,9 +355,9 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
         own = g < p.n_group && sub < per ? min(C, per - sub) : 0u;
     }
     const bool by_score = p.bias || p.n_group > 1;
-    const uint32_t first = 4u * __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + wv);
+    const uint32_t first = TW * __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + wv);
 
-    for (uint32_t t0 = first; t0 < p.tokens; t0 += gridDim.x * (4u * kWaves)) {
+    for (uint32_t t0 = first; t0 < p.tokens; t0 += gridDim.x * (TW * kWaves)) {
         // a wave past the last token repeats it in its other rows and stores nothing from them
         const uint32_t t = t0 + row;
         const size_t at = (size_t)min(t, p.tokens - 1u) * p.experts;
@@ -386,7 +391,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
 #pragma unroll
             for (int j = 0; j < M; ++j)
                 m = fmaxf(m, x[j]);
-            m = unordered(row_umax(ordered(m)));
+            m = unordered(row_umax<RL>(ordered(m)));
             bad |= m == INFINITY;
             top = m == -INFINITY ? 0.0 : (double)m; // every expert masked: no inf - inf
         }
@@ -412,7 +417,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
                         sum += e[j];
                     }
                 }
-                sum = row_sum(sum);
+                sum = row_sum<RL>(sum);
                 inv_sum = sum > 0.0 ? reciprocal64(sum) : 0.0; // at least 1
 #pragma unroll
                 for (int j = 0; j < M; ++j)
@@ -458,11 +463,11 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
             for (int j = 0; j < M; ++j)
                 if (held(j))
                     sum += shifted(x[j]);
-            sum = row_sum(sum);
+            sum = row_sum<RL>(sum);
             inv_sum = sum > 0.0 ? reciprocal64(sum) : 0.0; // at least 1
         }
         const uint64_t bad_lanes = __builtin_amdgcn_ballot_w64(bad);
-        const bool poisoned = (uint32_t)(bad_lanes >> (lane & 48u)) & 0xFFFFu;
+        const bool poisoned = (uint32_t)(bad_lanes >> (row * RL)) & ((1u << RL) - 1u);
         if (bad_lanes != 0) { // a poisoned row still has to sort
 #pragma unroll
             for (int j = 0; j < M; ++j)
@@ -471,7 +476,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
 
         // ---- groups: the lanes of those that are not among the best hold nothing any more
         uint32_t base0 = from; // the expert of the lane's first slot
-        if (p.n_group > 1) {
+        if (RL == 16 && p.n_group > 1) {
             const float pinf = opaque_inf(false);
             float a1 = fmax2(x[0], x[1], pinf), a2 = fmin2(x[0], x[1], opaque_inf(true));
 #pragma unroll
@@ -548,16 +553,16 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
         }
 
         // ---- k rounds, four tokens at once; depth: the picks left, this one included
-        uint2* const pick_row = &s_pick[wv][row << 4];
+        uint2* const pick_row = &s_pick[wv][row * RL];
         auto round = [&](uint32_t it, uint32_t depth) {
             uint32_t h = key[0][0];
 #pragma unroll
             for (int l = 1; l < S; ++l)
                 h = max(h, key[l][0]);
-            const uint32_t m = row_umax(h);
+            const uint32_t m = row_umax<RL>(h);
             const uint64_t hit = __builtin_amdgcn_ballot_w64(h == m);
-            // the lowest set bit of each row's 16 bits (every row has one)
-            const uint64_t win = hit & ~(hit - 0x0001000100010001ull);
+            // the lowest set bit of each row's bits (every row has one)
+            const uint64_t win = hit & ~(hit - (RL == 16 ? 0x0001000100010001ull : 0x0101010101010101ull));
             const bool mine = __builtin_amdgcn_inverse_ballot_w64(win);
             if constexpr (S == 1) {
                 if (mine) {
@@ -617,7 +622,7 @@ __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_
             s = p.softmax ? shifted(l) * inv_sum : sigmoid64(l);
         }
         if (p.normalise) {
-            const double sum = row_sum(s);
+            const double sum = row_sum<RL>(s);
             if (sum != 0.0)
                 s /= sum;
         }
@@ -915,36 +920,41 @@ bool overlaps(const void* a, size_t an, const void* b, size_t bn)
 
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
-template <bool BF16, int L, int FC, bool MOVE = false>
-void launch_route_k(const RouteParams& p, dim3 grid, hipStream_t s)
+template <bool BF16, int L, int FC, bool MOVE = false, int RL = 16>
+void launch_route_k(const RouteParams& p, hipStream_t s)
 {
+    const uint32_t tokens = kWaves * (kWave / RL), blocks = (p.tokens + tokens - 1u) / tokens;
+    const dim3 grid(blocks < kMaxBlocks ? blocks : (uint32_t)kMaxBlocks);
     if (p.k == 8)
-        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, true, MOVE>), grid, dim3(kThreads), 0, s, p);
+        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, true, MOVE, RL>), grid, dim3(kThreads), 0, s, p);
     else
-        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, false, MOVE>), grid, dim3(kThreads), 0, s, p);
+        hipLaunchKernelGGL((route_row_kernel<BF16, L, FC, false, MOVE, RL>), grid, dim3(kThreads), 0, s, p);
 }
 
 // by the lists of eight a lane needs, the usual expert counts with their count compiled in
 template <bool BF16>
-void launch_route_row(const RouteParams& p, dim3 grid, hipStream_t s)
+void launch_route_row(const RouteParams& p, hipStream_t s)
 {
     switch ((p.n_group << p.gl_log2) == 16u && p.lane_experts * 16u == p.experts ? p.experts : 0u) {
-    case 64: return launch_route_k<BF16, 1, 4>(p, grid, s);
-    case 128: return launch_route_k<BF16, 1, 8>(p, grid, s);
+    case 64: // 32768 tokens of bf16, softmax top-6: 6.1 us with eight tokens a wave, 7.3 with four (64 tokens 3.5 / 3.4)
+        if (p.n_group == 1 && p.k <= 8)
+            return launch_route_k<BF16, 1, 8, false, 8>(p, s);
+        return launch_route_k<BF16, 1, 4>(p, s);
+    case 128: return launch_route_k<BF16, 1, 8>(p, s);
     case 256:
         if (p.n_group > 1 && (p.topk_group << p.gl_log2) <= 8)
-            return launch_route_k<BF16, 2, 16, true>(p, grid, s);
-        return launch_route_k<BF16, 2, 16>(p, grid, s);
-    case 160: return launch_route_k<BF16, 2, 10>(p, grid, s);
-    case 192: return launch_route_k<BF16, 2, 12>(p, grid, s);
-    case 384: return launch_route_k<BF16, 3, 24>(p, grid, s);
-    case 512: return launch_route_k<BF16, 4, 32>(p, grid, s);
+            return launch_route_k<BF16, 2, 16, true>(p, s);
+        return launch_route_k<BF16, 2, 16>(p, s);
+    case 160: return launch_route_k<BF16, 2, 10>(p, s);
+    case 192: return launch_route_k<BF16, 2, 12>(p, s);
+    case 384: return launch_route_k<BF16, 3, 24>(p, s);
+    case 512: return launch_route_k<BF16, 4, 32>(p, s);
     }
     switch ((p.lane_experts + 7) / 8) {
-    case 1: return launch_route_k<BF16, 1, 0>(p, grid, s);
-    case 2: return launch_route_k<BF16, 2, 0>(p, grid, s);
-    case 3: return launch_route_k<BF16, 3, 0>(p, grid, s);
-    default: return launch_route_k<BF16, 4, 0>(p, grid, s);
+    case 1: return launch_route_k<BF16, 1, 0>(p, s);
+    case 2: return launch_route_k<BF16, 2, 0>(p, s);
+    case 3: return launch_route_k<BF16, 3, 0>(p, s);
+    default: return launch_route_k<BF16, 4, 0>(p, s);
     }
 }
 
@@ -1022,12 +1032,10 @@ tk_status tk_route(const void* logits, tk_dtype in_dtype, const float* bias, int
     p.group_experts = (uint32_t)per;
     p.lane_experts = (uint32_t)((per + (1 << p.gl_log2) - 1) >> p.gl_log2);
     if (k <= 16 && n_group <= 16 && p.lane_experts <= 32) {
-        const int64_t rblocks = (tokens + 4 * kWaves - 1) / (4 * kWaves);
-        const dim3 rgrid((uint32_t)(rblocks < kMaxBlocks ? rblocks : kMaxBlocks));
         if (bf16)
-            launch_route_row<true>(p, rgrid, s);
+            launch_route_row<true>(p, s);
         else
-            launch_route_row<false>(p, rgrid, s);
+            launch_route_row<false>(p, s);
         return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
     }
     const int64_t blocks = (tokens + kWaves - 1) / kWaves;
