@@ -158,7 +158,8 @@ tk_status tk_route(const void* logits, tk_dtype in_dtype, const float* bias, int
  *   softmax              dlogit_e = s_e * (d_e - sum_i d_i s_i) for every e, d_e
  *                        0 where e is not chosen
  *   softmax, normalised  dlogit_j = w_j * (d_j - sum_i d_i w_i)
- *   and 0 elsewhere; sums in fp32, each value rounded once to in_dtype.
+ *   and 0 elsewhere, in 64 bits (softmax over all experts: from fp32
+ *   exponentials), rounded to fp32 and from there to in_dtype.
  *
  *  dweight      fp32 [tokens, k];  topk_idx  int32 [tokens, k], as tk_route
  *               wrote it (an entry outside 0..experts-1 is absent; a repeated

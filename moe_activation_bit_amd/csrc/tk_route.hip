@@ -91,6 +91,8 @@ __device__ __forceinline__ double exp64(double x)
 }
 // ... for a number x <= 0 of any size: below -1100 it gives 0 as there
 __device__ __forceinline__ double exp64_neg(double x) { return exp64(__builtin_fmax(x, -1100.0)); }
+// ... and NaN gives NaN
+__device__ __forceinline__ double exp64_nan(double x) { return exp64(x < -1100.0 ? -1100.0 : x); }
 
 // 1/d for a normal d whose reciprocal is normal: the hardware's estimate and one Newton step
 __device__ __forceinline__ double reciprocal64(double d)
@@ -655,6 +657,14 @@ __device__ __forceinline__ void store_grad(void* base, size_t i, float v)
     }
 }
 
+// Sums, scores and differences in 64 bits here and below: d - dot is a small
+// difference of large numbers where the gradients of a token's weights are
+// nearly equal or one expert has nearly all of the weight (in 32 bits,
+// gradients within 10^-3 of each other gave results off by 10^-4 of their
+// size).  Softmax over all experts takes fp32 exponentials, the same ones in the
+// sum and in the scores: what they are off by then scales the scores' shares and
+// cancels nothing (64-bit ones: 8192 tokens x 512 experts in bf16 10.1 us instead
+// of 8.6).
 // One wave per token; lane j < k holds the token's slot j, and the row is put
 // together in LDS before it is written.
 template <bool BF16>
@@ -663,10 +673,10 @@ __device__ __forceinline__ void route_backward_token(const RouteBwdParams& p, ui
 {
     const size_t row = (size_t)t * p.experts;
     int32_t e = -1;
-    float d = 0.0f;
+    double d = 0.0;
     if (lane < p.k) {
         e = p.idx[(size_t)t * p.k + lane];
-        d = p.scale * p.dweight[(size_t)t * p.k + lane];
+        d = (double)p.scale * (double)p.dweight[(size_t)t * p.k + lane];
     }
     bool live = (uint32_t)e < p.experts;
     for (uint32_t i = 0; i + 1 < p.k; ++i) {
@@ -676,13 +686,10 @@ __device__ __forceinline__ void route_backward_token(const RouteBwdParams& p, ui
     const float l = live ? load_logit<BF16>(p.logits, row + (uint32_t)e) : -INFINITY;
 
     const bool dense = p.softmax && !p.normalise;
-    float s = 0.0f;               // the score of this lane's slot
-    double s64 = 0.0;             // the same of a sigmoid, and 1 - s
-    float slope = 0.0f;
-    float top = 0.0f, inv_sum = 1.0f;
-    if (p.softmax) {
-        // over the whole row, or, normalised, over the chosen experts alone
-        top = l;
+    d = live ? d : 0.0;
+    float grad;
+    if (p.softmax) { // over the whole row, or, normalised, over the chosen experts alone
+        float top = l;
         if (dense)
             for (uint32_t i = lane; i < p.experts; i += kWave)
                 top = fmaxf(top, load_logit<BF16>(p.logits, row + i));
@@ -691,39 +698,33 @@ __device__ __forceinline__ void route_backward_token(const RouteBwdParams& p, ui
             top = fmaxf(top, __shfl_xor(top, m));
         if (top == -INFINITY)
             top = 0.0f;
-        float sum = 0.0f;
-        if (dense) {
+        const double own = !live ? 0.0 : dense ? (double)expf(l - top) : exp64_nan((double)l - (double)top);
+        double sum = dense ? 0.0 : own;
+        if (dense)
             for (uint32_t i = lane; i < p.experts; i += kWave)
-                sum += expf(load_logit<BF16>(p.logits, row + i) - top);
-        } else if (live) {
-            sum = expf(l - top);
-        }
+                sum += (double)expf(load_logit<BF16>(p.logits, row + i) - top);
         sum = wave_sum(sum);
-        inv_sum = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-        s = live ? expf(l - top) * inv_sum : 0.0f;
-    } else if (live) {
-        s64 = l == l ? sigmoid64(l) : (double)l;
-        s = (float)s64;
-        slope = (float)sigmoid64(-l);
-    }
-    float ds = live ? d : 0.0f;
-    float grad;
-    if (p.softmax) {
-        const float dot = wave_sum(ds * s);
-        grad = s * (ds - dot);
+        const double inv_sum = sum == 0.0 ? 0.0 : reciprocal64(sum); // else at least 1, or NaN
+        const double s = own * inv_sum, dot = wave_sum(d * s);
+        const float rest = (float)-(inv_sum * dot);
+        grad = (float)(s * (d - dot));
         for (uint32_t i = lane; i < p.experts; i += kWave)
-            s_row[i] = dense ? -(expf(load_logit<BF16>(p.logits, row + i) - top) * inv_sum) * dot : 0.0f;
+            s_row[i] = dense ? expf(load_logit<BF16>(p.logits, row + i) - top) * rest : 0.0f;
     } else {
+        double s = 0.0, slope = 0.0;
+        if (live) {
+            s = l == l ? sigmoid64(l) : (double)l;
+            slope = sigmoid64(-l);
+        }
         if (p.normalise) {
             // scores too small for 32 bits still share the weight between them
-            const double total = wave_sum(s64);
+            const double total = wave_sum(s);
             if (total != 0.0) {
-                s = (float)(s64 / total);
-                const float dot = wave_sum(ds * s);
-                ds = live ? ds - dot : 0.0f;
+                s /= total;
+                d -= wave_sum(d * s);
             }
         }
-        grad = ds * s * slope;
+        grad = (float)(d * s * slope);
         for (uint32_t i = lane; i < p.experts; i += kWave)
             s_row[i] = 0.0f;
     }
@@ -763,17 +764,6 @@ __device__ __forceinline__ bool named_before(int32_t e, uint32_t q, uint32_t k)
     }
 }
 
-__device__ __forceinline__ float row_sum(float v)
-{
-    auto add = [](float a, auto ctrl) {
-        return a + ffrom((uint32_t)__builtin_amdgcn_update_dpp(0, (int)fbits(a), decltype(ctrl)::value, 0xF, 0xF, false));
-    };
-    v = add(v, std::integral_constant<int, 0xB1>{});
-    v = add(v, std::integral_constant<int, 0x4E>{});
-    v = add(v, std::integral_constant<int, 0x141>{});
-    return add(v, std::integral_constant<int, 0x140>{});
-}
-
 // Four tokens per wave, one per 16-lane row (k <= 16): lane q < k of a row holds
 // the token's slot q.  The four rows, consecutive in memory, are put together
 // in LDS and written as one run; VEC: 16 bytes a lane (the rows' bytes and
@@ -800,15 +790,15 @@ __global__ __launch_bounds__(kThreads) void route_backward_row_kernel(RouteBwdPa
         const uint32_t count = min(4u, p.tokens - t0) * p.experts;
         const size_t at = (size_t)t * p.experts, run = (size_t)t0 * p.experts;
         int32_t e = -1;
-        float d = 0.0f;
+        double d = 0.0;
         if (q < p.k) {
             e = p.idx[(size_t)t * p.k + q];
-            d = p.scale * p.dweight[(size_t)t * p.k + q];
+            d = (double)p.scale * (double)p.dweight[(size_t)t * p.k + q];
         }
         const bool again = named_before(e, q, p.k);
         const bool live = (uint32_t)e < p.experts && !again;
         const float l = live ? load_logit<BF16>(p.logits, at + (uint32_t)e) : -INFINITY;
-        d = live ? d : 0.0f;
+        d = live ? d : 0.0;
 
         // the rows before the chosen experts' gradients: zeros, or the logits
         if constexpr (DENSE) {
@@ -844,7 +834,8 @@ __global__ __launch_bounds__(kThreads) void route_backward_row_kernel(RouteBwdPa
             top = unordered(row_umax(ordered(top)));
             if (top == -INFINITY)
                 top = 0.0f;
-            double sum = 0.0;
+            const double own = !live ? 0.0 : DENSE ? (double)expf(l - top) : exp64_nan((double)l - (double)top);
+            double sum = DENSE ? 0.0 : own;
             if constexpr (DENSE) {
 #pragma unroll 8
                 for (uint32_t i = q; i < p.experts; i += 16u) {
@@ -853,37 +844,34 @@ __global__ __launch_bounds__(kThreads) void route_backward_row_kernel(RouteBwdPa
                     if (t0 + row < p.tokens)
                         mine[i] = v;
                 }
-            } else {
-                sum = live ? (double)expf(l - top) : 0.0;
             }
-            const float total = (float)row_sum(sum);
-            const float inv_sum = total > 0.0f || total != total ? 1.0f / total : 0.0f;
-            const float s = live ? expf(l - top) * inv_sum : 0.0f;
-            const float dot = row_sum(d * s);
-            grad = s * (d - dot);
+            sum = row_sum(sum);
+            const double inv_sum = sum == 0.0 ? 0.0 : reciprocal64(sum); // else at least 1, or NaN
+            const double s = own * inv_sum, dot = row_sum(d * s);
+            grad = (float)(s * (d - dot));
             if constexpr (DENSE) {
+                const float rest = (float)-(inv_sum * dot);
                 if (t0 + row < p.tokens) {
 #pragma unroll 8
                     for (uint32_t i = q; i < p.experts; i += 16u)
-                        mine[i] = -(mine[i] * inv_sum) * dot;
+                        mine[i] *= rest;
                 }
             }
         } else {
             // s and 1 - s from one exponential, in 64 bits: scores too small for 32 still share the weight
             const double x = exp64_neg(-(double)fabsf(l)), one = reciprocal64(1.0 + x);
-            double s64 = live ? (l >= 0.0f ? one : x * one) : 0.0;
-            const float slope = (float)(l >= 0.0f ? x * one : one);
+            double s = live ? (l >= 0.0f ? one : x * one) : 0.0;
+            const double slope = l >= 0.0f ? x * one : one;
             if (l != l)
-                s64 = (double)l;
-            float s = (float)s64, ds = d;
+                s = (double)l;
             if (p.normalise) {
-                const double total = row_sum(s64);
+                const double total = row_sum(s);
                 if (total != 0.0) {
-                    s = (float)(s64 / total);
-                    ds = d - row_sum(d * s);
+                    s /= total;
+                    d -= row_sum(d * s);
                 }
             }
-            grad = ds * s * slope;
+            grad = (float)(d * s * slope);
         }
         exchange();
         if (live && t0 + row < p.tokens)

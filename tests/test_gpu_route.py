@@ -254,3 +254,65 @@ def test_backward_of_the_forward_is_the_difference_quotient(softmax, normalise):
 
         # about 100 terms of order 1, some 30 roundings each, and t^2
         assert abs((loss(t) - loss(-t)) / (2 * t) - (g * u).sum()) <= 100 * 30 * ref.U32 + 1e-6
+
+
+def check_backward_in_64_bits(dw, idx, x, bf16, softmax, normalise, got):
+    """Half a step of the result's type, however much the formula's differences cancel: everything before it is in 64
+    bits (an exponential's argument of up to 2^11 is off by 2^-53 of its size, some 30 roundings besides: 2^-40 of the
+    terms' magnitudes).  Softmax over all experts: its fp32 exponentials are off by u, half a step for each unit of
+    their arguments and two for their own; so is a result, and by u of sum_i s_i |d_e - d_i|, what its difference is
+    the sum of; an unchosen expert's takes two more roundings."""
+    want, mag = ref.route_backward(dw, idx, x, softmax, normalise, 2.5)
+    steps, more = ref.U32, 0.0
+    if softmax and not normalise:
+        u = ref.U32 * (float(x.max() - x.min()) + 2)
+        d = np.zeros(x.shape)
+        for t, row in enumerate(idx):
+            for j, e in enumerate(row):
+                if e >= 0:
+                    d[t, e] = 2.5 * float(dw[t, j])
+        s = ref.scores(x, True)
+        steps, more = 3 * ref.U32 + 2 * u, u * s * (s[:, None, :] * np.abs(d[:, :, None] - d[:, None, :])).sum(2)
+    bound = ((ref.UB16 + steps) if bf16 else steps) * (1 + 2.0 ** -10) * np.abs(want) + more + 2.0 ** -40 * mag + 2.0 ** -133
+    err = np.abs(got - want)
+    assert np.all(err <= bound), f"off by {np.max(err / bound):.2f} of the bound"
+
+
+@pytest.mark.parametrize("E,k", [(8, 1), (8, 2), (64, 2), (100, 6), (256, 8), (512, 16), (64, 17), (300, 33)])
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("normalise", [0, 1])
+def test_backward_whose_differences_cancel(E, k, softmax, normalise):
+    """Gradients that are nearly equal for all chosen experts, and experts that take nearly all of the weight: d - dot
+    is a small difference of large numbers."""
+    say("route backward cancelling", E, k, softmax, normalise)
+    rng = np.random.default_rng(E + k)
+    for n, (bf16, spread, lead) in enumerate([(False, 1e-3, 0.0), (False, 1e-6, 0.0), (False, 1.0, 9.0), (False, 1.0, 16.0),
+                                              (True, 1e-3, 0.0), (True, 1.0, 9.0)]):
+        x, _ = make(E + k + n, 37, E, bf16)
+        x[np.arange(37), rng.integers(0, E, 37)] += np.float32(lead)
+        x = ref.round_bf16(x) if bf16 else x
+        idx, _ = ref.route(x, None, k, 1, 1, softmax, normalise, 2.5)
+        idx[rng.random(idx.shape) < 0.02] = -1
+        dw = (1 + spread * rng.standard_normal((37, k))).astype(np.float32)
+        check_backward_in_64_bits(dw, idx, x, bf16, softmax, normalise, run_backward(dw, idx, x, bf16, softmax, normalise))
+
+
+@pytest.mark.parametrize("k", [2, 20])
+@pytest.mark.parametrize("softmax", [False, True])
+@pytest.mark.parametrize("normalise", [0, 1])
+def test_backward_shows_nan_in_its_own_token(k, softmax, normalise):
+    say("route backward nan", k, softmax, normalise)
+    x, _ = make(5, 6, 64, False)
+    idx, _ = ref.route(x, None, k, 1, 1, softmax, normalise, 2.5)
+    dw = np.random.default_rng(1).standard_normal((6, k)).astype(np.float32)
+    clean = run_backward(dw, idx, x, False, softmax, normalise)
+    xn, dn = x.copy(), dw.copy()
+    xn[1, idx[1, 1]] = np.nan
+    if softmax:
+        xn[2, idx[2, 0]] = np.inf
+    dn[4, 1] = np.nan
+    got = run_backward(dn, idx, xn, False, softmax, normalise)
+    for t in (1, 4) + ((2,) if softmax else ()):
+        assert np.isnan(got[t, idx[t, 1 if t != 2 else 0]]), t
+    for t in (0, 3, 5):
+        assert np.array_equal(got[t], clean[t])
