@@ -52,8 +52,8 @@ typedef enum {
  * of the inputs, one write of the outputs, one launch.
  *
  *   h    = RN_t(RN(x + residual)), t the type in_dtype (h = x without residual)
- *   rstd = RN(1 / sqrt(sum h^2 / hidden + eps))   (the sum in 64 bits, so that
- *          its order does not show)
+ *   rstd = RN(1 / sqrt(sum h^2 / hidden + eps))   (in 64 bits, the order of the
+ *          sum fixed by hidden)
  *   y    = RN(RN(h * rstd) * weight)              (fp32)
  *   codes and scales of y as tk_cast_fp8 makes them from fp32 rows.
  * A row of zeros has codes and scales of zero (UE8M0: byte 0); a NaN or an

@@ -133,14 +133,20 @@ __device__ __forceinline__ float read_lane(float v, int lane)
     return as_float(__builtin_amdgcn_readlane(as_uint(v), lane));
 }
 
-// sum over all 64 lanes (every lane active), in a fixed order
+// sum over each row of 16 lanes, in every lane of it (every lane active), in a fixed order
 template <typename T>
-__device__ __forceinline__ T wave_sum(T v)
+__device__ __forceinline__ T row_sum(T v)
 {
     v = dpp_add<0xB1>(v);  // quad_perm [1,0,3,2]: lane ^ 1
     v = dpp_add<0x4E>(v);  // quad_perm [2,3,0,1]: lane ^ 2
     v = dpp_add<0x141>(v); // row_half_mirror
-    v = dpp_add<0x140>(v); // row_mirror: every lane holds its row's sum
+    return dpp_add<0x140>(v); // row_mirror
+}
+// ... over all 64 lanes
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v)
+{
+    v = row_sum(v);
     return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
 }
 
@@ -177,9 +183,13 @@ constexpr int kGroupLds = 2;   // any other width: the slots' maxima meet in LDS
 
 // One row per `waves` waves: step s of wave w of a row is slots
 // (s * waves + w) * 64 .. + 63, a lane holding 8 columns of each of its S steps.
+// Of rows of up to 16 steps each step's sum of squares is taken by itself, since
+// there S goes by the number of rows too: squares of fp32 fill 48 bits, so that
+// another order of their sum can show in 64.
 template <bool F32, int S, int GM, int SFMT, int MAXT>
 __global__ __launch_bounds__(MAXT) void rmsnorm_cast_kernel(NormParams p)
 {
+    constexpr int P = S <= 2 ? S : 1;
     __shared__ double part_sum[2][16]; // by the parity of the pass, so that one barrier a pass is enough
     __shared__ uint32_t part_max[2][16];
     extern __shared__ uint32_t dyn[]; // kGroupLds: each row's slot maxima, then its groups' multipliers
@@ -188,6 +198,8 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_cast_kernel(NormParams p)
     const uint32_t rows = p.waves == 1 ? blockDim.x / kWaveSize : 1u; // rows of this workgroup
     const uint32_t part = p.waves == 1 ? 0u : wib;
     const uint32_t row_in = p.waves == 1 ? wib : 0u;
+    const bool by_step = P > 1 && P * p.waves <= 16u; // else a wave's steps together
+    const uint32_t parts = by_step ? P * p.waves : p.waves;
     uint32_t parity = 0;
     // rows past the grid (a launch holds fewer than 2^32 work-items) take further passes
     for (uint32_t first = blockIdx.x * rows; first < p.n; first += gridDim.x * rows, parity ^= 1u) {
@@ -197,9 +209,10 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_cast_kernel(NormParams p)
         const size_t row_slot = (size_t)row * slots;
 
         float v[S][8], w[S][8];
-        double sum = 0.0;
+        double sums[P] = {};
     #pragma unroll
         for (int s = 0; s < S; ++s) {
+            double& sum = sums[s % P];
             const uint32_t slot = ((uint32_t)s * p.waves + part) * kWaveSize + lane;
     #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -229,14 +242,18 @@ __global__ __launch_bounds__(MAXT) void rmsnorm_cast_kernel(NormParams p)
                     sum = __builtin_fma((double)v[s][j], (double)v[s][j], sum);
             }
         }
-        sum = wave_sum(sum);
+        double sum = wave_sum(by_step ? sums[0] : sums[0] + (P > 1 ? sums[P - 1] : 0.0));
         if (p.waves > 1) {
             if (lane == 0)
                 part_sum[parity][wib] = sum;
+            if (by_step) {
+                sum = wave_sum(sums[P - 1]);
+                if (lane == 0)
+                    part_sum[parity][p.waves + wib] = sum;
+            }
             __syncthreads();
-            sum = 0.0;
-            for (uint32_t i = 0; i < p.waves; ++i)
-                sum += part_sum[parity][i];
+            const uint32_t i = lane & 15u;
+            sum = row_sum(i < parts ? part_sum[parity][i] : 0.0); // steps past the row's end are zero, too
         }
         const float rstd = (float)rsqrt64(__builtin_fma(sum, p.inv_hidden, p.eps));
         if (valid && p.rstd && part == 0 && lane == 0)

@@ -350,3 +350,51 @@ def test_backward_without_dweight_of_any_width():
         want, _ = run_backward(dy, h, w, rstd, dres, True)
         got, _ = run_backward(dy, h, w, rstd, dres, True, dweight=False)
         assert np.array_equal(got, want), (n, hidden)
+
+
+def border_rows(hidden):
+    """fp32 rows whose sums of squares lie within a few units of the 64-bit last place of where 1/rms rounds to the next
+    fp32 number, and differ by four of those units with the order of the sum: eight squares just below 2^-53 count
+    beside each other, and not one by one beside a 1."""
+    steps = -(-hidden // 512)
+    half = (steps + 1) // 2
+    r = np.float32(np.sqrt(hidden / 1.4))
+    mid = (float(r) + float(np.nextafter(r, np.float32(0)))) / 2
+    rows = np.zeros((49, hidden), np.float32)
+    for j in range(49):
+        rows[j, 0] = 1
+        rows[j, half * 512:half * 512 + 8] = np.nextafter(np.float32(2.0 ** -26.5), np.float32(0))
+        rest = hidden / mid ** 2 - 1 + (j - 24 - 2) * 2.0 ** -52
+        for i in range(3):  # what is left of the sum, by squares of fp32 numbers
+            a = np.float32(np.sqrt(rest))
+            if float(a) ** 2 > rest:
+                a = np.nextafter(a, np.float32(0))
+            rows[j, 512 + 8 * i] = a
+            rest -= float(a) ** 2
+    return rows
+
+
+@pytest.mark.parametrize("hidden", [2560, 7168, 8192])
+def test_norm_rows_do_not_depend_on_their_number_at_a_rounding_border(hidden):
+    say("norm batch border", hidden)
+    x = border_rows(hidden)
+    w = np.ones(hidden, np.float32)
+    few = run_norm(x, None, w, False, 0.0, 0, 0)
+    many = run_norm(np.tile(x, (21, 1)), None, w, False, 0.0, 0, 0)
+    # the sums' last bits decide on the way to fp32: both neighbours appear
+    assert len(np.unique(few["rstd"])) == 2
+    for m in few:
+        assert np.array_equal(np.tile(few[m], (21,) + (1,) * (few[m].ndim - 1)), many[m]), m
+
+
+@pytest.mark.parametrize("hidden", [2304, 7168, 12288])
+def test_norm_fp32_rows_of_many_magnitudes_do_not_depend_on_their_number(hidden):
+    say("norm batch fp32", hidden)
+    rng = np.random.default_rng(hidden)
+    x = (rng.standard_normal((1100, hidden)) * 2.0 ** rng.integers(-40, 40, (1100, hidden))).astype(np.float32)
+    w = (1 + 0.25 * rng.standard_normal(hidden)).astype(np.float32)
+    whole = run_norm(x, None, w, False, 1e-6, 128, 0)
+    for lo, hi in ((0, 1), (600, 1100)):
+        part = run_norm(x[lo:hi], None, w, False, 1e-6, 128, 0)
+        for m in part:
+            assert np.array_equal(part[m], whole[m][lo:hi]), m
