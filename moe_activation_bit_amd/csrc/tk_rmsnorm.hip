@@ -819,20 +819,15 @@ tk_status tk_rmsnorm_cast_fp8(const void* x, const void* residual, tk_dtype in_d
     const dim3 grid(blocks < kMaxBlocks ? blocks : kMaxBlocks), block(rows * p.waves * kWaveSize);
     const size_t lds = (size_t)rows * (p.q.slots + p.q.groups_row) * 4u;
     hipStream_t s = static_cast<hipStream_t>(stream);
-#define TK_NORM(SS)                                                                      \
-    case SS:                                                                             \
-        if (block.x <= 256)                                                              \
-            f32 ? launch_norm_gm<true, SS, 256>(gm, sp.kind, p, grid, block, lds, s)      \
-                : launch_norm_gm<false, SS, 256>(gm, sp.kind, p, grid, block, lds, s);    \
-        else                                                                             \
-            f32 ? launch_norm_gm<true, SS, 1024>(gm, sp.kind, p, grid, block, lds, s)     \
-                : launch_norm_gm<false, SS, 1024>(gm, sp.kind, p, grid, block, lds, s);   \
-        break;
-    switch (S) {
-        TK_NORM(1)
-        TK_NORM(2)
-        TK_NORM(4)
-    }
+#define TK_NORM(SS, T)                                                          \
+    f32 ? launch_norm_gm<true, SS, T>(gm, sp.kind, p, grid, block, lds, s)      \
+        : launch_norm_gm<false, SS, T>(gm, sp.kind, p, grid, block, lds, s)
+    if (S == 4) // more than 32 steps: nine waves or more
+        TK_NORM(4, 1024);
+    else if (S == 2)
+        block.x <= 256 ? (TK_NORM(2, 256)) : (TK_NORM(2, 1024));
+    else
+        block.x <= 256 ? (TK_NORM(1, 256)) : (TK_NORM(1, 1024));
 #undef TK_NORM
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }

@@ -162,3 +162,9 @@ def test_gemv_empty_and_unsupported():
     assert gemv(tokens=0, x_group=32, x_scale_fmt=1) == OK
     for fmt in (tk.TK_SCALE_FP32_COLMAJOR, tk.TK_SCALE_UE8M0_COLMAJOR, tk.TK_SCALE_UE8M0_PACKED):
         assert gemv(scale_fmt=fmt) == UNSUPPORTED and gemv(x_scale_fmt=fmt) == UNSUPPORTED
+
+
+def test_no_norm_kernel_that_no_call_reaches():
+    """Four steps a wave means more than 32 of them in a row, so nine waves or more: no form for 256 threads."""
+    names = set(re.findall(rb"rmsnorm_cast_kernelILb[01]ELi(\d)ELi\dELi\dELi(\d+)EE", open(tk.LIB_PATH, "rb").read()))
+    assert names == {(b"1", b"256"), (b"1", b"1024"), (b"2", b"256"), (b"2", b"1024"), (b"4", b"1024")}
