@@ -316,3 +316,52 @@ def test_backward_shows_nan_in_its_own_token(k, softmax, normalise):
         assert np.isnan(got[t, idx[t, 1 if t != 2 else 0]]), t
     for t in (0, 3, 5):
         assert np.array_equal(got[t], clean[t])
+
+
+# With the shapes above every form of the kernels: 64 experts by eight and by four tokens a wave, the compiled-in counts
+# and the others in one to four lists a lane, each with top-8 and another k, and one token a wave at every 64 experts.
+MORE_SHAPES = [
+    (64, 8, 1, 1), (64, 3, 1, 1), (64, 8, 8, 4), (64, 8, 4, 2), (64, 8, 16, 16), (64, 12, 1, 1), (64, 5, 2, 1),
+    (33, 8, 1, 1), (100, 8, 1, 1), (128, 6, 1, 1), (128, 8, 8, 2), (160, 8, 1, 1), (192, 8, 1, 1), (192, 6, 8, 4),
+    (200, 8, 1, 1), (200, 6, 1, 1), (256, 6, 1, 1), (256, 6, 8, 4), (256, 6, 8, 8), (300, 6, 1, 1), (384, 6, 1, 1),
+    (384, 8, 8, 4), (500, 8, 1, 1), (500, 6, 1, 1), (512, 6, 1, 1), (512, 6, 16, 8), (100, 20, 1, 1), (150, 20, 1, 1),
+    (300, 17, 1, 1), (384, 17, 1, 1), (448, 17, 1, 1), (40, 8, 20, 10), (12, 8, 1, 1), (8, 8, 4, 4),
+]
+
+
+@pytest.mark.parametrize("E,k,ng,tg", MORE_SHAPES)
+@pytest.mark.parametrize("softmax", [False, True])
+def test_route_every_form(E, k, ng, tg, softmax):
+    say("route every form", E, k, ng, tg, softmax)
+    for n, (T, bf16, with_bias, normalise, masked) in enumerate([
+            (1, False, True, 1, 0.0), (75, False, False, 0, 0.0), (66, True, True, 1, 0.2), (35, False, True, 0, 0.95),
+            (50, True, False, 1, 0.5)]):
+        x, bias = make(E * 1000 + k * 10 + n, T, E, bf16, masked)
+        b = bias if with_bias else None
+        check_route(x, b, k, ng, tg, softmax, normalise, run_route(x, bf16, b, k, ng, tg, softmax, normalise))
+    # ties (of all, and of a few values), empty rows, one expert left, NaN and infinities
+    rng = np.random.default_rng(E + k)
+    x, bias = make(E + k, 40, E, False)
+    x[0], x[1], x[2] = 0.0, -np.inf, -np.inf
+    x[2, E - 1] = 3.0
+    x[3:20] = rng.integers(-2, 3, (17, E))
+    x[20:30][rng.random((10, E)) < 0.9] = -np.inf
+    x[30, E // 2], x[31, 0] = np.nan, np.inf
+    x[32] = 40 + rng.standard_normal(E)
+    x[33] = -300 - 50 * rng.random(E)
+    for b in (None, np.zeros(E, np.float32), bias):
+        check_route(x, b, k, ng, tg, softmax, 1, run_route(x, False, b, k, ng, tg, softmax, 1))
+
+
+@pytest.mark.parametrize("E,k,ng,tg", [(64, 8, 1, 1), (64, 8, 8, 4), (64, 6, 1, 1), (256, 8, 8, 4), (512, 8, 16, 8), (160, 6, 8, 3),
+                                       (96, 4, 3, 2), (100, 8, 1, 1), (300, 20, 1, 1)])
+@pytest.mark.parametrize("spread", [0, 2.0 ** -27, 2.0 ** -24, 2.0 ** -20, 2.0 ** -16])
+@pytest.mark.parametrize("softmax", [False, True])
+def test_route_scores_that_nearly_tie(E, k, ng, tg, spread, softmax):
+    say("route near ties of either score", E, k, ng, tg, spread, softmax)
+    for seed in range(6):
+        rng = np.random.default_rng(E + k + seed)
+        x = np.repeat((2 * rng.standard_normal((1, E))).astype(np.float32), 11, 0)
+        s = ref.scores(x[:1], softmax)[0]
+        bias = (0.7 - s + spread * rng.standard_normal(E)).astype(np.float32)
+        check_route(x, bias, k, ng, tg, softmax, 1, run_route(x, False, bias, k, ng, tg, softmax, 1))
