@@ -210,3 +210,76 @@ def test_weights_from_the_cast():
         wv = ref.fp4_values(oc.reshape(E, out, -1), os_.reshape(E, out, -1), sfmt == UE8M0)
         want, mag = ref.gemv(ref.x_values(xo, xso.reshape(tokens, -1), "fp8"), idx, k, 0, wv)
         check(y.cpu().numpy(), False, want, mag, inner, False)
+
+
+def want_on_gpu(xk, x, xs, idx, k, slots, codes, scales, u8):
+    """ref.gemv's results by 64-bit products on the GPU, an expert at a time."""
+    xv, lut = up(ref.x_values(x, xs, xk)), up(ref.E2M1)
+    rows = up(idx.reshape(-1))
+    out, mag = (torch.zeros((len(rows), codes.shape[1]), dtype=torch.float64, device=DEV) for _ in range(2))
+    for e in range(codes.shape[0]):
+        mine = torch.nonzero(rows == e)[:, 0]
+        if len(mine):
+            c = up(codes[e]).to(torch.int64)
+            w = torch.stack([lut[c & 15], lut[c >> 4]], -1).reshape(codes.shape[1], -1)
+            sc = up(ref.e8m0_value(scales[e]) if u8 else scales[e].astype(np.float64))
+            w = (w.reshape(*sc.shape, -1) * sc[..., None]).reshape(w.shape).t().contiguous()
+            v = xv[mine if slots else mine // k]
+            out[mine], mag[mine] = v @ w, v.abs() @ w.abs()
+    return out.cpu().numpy(), mag.cpu().numpy()
+
+
+# Launches of 2048 workgroups and more, whose waves go through two tiles of weight rows, and of 4096, four: every kind of
+# activation and of scale, whole steps of 256 columns and others, rows of weights that end inside a wave's tiles,
+# one pass over an expert's rows and several, x rows that stay in LDS from tile to tile and ones staged again for each.
+TILED = [  # as CASES; experts of 0: one matrix for all rows
+    (40, 8, 64, 4100, 512, "fp8", 128, 0, True, 32), (64, 16, 64, 2050, 1024, "bf16", 0, 0, True, 32),
+    (64, 8, 64, 4099, 544, "fp8e", 32, 1, True, 32), (48, 8, 64, 4097, 768, "fp8", 128, 0, False, 128),
+    (40, 8, 32, 4101, 1280, "bf16", 0, 1, False, 0), (9, 64, 64, 2077, 2560, "fp8", 0, 0, True, 32),
+    (200, 4, 16, 8200, 288, "fp8", 0, 0, True, 0), (33, 16, 64, 2100, 256, "fp8e", 0, 0, False, 128),
+    (32, 8, 64, 4096, 1024, "fp8e", 128, 0, True, 32), (20, 16, 64, 2049, 512, "fp8", 256, 0, True, 64),
+    (512, 1, 0, 8210, 1280, "fp8", 128, 0, True, 32), (272, 1, 0, 8196, 4384, "bf16", 0, 0, True, 32),
+    (272, 1, 0, 8190, 4608, "fp8", 128, 0, True, 32), (600, 1, 0, 7000, 640, "fp8e", 32, 0, False, 128),
+]
+
+
+@pytest.mark.parametrize("case", TILED, ids=str)
+def test_several_tiles_a_wave(case):
+    tokens, k, E, out, inner, xk, xg, slots, u8, group = case
+    say("gemv tiles", case)
+    for exact in (True, False):
+        x, xs, idx, codes, scales = make(out + inner, tokens, k, max(E, 1), out, inner, xk, xg, slots, u8, group, exact, dense=not E)
+        if E:
+            idx[0], idx[1, 0], idx[tokens // 2:tokens // 2 + 3] = -1, E, 5 % E  # absent, out of range, crowded
+        chosen = np.zeros((tokens, 1), np.int32) if idx is None else idx
+        want, mag = want_on_gpu(xk, x, xs, chosen, k, slots, codes, scales, u8)
+        for out_bf16 in (False, True):
+            got = run(xk, x, xs, xg, idx, tokens, k, slots, codes, scales, u8, group, out_bf16)
+            check(got, out_bf16, want, mag, inner, exact)
+            assert not got[chosen.reshape(-1) < 0].any()
+
+
+@pytest.mark.parametrize("xk,xg", [("bf16", 0), ("fp8", 128), ("fp8", 0), ("fp8e", 32)])
+@pytest.mark.parametrize("u8,group,inner", [(True, 32, 2048), (True, 128, 2048), (False, 128, 2048), (True, 32, 2016), (False, 0, 2016)])
+def test_rows_do_not_depend_on_the_batch_however_the_columns_are_shared(xk, xg, u8, group, inner):
+    """One token: four waves share a row's columns.  Two: two do.  Sixteen and 40: one wave takes them all, two tiles one
+    after the other.  The parts and their order stay."""
+    say("gemv batch and waves", xk, xg, u8, group, inner)
+    E, out, k, T = 64, 2048, 8, 40
+    xg = xg if xg == 0 or inner % xg == 0 else 0
+    x, xs, idx, codes, scales = make(inner + group, T, k, E, out, inner, xk, xg, 0, u8, group, False)
+    idx[39] = idx[3]
+    cd, sd = up(codes), up(scales)
+
+    def rows(lo, hi):
+        y = torch.empty(((hi - lo) * k, out), device=DEV)
+        xd = up(x[lo:hi].view(np.int16)) if xk == "bf16" else up(x[lo:hi])
+        rc = tk.tk_expert_gemv_fp4(xd, None if xs is None else up(xs[lo:hi]), tk.TK_DTYPE_BF16 if xk == "bf16" else tk.TK_DTYPE_FP8,
+                                   UE8M0 if xk == "fp8e" else FP32, xg, up(idx[lo:hi]), hi - lo, k, 0, cd, sd,
+                                   UE8M0 if u8 else FP32, group, E, out, inner, tk.TK_DTYPE_FP32, y)
+        assert rc == OK, tk.tk_status_str(rc)
+        return y.cpu().numpy()
+
+    whole = rows(0, T)
+    for lo, hi in ((0, 1), (17, 18), (39, 40), (3, 5), (8, 12), (16, 32)):
+        assert np.array_equal(rows(lo, hi).view(np.uint32), whole[lo * k:hi * k].view(np.uint32)), (lo, hi)
