@@ -180,8 +180,11 @@ tk_status tk_route_backward(const float* dweight, const int32_t* topk_idx, const
  *
  * with 4-bit weights: W[e][o][c] = codes * scale, as tk_cast_fp4 writes them
  * from bf16 or fp32 rows [experts*out_features, in_features] with a row-major
- * scale_fmt.  Products and sums in fp32 (each weight and activation enters
- * exactly), rounded once to out_dtype.  A chosen expert's weights are read once
+ * scale_fmt.  Products and sums in fp32, rounded once to out_dtype.  Codes with
+ * UE8M0 scales enter as bf16 numbers, which hold every weight, and every
+ * activation down to 2^-133: what an E4M3 code has below that under the scale
+ * bytes 0, 1 and 2 is rounded away (values of 2^128 and more are infinite, as in
+ * fp32).  A chosen expert's weights are read once
  * for its rows together, up to 16 at a time: made for a step of decoding, a few
  * rows an expert.
  *

@@ -107,9 +107,9 @@ constexpr uint32_t kOwnLds = kThreads / kWaveSize * (kTile * 8 + kTile * 128 + k
 
 // Matrix instructions on 16 weight rows at a time, for up to 16 of the rows that
 // chose the expert.  Codes and FP8 activations become bf16 in
-// registers, with their UE8M0 scales on the way: both are exact (two and four
-// significant bits), and the products and sums of the 16x16x32 bf16
-// instructions are those of fp32.  (The E2M1 x E4M3 instruction would take the
+// registers, with their UE8M0 scales on the way: two and four significant bits,
+// exact (but for activations below 2^-133, bf16's smallest step), and the
+// products and sums of the 16x16x32 bf16 instructions are those of fp32.  (The E2M1 x E4M3 instruction would take the
 // codes as they are, but drops what lies 2^-14 below the largest product of a
 // step: random E4M3 bytes gave sums off by up to 7.7e-5 of their terms'
 // magnitude, where the bf16 instructions were exact.)

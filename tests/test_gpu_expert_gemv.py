@@ -283,3 +283,22 @@ def test_rows_do_not_depend_on_the_batch_however_the_columns_are_shared(xk, xg, 
     whole = rows(0, T)
     for lo, hi in ((0, 1), (17, 18), (39, 40), (3, 5), (8, 12), (16, 32)):
         assert np.array_equal(rows(lo, hi).view(np.uint32), whole[lo * k:hi * k].view(np.uint32)), (lo, hi)
+
+
+@pytest.mark.parametrize("byte", [0, 1, 2, 3, 4, 100, 254])
+def test_activations_at_the_ends_of_bf16(byte):
+    """FP8 activations with UE8M0 scales are taken as bf16 numbers: exact but for what lies below 2^-133, half of whose
+    steps are rounded to even, or past the largest number, which fp32 does not hold either."""
+    say("gemv activations", byte)
+    out, inner = 16, 128
+    code = np.array([c for c in range(256) if c & 127 != 127], np.uint8)
+    x = np.zeros((len(code), inner), np.uint8)
+    x[:, 37] = code
+    scale = 247 - max(0, byte - 60)  # of the weights, 1 by their codes: results between 2^-80 and 2^80
+    got = run("fp8e", x, np.full((len(code), 1), byte, np.uint8), 0, None, len(code), 1, 0, np.full((1, out, inner // 2), 0x22, np.uint8),
+              np.full((1, out, inner // 32), scale, np.uint8), True, 32, False)
+    v = ref.e4m3_values()[code] * 2.0 ** (byte - 127)
+    near = np.round(v * 2.0 ** 133) * 2.0 ** -133
+    assert byte > 2 or (near != v).any()
+    want = np.where(np.abs(v) < 2.0 ** 128, near * 2.0 ** (scale - 127), np.copysign(np.inf, v)).astype(np.float32)
+    assert np.array_equal(got, np.repeat(want[:, None], out, 1) + np.float32(0))
