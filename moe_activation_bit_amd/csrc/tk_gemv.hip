@@ -418,6 +418,9 @@ __global__ __launch_bounds__(kThreads, PART == 2 ? 3 : 4) void gemv_fp4_kernel(G
                     for (int h = 0; h < 2; ++h) {
                         if (h)
                             __builtin_amdgcn_sched_barrier(0);
+                        // past the row's end there is no scale, and zero times an infinite one would be NaN (wave-uniform)
+                        if (PART && !FAST && h && (b0 + c0 + t) * kStep + 128u >= p.in_features)
+                            break;
                         // only the exponent is looked at: 0 is 2^-127, 255 NaN
                         const float s = as_float((((h ? sb2.y : sb2.x) >> (8u * q)) & 255u) << 23);
                         const v4u wh = h ? *w_get4 : *w_get;

@@ -302,3 +302,29 @@ def test_activations_at_the_ends_of_bf16(byte):
     assert byte > 2 or (near != v).any()
     want = np.where(np.abs(v) < 2.0 ** 128, near * 2.0 ** (scale - 127), np.copysign(np.inf, v)).astype(np.float32)
     assert np.array_equal(got, np.repeat(want[:, None], out, 1) + np.float32(0))
+
+
+@pytest.mark.parametrize("inner", [32, 96, 128, 384, 640, 256, 512])
+def test_infinite_scales_of_rows_that_end_inside_a_step(inner):
+    """An infinite fp32 scale makes infinities of its products, and no NaN of the columns past a row's end."""
+    say("gemv infinite scales", inner)
+    out, inf = 20, np.float32(np.inf)
+    codes = np.full((1, out, inner // 2), 0x22, np.uint8)  # every weight 1
+    codes[0, 1::2] = 0xAA                                  # or -1
+    sign = np.where(np.arange(out) % 2, -1.0, 1.0)
+    one8, one16 = np.full((3, inner), 0x38, np.uint8), ref.bf16_bits(np.ones((3, inner), np.float32))
+    for group in (0, 128) if inner % 128 == 0 else (0,):
+        scales = np.ones((1, out, inner // (group or inner)), np.float32)
+        scales[0, 4:, -1] = inf
+        want = np.tile(np.where(np.arange(out) < 4, sign * inner, sign * inf), (3, 1)).astype(np.float32)
+        for xk, x, xs in (("bf16", one16, None), ("fp8", one8, np.ones((3, 1), np.float32)), ("fp8e", one8, np.full((3, 1), 127, np.uint8))):
+            got = run(xk, x, xs, 0, None, 3, 1, 0, codes, scales, False, group, False)
+            assert np.array_equal(got, want), (xk, group)
+    if inner % 128 == 0:  # of the activations
+        xs = np.ones((3, inner // 128), np.float32)
+        xs[1, -1] = inf
+        want = np.tile(sign * inner, (3, 1)).astype(np.float32)
+        want[1] = sign * inf
+        for u8, scales in ((True, np.full((1, out, inner // 32), 127, np.uint8)), (False, np.ones((1, out, inner // 128), np.float32))):
+            got = run("fp8", one8, xs, 128, None, 3, 1, 0, codes, scales, u8, 32 if u8 else 128, False)
+            assert np.array_equal(got, want), u8
