@@ -122,8 +122,10 @@ _STATUS = tuple(TkStatus(i) for i in range(len(TkStatus)))
 def _current_stream() -> int:
     import torch
     if torch.cuda.is_initialized():
-        # the handle alone: making torch's stream object around it takes 2.9 us of a small launch's 7
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        try:  # the handle alone: making torch's stream object around it takes 2.9 us of a small launch's 7
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:  # a torch without these two, which are not of its public interface
+            pass
     return int(torch.cuda.current_stream().cuda_stream)
 
 

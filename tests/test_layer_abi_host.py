@@ -168,3 +168,14 @@ def test_no_norm_kernel_that_no_call_reaches():
     """Four steps a wave means more than 32 of them in a row, so nine waves or more: no form for 256 threads."""
     names = set(re.findall(rb"rmsnorm_cast_kernelILb[01]ELi(\d)ELi\dELi\dELi(\d+)EE", open(tk.LIB_PATH, "rb").read()))
     assert names == {(b"1", b"256"), (b"1", b"1024"), (b"2", b"256"), (b"2", b"1024"), (b"4", b"1024")}
+
+
+@pytest.mark.parametrize("gone", ["_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_the_default_stream_without_torchs_private_functions(monkeypatch, gone):
+    import types
+
+    import torch
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.delattr(torch._C, gone, raising=False)
+    assert tk._current_stream() == 77
