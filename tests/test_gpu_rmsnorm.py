@@ -398,3 +398,22 @@ def test_norm_fp32_rows_of_many_magnitudes_do_not_depend_on_their_number(hidden)
         part = run_norm(x[lo:hi], None, w, False, 1e-6, 128, 0)
         for m in part:
             assert np.array_equal(part[m], whole[m][lo:hi]), m
+
+
+@pytest.mark.parametrize("n,hidden", [(333, 1024), (1024, 1024), (512, 8192), (300, 16384), (1030, 16392), (1600, 20480),   # columns summed apart
+                                      (4099, 504), (16000, 512), (5000, 1016), (9001, 2048),                               # several rows a workgroup
+                                      (1025, 4096), (3000, 7168), (1100, 8192), (600, 12616)])                             # one
+@pytest.mark.parametrize("bf16", [True, False])
+def test_backward_dweight_within_its_roundings(n, hidden, bf16):
+    """Two roundings a product, then the longest chain of additions: up to 256 parts of the rows one after the other in
+    each, eight rows of a workgroup, 16 parts in order and 16 sums of those; or 32 or 64 parts in batches of eight."""
+    say("norm backward dweight", n, hidden, bf16)
+    dy, _, w = make(n + hidden, n, hidden, bf16, False)
+    h, _, _ = make(n + hidden + 1, n, hidden, bf16, False, 4.0)
+    rstd = ref.norm(value(h, bf16), w, 1e-6)[0].astype(np.float32)
+    _, dw = run_backward(dy, h, w, rstd, None, bf16)
+    terms = value(dy, bf16).astype(np.float64) * (value(h, bf16) * rstd.astype(np.float64)[:, None])
+    depth = 2 + max(-(-n // 256) + 8 + 16 + 16, -(-n // (32 * 8)) + 8 + 2 + 16)
+    assert np.all(np.abs(dw - terms.sum(0)) <= ref.U32 * depth * np.abs(terms).sum(0))
+    # and in norm: roundings of random terms are independent, so that their sum grows with the root of the depth
+    assert np.linalg.norm(dw - terms.sum(0)) <= ref.U32 * np.sqrt(depth) * np.linalg.norm(np.abs(terms).sum(0))
