@@ -157,7 +157,8 @@ tk_status tk_route(const void* logits, tk_dtype in_dtype, const float* bias, int
  *   sigmoid, normalised  dlogit_j = (d_j - sum_i d_i w_i) / S * s_j * (1 - s_j)
  *   softmax              dlogit_e = s_e * (d_e - sum_i d_i s_i) for every e, d_e
  *                        0 where e is not chosen
- *   softmax, normalised  dlogit_j = w_j * (d_j - sum_i d_i w_i)
+ *   softmax, normalised  dlogit_j = w_j * (d_j - sum_i d_i w_i), w the softmax
+ *                        of the chosen logits among themselves
  *   and 0 elsewhere, in 64 bits (softmax over all experts: from fp32
  *   exponentials), rounded to fp32 and from there to in_dtype.
  *

@@ -115,11 +115,14 @@ constexpr uint32_t kOwnLds = kThreads / kWaveSize * (kTile * 8 + kTile * 128 + k
 // magnitude, where the bf16 instructions were exact.)
 //
 // What bounds it is the weights' bytes (7168 -> 4096, top-8 of 8 experts for one
-// token: 24.8 us, 5.0 TB/s; 2048 -> 7168 for 16 tokens' top-8 of 64: 85.2 us, 5.2
-// TB/s; one row of a single expert, 7168 -> 4096: 8 us, a launch and the row's
-// staging), so everything else keeps out of their way.  For many rows of one
-// expert it is the staging of the rows, once for every pass and workgroup (64
-// rows of 7168 -> 4096: 23 us).  A wave reads a step's 16 x 128 bytes with two instructions of eight
+// token: 24.1 us, 5.2 TB/s, a bare read of as many bytes 19.4; 2048 -> 7168 for 16
+// tokens' top-8 of 64: 80 us, 5.5 TB/s, a bare read 64; one row of a single
+// expert, 7168 -> 4096: 8 us, a launch and the row's staging; scales of other
+// groups than 32 columns, or in fp32, are read one by one: 7168 -> 4096 with one
+// for 128 columns 29.5 us, in fp32 29.8), so everything else keeps out of their
+// way.  For many rows of one expert it is the staging of the rows, once for every
+// pass and workgroup (64 rows of 7168 -> 4096: 23 us in bf16, 25.5 in FP8).
+// A wave reads a step's 16 x 128 bytes with two instructions of eight
 // whole lines (lane l: row l / 8, 16 bytes l % 8), kAhead steps before their
 // use, and passes them through 2 KiB of LDS of its own into the instruction's
 // layout, lane (r, q) = (l & 15, l >> 4): weight row r, columns 32q.. of each

@@ -810,8 +810,9 @@ tk_status tk_rmsnorm_cast_fp8(const void* x, const void* residual, tk_dtype in_d
         p.q.gmagic = (uint32_t)(((1ull << 32) + p.q.gslots - 1) / p.q.gslots);
     }
     const uint32_t steps = (p.q.slots + kWaveSize - 1) / kWaveSize;
-    // One step a wave for rows of up to four and for launches too small to fill the chip, else two: 16384 x 7168
-    // in bf16 with every output 244 / 190 / 219 us at 1 / 2 / 4 steps, 57344 x 2048 175 / 177 / 199 us.
+    // One step a wave for rows of up to four and for launches too small to fill the chip, else two: in bf16 with every
+    // output 16384 x 7168 200 / 191 / 191 us at 1 / 2 / 4 steps, 512 x 7168 8.2 / 8.0 / 9.8, 16384 x 4096 with the
+    // stream and the codes 83.9 / 83.5 / 90.0, 57344 x 2048 178 / - / 181.
     const uint32_t S = steps_per_wave(steps, steps <= 4 || n < 512 ? 1u : 2u);
     p.waves = (steps + S - 1) / S;
     const uint32_t rows = p.waves == 1 ? 4u : 1u;
@@ -888,8 +889,10 @@ tk_status tk_rmsnorm_backward(const void* dy, const void* h, tk_dtype in_dtype, 
         const uint32_t passes = ((uint32_t)n + p.rows - 1u) / p.rows;
         parts = passes < TK_RMSNORM_PARTS ? passes : TK_RMSNORM_PARTS;
         dim3 grid(parts), block(p.rows * p.waves * kWaveSize);
-        // Whether dweight is summed beside the rows.  In bf16, so and by partial rows: 1024 x 1024 4.9 / 6.6 us, 1024 x
-        // 4096 14.7 / 12.6, 500 x 4096 9.2 / 9.5, 300 x 16384 13.9 / 19.4, 500 x 12616 21.1 / 19.6.  Beyond 16384
+        // Whether dweight is summed beside the rows: so and by partial rows, in bf16, 512 x 1024 3.7 / 6.1 us, 1024 x
+        // 1024 4.4 / 6.6, 500 x 4096 8.2 / 9.7, 512 x 8192 10.4 / 14.8, 300 x 16384 15.2 / 19.4, 2048 x 1024 14.3 / 8.1;
+        // in fp32 512 x 7168 16.3 / 21.6, 2048 x 1024 16.6 / 11.8.  Near the border the other form is up to 1.3 times as
+        // fast: bf16 1024 x 2048 10.0 / 8.7, 700 x 7168 12.9 / 15.2, fp32 640 x 4096 12.3 / 16.2.  Beyond 16384
         // columns always: a wave has no registers left for their sums (2048 x 32768 133 us, with them spilled 326).
         const bool together = (dweight && n <= 1024 && n * hidden <= (n <= 512 ? 5 << 20 : 2 << 20)) || S == 4;
 #define TK_NORM_BWD(SS)                                                      \

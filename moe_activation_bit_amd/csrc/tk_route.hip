@@ -5,9 +5,8 @@
 // Scores are computed in 64 bits and rounded once, so that the order of two
 // experts is that of their exact scores rounded to fp32 (plus the bias), and
 // does not hang on how an fp32 exponential was built.  gfx950 runs fp64
-// additions, products and FMAs at the rate of fp32's (4.8 cycles a wave against
-// 4.6, measured), so the 22 of a sigmoid cost about 3 us at 16384 tokens x 256
-// experts.
+// multiply-adds at the rate of fp32's (4.7 cycles a wave against 4.6), so the 22
+// instructions of a sigmoid cost about 3 us at 16384 tokens x 256 experts.
 //
 // route_row_kernel (k <= 16, up to 16 groups): four tokens per wave, one per
 // 16-lane row, a lane holding consecutive experts of a group as lists of eight
@@ -329,8 +328,8 @@ constexpr uint32_t kMasked = 0x007FFFFFu; // ordered(-inf): the key of a masked 
 // kept lane's halves go to two lanes of the row, in order, so that every lane
 // sorts one list.
 // Bound by its fp64 and selection arithmetic: 926 vector instructions a wave at
-// 256 experts in 8 groups, top-8, some 7.4 us of the 10.4 us that 16384 tokens
-// take (1379 and 15.7 us before MOVE, the paired reciprocals and the masks
+// 256 experts in 8 groups, top-8, some 7.4 us of the 9.7 to 10.9 us that 16384
+// tokens take (1379 and 15.7 us before MOVE, the paired reciprocals and the masks
 // looked for at once).
 template <bool BF16, int L, int FC, bool K8, bool MOVE, int RL>
 __global__ __launch_bounds__(kThreads, L <= 2 && FC > 0 ? 4 : 2) void route_row_kernel(RouteParams p)
