@@ -321,3 +321,67 @@ def test_weight_offsets_past_32_bits():
         assert tk.tk_expert_gemv_fp4(x[r // k].clone(), None, BF16, 0, 0, one, 1, k, 0, codes[e].clone(), scales[e].clone(),
                                      tk.TK_SCALE_UE8M0, 32, 1, out, inner, FP32, want) == OK
         assert torch.equal(got[r], want[0]), (r, e)
+
+
+# ---- addresses aligned to an element and no more --------------------------------------------------
+
+
+def shifted(t, by=1):
+    """A copy of t that begins `by` elements after a 256-byte boundary."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device=DEV)
+    buf[by:] = t.reshape(-1)
+    out = buf[by:].view(t.shape)
+    assert out.data_ptr() % 256 == by * t.element_size()
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k,ng,tg", [(64, 6, 1, 1), (64, 8, 8, 4), (128, 8, 1, 1), (256, 8, 8, 4), (160, 6, 1, 1), (512, 8, 1, 1), (100, 5, 1, 1), (256, 20, 1, 1)])
+def test_routing_at_any_elements_address(dtype, E, k, ng, tg):
+    say("routing, shifted", dtype, E, k, ng, tg)
+    T = 37
+    gen = torch.Generator(device=DEV).manual_seed(E + k)
+    x = (2 * torch.randn(T, E, generator=gen, device=DEV)).to(dtype)
+    bias, dw = torch.randn(E, generator=gen, device=DEV) * .1, torch.randn(T, k, generator=gen, device=DEV)
+    code = FP32 if dtype == torch.float32 else BF16
+    for softmax in (0, 1):
+        for norm in (0, 1):
+            got = []
+            for place in (lambda t: t, shifted):
+                idx, w, d = (place(torch.zeros(shape, dtype=t, device=DEV)) for shape, t in
+                             (((T, k), torch.int32), ((T, k), torch.float32), ((T, E), dtype)))
+                xs = place(x)
+                assert tk.tk_route(xs, code, place(bias), T, E, k, ng, tg, softmax, norm, 2.5, idx, w) == OK
+                assert tk.tk_route_backward(place(dw), idx, xs, code, T, E, k, softmax, norm, 2.5, d) == OK
+                got.append((idx, w, d))
+            for a, b in zip(*got):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("u8,group", [(True, 32), (True, 128), (False, 128), (False, 0)])
+@pytest.mark.parametrize("x8", [False, True])
+def test_products_at_any_elements_address(u8, group, x8):
+    say("products, shifted", u8, group, x8)
+    T, k, E, out, inner = 5, 2, 4, 70, 1024
+    gen = torch.Generator(device=DEV).manual_seed(group + x8)
+    if x8:
+        x, xs = torch.randint(0, 120, (T, inner), generator=gen, device=DEV, dtype=torch.int32).to(torch.uint8), torch.rand(T, inner // 128, generator=gen, device=DEV)
+    else:
+        x, xs = torch.randn(T, inner, generator=gen, device=DEV).to(torch.bfloat16), None
+    codes = torch.randint(0, 256, (E, out, inner // 2), generator=gen, device=DEV, dtype=torch.int32).to(torch.uint8)
+    G = inner // (group or inner)
+    sc = torch.randint(118, 124, (E, out, G), generator=gen, device=DEV, dtype=torch.int32).to(torch.uint8) if u8 else torch.rand(E, out, G, generator=gen, device=DEV)
+    idx = torch.randint(0, E, (T, k), generator=gen, device=DEV, dtype=torch.int32)
+    for dtype in (torch.bfloat16, torch.float32):
+        got = []
+        for place in (lambda t: t, shifted):
+            y = place(torch.zeros(T * k, out, dtype=dtype, device=DEV))
+            assert tk.tk_expert_gemv_fp4(x, None if xs is None else place(xs), FP8 if x8 else BF16, 0, 128 if x8 else 0, place(idx), T, k, 0,
+                                         codes, place(sc), 1 if u8 else 0, group, E, out, inner, FP32 if dtype == torch.float32 else BF16, y) == OK
+            got.append(y)
+        assert torch.equal(*got)
+        # weights at 16 bytes past a boundary, through the caches instead of past them
+        y = torch.empty_like(got[0])
+        assert tk.tk_expert_gemv_fp4(x, xs, FP8 if x8 else BF16, 0, 128 if x8 else 0, idx, T, k, 0, shifted(codes, 16), sc, 1 if u8 else 0, group,
+                                     E, out, inner, FP32 if dtype == torch.float32 else BF16, y) == OK
+        assert torch.equal(y, got[0])
