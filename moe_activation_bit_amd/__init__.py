@@ -1,11 +1,12 @@
 """Python binding of the MI355X fused SwiGLU + top-k weight + FP8/FP4 cast,
 the stand-alone cast, the top-k gating and the weighted top-k reduce, and of
 the operators of an MoE layer around them (RMS norm with FP8 output, routing,
-the experts' products with 4-bit weights).
+the experts' products with 4-bit weights; grouped products, their gradients and
+SwiGLU's from 8-bit checkpoints).
 
 Argument marshalling only: every function here forwards to the C ABI in
-``include/tk.h`` and ``include/tk_layer.h`` (library ``libtk.so`` built from ``csrc/*.hip``) under the
-same name, through the small CPython extension ``_tkpy`` (``csrc/tk_py.c``,
+``include/tk.h``, ``include/tk_layer.h`` and ``include/tk_expert.h`` (library
+``libtk.so`` built from ``csrc/*.hip``) under the same name, through the small CPython extension ``_tkpy`` (``csrc/tk_py.c``,
 a fraction of a microsecond per call where ctypes took a few).  All
 arithmetic runs in the library's HIP kernels; there is no CPU fallback, and
 calling a function whose library or extension is missing raises.
@@ -30,7 +31,8 @@ __all__ = [
     "TK_RMSNORM_PARTS", "LIB_PATH", "load_library", "load_extension",
     "tk_init", "tk_swiglu_cast_fp8", "tk_swiglu_cast_fp4", "tk_swiglu_forward", "tk_cast_fp8", "tk_cast_fp4",
     "tk_topk_gate", "tk_moe_reduce", "tk_status_str", "tk_rmsnorm_cast_fp8", "tk_rmsnorm_backward", "tk_route",
-    "tk_route_backward", "tk_expert_gemv_fp4",
+    "tk_route_backward", "tk_expert_gemv_fp4", "TK_DTYPE_FP4", "tk_expert_gemm", "tk_expert_gemm_dgrad",
+    "tk_expert_gemm_wgrad", "tk_swiglu_checkpoint_fp8", "tk_swiglu_backward",
 ]
 
 TK_SCALE_FP32 = 0
@@ -41,6 +43,7 @@ TK_SCALE_UE8M0_PACKED = 4
 TK_DTYPE_BF16 = 0
 TK_DTYPE_FP32 = 1
 TK_DTYPE_FP8 = 2
+TK_DTYPE_FP4 = 3
 TK_SCORE_SIGMOID = 0
 TK_SCORE_SOFTMAX = 1
 TK_RMSNORM_PARTS = 256
@@ -55,7 +58,8 @@ class TkStatus(enum.IntEnum):
 
 _lib: Optional[ctypes.CDLL] = None
 
-# the exported symbols and their C signatures, as declared in include/tk.h and include/tk_layer.h
+# the exported symbols and their C signatures, as declared in include/tk.h, include/tk_layer.h
+# and include/tk_expert.h
 _CAST_ARGS = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
               ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
               ctypes.c_void_p]
@@ -95,6 +99,26 @@ SIGNATURES = {
                                           ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                           ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                           ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
+    "tk_expert_gemm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int64,
+                                      ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int64,
+                                      ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                                      ctypes.c_void_p]),
+    "tk_expert_gemm_dgrad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                            ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
+    "tk_expert_gemm_wgrad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                            ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                            ctypes.c_void_p, ctypes.c_void_p]),
+    "tk_swiglu_checkpoint_fp8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                                ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_void_p,
+                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "tk_swiglu_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                          ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p]),
 }
 
 
@@ -242,6 +266,44 @@ def tk_expert_gemv_fp4(x, x_scales, x_dtype, x_scale_fmt, x_group, topk_idx, tok
     return _STATUS[(_ext or load_extension()).tk_expert_gemv_fp4(
         x, x_scales, x_dtype, x_scale_fmt, x_group, topk_idx, tokens, k, x_slots, codes, scales, scale_fmt, group_size,
         experts, out_features, in_features, out_dtype, out, stream)]
+
+
+def tk_expert_gemm(x, x_scales, x_dtype, x_scale_fmt, x_group, x_rows, row_index, expert_offsets, n_rows, w, w_scales,
+                   w_dtype, w_scale_fmt, w_group, experts, out_features, in_features, out_dtype, out,
+                   stream=None) -> TkStatus:
+    """See tk_expert_gemm in include/tk_expert.h."""
+    return _STATUS[(_ext or load_extension()).tk_expert_gemm(
+        x, x_scales, x_dtype, x_scale_fmt, x_group, x_rows, row_index, expert_offsets, n_rows, w, w_scales, w_dtype,
+        w_scale_fmt, w_group, experts, out_features, in_features, out_dtype, out, stream)]
+
+
+def tk_expert_gemm_dgrad(dy, dy_rows, row_index, expert_offsets, n_rows, w, experts, out_features, in_features,
+                         out_dtype, dx, stream=None) -> TkStatus:
+    """See tk_expert_gemm_dgrad in include/tk_expert.h."""
+    return _STATUS[(_ext or load_extension()).tk_expert_gemm_dgrad(
+        dy, dy_rows, row_index, expert_offsets, n_rows, w, experts, out_features, in_features, out_dtype, dx, stream)]
+
+
+def tk_expert_gemm_wgrad(dy, dy_rows, dy_index, x, x_scales, x_dtype, x_group, x_rows, x_index, expert_offsets, n_rows,
+                         experts, out_features, in_features, accumulate, out_dtype, dw, stream=None) -> TkStatus:
+    """See tk_expert_gemm_wgrad in include/tk_expert.h."""
+    return _STATUS[(_ext or load_extension()).tk_expert_gemm_wgrad(
+        dy, dy_rows, dy_index, x, x_scales, x_dtype, x_group, x_rows, x_index, expert_offsets, n_rows, experts,
+        out_features, in_features, accumulate, out_dtype, dw, stream)]
+
+
+def tk_swiglu_checkpoint_fp8(x, topk_weight, n, hidden, group_size, clamp_limit, scale_fmt, codes, scales, x_codes,
+                             x_scales, stream=None) -> TkStatus:
+    """See tk_swiglu_checkpoint_fp8 in include/tk_expert.h."""
+    return _STATUS[(_ext or load_extension()).tk_swiglu_checkpoint_fp8(
+        x, topk_weight, n, hidden, group_size, clamp_limit, scale_fmt, codes, scales, x_codes, x_scales, stream)]
+
+
+def tk_swiglu_backward(dy, h, h_scales, h_dtype, scale_fmt, group_size, topk_weight, n, hidden, clamp_limit, dh,
+                       dweight, y, stream=None) -> TkStatus:
+    """See tk_swiglu_backward in include/tk_expert.h."""
+    return _STATUS[(_ext or load_extension()).tk_swiglu_backward(
+        dy, h, h_scales, h_dtype, scale_fmt, group_size, topk_weight, n, hidden, clamp_limit, dh, dweight, y, stream)]
 
 
 def tk_status_str(status: int) -> str:

@@ -36,7 +36,7 @@ def _run(cmd):
 
 OBJ_DIR = os.path.join(HERE, "_build")
 TK_SOURCES = ["tk_swiglu_cast.hip", "tk_cast.hip", "tk_topk.hip", "tk_reduce.hip", "tk_pos.hip",
-              "tk_rmsnorm.hip", "tk_route.hip", "tk_gemv.hip"]
+              "tk_rmsnorm.hip", "tk_route.hip", "tk_gemv.hip", "tk_gemm.hip", "tk_gemm_q.hip", "tk_checkpoint.hip"]
 
 
 def _hip_object(src):

@@ -1,0 +1,462 @@
+// tk_gemm.hip -- the experts' matrix products in bf16 over ragged rows and
+// their gradients, behind tk_expert_gemm (bf16 operands), tk_expert_gemm_dgrad
+// and tk_expert_gemm_wgrad in include/tk_expert.h.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "tk_gemm_host.h"
+#include "tk_gemm_tile.h"
+
+namespace {
+
+using namespace tk_gemm;
+
+// The product that a launch computes, result[row][column] = sum over k:
+//   kForward  rows r of x, columns o:       x[r][k] * w[o][k]
+//   kDgrad    rows r of dy, columns c:      dy[r][k] * w[k][c]
+//   kWgrad    rows o, columns c, k a row:   dy[k][o] * x[k][c]
+constexpr int kForward = 0, kDgrad = 1, kWgrad = 2;
+
+constexpr uint32_t kDepth = 64; // k of a step: 128 bytes of a row
+
+// 8 values of a matrix instruction's lane from a tile kept [k][column]: two
+// transposing reads of four rows each
+__device__ __forceinline__ v8b read_transposed(const char* at, uint32_t pitch)
+{
+    typedef __attribute__((address_space(3))) v4s lds_v4s;
+    const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at));
+    const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4u * pitch));
+    return __builtin_bit_cast(v8b, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int KIND, int TC, int TR, int WC, int WR, bool X8>
+__global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
+{
+    constexpr uint32_t kWaves = WC * WR;
+    constexpr bool kCT = KIND != kForward, kRT = KIND == kWgrad; // kept [k][..] in memory and in LDS
+    constexpr int NC = TC / WC / 16, NR = TR / WR / 16;
+    constexpr uint32_t kBytesC = TC * kDepth * 2, kBytesR = TR * kDepth * 2;
+    constexpr int kCopiesC = (kBytesC / 1024 + kWaves - 1) / kWaves, kCopiesR = (kBytesR / 1024 + kWaves - 1) / kWaves;
+    constexpr bool kEvenC = kBytesC / 1024 % kWaves == 0, kEvenR = kBytesR / 1024 % kWaves == 0;
+    constexpr int kCodes = X8 ? TC * kDepth / 16 / (64 * kWaves) : 1; // 16-code pieces of x a thread
+    __shared__ __attribute__((aligned(1024))) char s_c[2][kBytesC];
+    __shared__ __attribute__((aligned(1024))) char s_r[2][kBytesR];
+
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1), r = lane & 15u, q = lane >> 4;
+    const uint32_t wave = uniform(threadIdx.x / kWaveSize), wc = wave % WC, wr = wave / WC;
+
+    // ---- this workgroup's tile
+    const uint32_t col_tiles = (p.cols + TC - 1) / TC;
+    uint32_t expert, row_base = 0, row0, rows, col0, depth; // result rows row0 .. row0 + rows - 1 (wgrad: of the weights)
+    if constexpr (KIND == kWgrad) {
+        const uint32_t row_tiles = (p.out_rows + TR - 1) / TR, per = row_tiles * col_tiles;
+        const uint32_t t = xcd_tile(blockIdx.x, p.experts * per);
+        if (t >= p.experts * per)
+            return;
+        expert = t / per;
+        const uint32_t in = t - expert * per;
+        row0 = in / col_tiles * TR;
+        rows = min((uint32_t)TR, p.out_rows - row0);
+        col0 = in % col_tiles * TC;
+        expert_rows(p.offsets, expert, p.n_rows, row_base, depth);
+        row_base = uniform(row_base);
+        depth = uniform(depth);
+        if (p.accumulate && depth == 0)
+            return;
+    } else {
+        Group g;
+        uint32_t t = 0;
+        if (!find_group(p.offsets, p.experts, p.n_rows, TR,
+                        [&](uint32_t total) {
+                            t = xcd_tile(blockIdx.x, total * col_tiles);
+                            return t / col_tiles;
+                        },
+                        g))
+            return;
+        // rows first: the row tiles of a few columns share their weights in the L2
+        const uint32_t in = t - g.first * col_tiles;
+        expert = g.expert;
+        row0 = g.row0 + in % g.tiles * TR;
+        rows = min((uint32_t)TR, g.rows - in % g.tiles * TR);
+        col0 = in / g.tiles * TC;
+        depth = p.depth;
+    }
+
+    // ---- where each lane's copies come from
+    // A tile kept [row][k] has 128 bytes a row; the 16 bytes c of row i lie at c ^ (i & 7), so that the 16 rows
+    // of a fragment meet in no bank.  One kept [k][column] has its columns' 32 bytes c of row k at c ^ hash(k),
+    // as the transposing reads take four rows k of 32 bytes from each of 16 lanes.
+    auto hash = [](uint32_t k) { return (k & 3u) | ((k >> 1) & 4u); };
+    const uint32_t ld_c = (KIND == kForward ? p.depth : p.cols) * (X8 ? 1u : 2u);
+    const uint32_t ld_r = (KIND == kForward ? p.depth : KIND == kDgrad ? p.depth : p.out_rows) * 2u;
+    const char* base_c = p.c; // forward and dgrad: the same for the whole wave; offset_c from there
+    uint32_t offset_c[kCopiesC];
+    const char* from_r[kCopiesR];
+    uint32_t piece_c[kCopiesC], piece_r[kCopiesR]; // [row][k]: the first k; [k][column]: the row k
+    if constexpr (KIND == kForward)
+        base_c += ((size_t)expert * p.cols + col0) * ld_c;
+    if constexpr (KIND == kDgrad)
+        base_c += (size_t)expert * p.depth * ld_c;
+    bool any_bad = false;
+    uint32_t bad = 0; // rows of the forward's and dgrad's row operand whose index names none
+#pragma unroll
+    for (int i = 0; i < kCopiesC; ++i) {
+        const uint32_t no = i * kWaves + wave;
+        if constexpr (!kCT) {
+            const uint32_t row = no * 8u + lane / 8u, k = ((lane & 7u) ^ (lane >> 3)) * 8u;
+            piece_c[i] = k;
+            offset_c[i] = min(row, p.cols - 1u - col0) * ld_c + k * 2u;
+        } else {
+            constexpr uint32_t kLanes = TC / 8; // lanes a row
+            const uint32_t k = no * (64u / kLanes) + lane / kLanes, s = lane % kLanes;
+            uint32_t col = col0 + (((s >> 1) ^ hash(k)) * 2u + (s & 1u)) * 8u;
+            col = col < p.cols ? col : 0u; // not stored
+            piece_c[i] = k;
+            offset_c[i] = (KIND == kDgrad ? k * ld_c : 0u) + col * 2u;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kCopiesR; ++i) {
+        const uint32_t no = i * kWaves + wave;
+        if constexpr (!kRT) {
+            const uint32_t row = no * 8u + lane / 8u, k = ((lane & 7u) ^ (lane >> 3)) * 8u;
+            uint32_t at = row0 + min(row, rows - 1u);
+            if (p.r_index)
+                at = (uint32_t)p.r_index[at];
+            if (at >= p.r_rows) {
+                at = 0;
+                bad |= 1u << i;
+            }
+            piece_r[i] = k;
+            from_r[i] = p.r + (size_t)at * ld_r + k * 2u;
+        } else {
+            constexpr uint32_t kLanes = TR / 8;
+            const uint32_t k = no * (64u / kLanes) + lane / kLanes, s = lane % kLanes;
+            uint32_t col = row0 + (((s >> 1) ^ hash(k)) * 2u + (s & 1u)) * 8u;
+            col = col < p.out_rows ? col : 0u;
+            piece_r[i] = k;
+            from_r[i] = p.r + col * 2u;
+        }
+    }
+    if constexpr (!kRT)
+        any_bad = __builtin_amdgcn_ballot_w64(bad != 0) != 0;
+
+    // wgrad: the source row of the expert's row k, past whose last there are zeros
+    auto source = [&](const int32_t* index, uint32_t k, uint32_t all) -> uint32_t {
+        if (k >= depth)
+            return ~0u;
+        const uint32_t at = index ? (uint32_t)index[row_base + k] : row_base + k;
+        return at < all ? at : ~0u;
+    };
+    uint32_t next_c[kCopiesC], next_r[kCopiesR], next_x[kCodes]; // the coming step's source rows
+    auto find_sources = [&](uint32_t t) {
+        if constexpr (KIND == kWgrad) {
+            if constexpr (!X8) {
+#pragma unroll
+                for (int i = 0; i < kCopiesC; ++i)
+                    next_c[i] = source(p.c_index, t * kDepth + piece_c[i], p.c_rows);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kCodes; ++i)
+                    next_x[i] = source(p.c_index, t * kDepth + (i * 64u * kWaves + threadIdx.x) / (TC / 16u), p.c_rows);
+            }
+#pragma unroll
+            for (int i = 0; i < kCopiesR; ++i)
+                next_r[i] = source(p.r_index, t * kDepth + piece_r[i], p.r_rows);
+        }
+    };
+
+    v4u codes[kCodes]; // X8: a step's codes and their scales on their way through registers
+    uint32_t code_scale[kCodes];
+    auto code_col = [&](int i) { return col0 + (i * 64u * kWaves + threadIdx.x) % (TC / 16u) * 16u; };
+
+    // Step t of both operands on its way into LDS.  Past the depth, and for rows that are none, zeros.
+    auto fetch = [&](uint32_t t, uint32_t buf) {
+        const bool whole = (t + 1u) * kDepth <= depth && !any_bad; // wave-uniform
+        if constexpr (KIND != kWgrad) {
+            const size_t step_c = kCT ? (size_t)t * kDepth * ld_c : (size_t)t * (kDepth * 2u);
+            const size_t step_r = (size_t)t * (kDepth * 2u);
+            auto each = [&](auto&& copy_c, auto&& copy_r) {
+#pragma unroll
+                for (int i = 0; i < kCopiesC; ++i)
+                    if (kEvenC || i * kWaves + wave < kBytesC / 1024)
+                        copy_c(i, s_c[buf] + (i * kWaves + wave) * 1024u);
+#pragma unroll
+                for (int i = 0; i < kCopiesR; ++i)
+                    if (kEvenR || i * kWaves + wave < kBytesR / 1024)
+                        copy_r(i, s_r[buf] + (i * kWaves + wave) * 1024u);
+            };
+            if (whole)
+                each([&](int i, char* to) { copy_to_lds(base_c + step_c, offset_c[i], to); },
+                     [&](int i, char* to) { copy_to_lds(from_r[i] + step_r, to); });
+            else
+                each(
+                    [&](int i, char* to) {
+                        copy_to_lds(t * kDepth + piece_c[i] < depth ? base_c + step_c + offset_c[i] : zeros(), to);
+                    },
+                    [&](int i, char* to) {
+                        copy_to_lds(t * kDepth + piece_r[i] < depth && !(bad >> i & 1u) ? from_r[i] + step_r : zeros(),
+                                    to);
+                    });
+        } else {
+            if constexpr (!X8) {
+#pragma unroll
+                for (int i = 0; i < kCopiesC; ++i)
+                    if (kEvenC || i * kWaves + wave < kBytesC / 1024)
+                        copy_to_lds(next_c[i] != ~0u ? base_c + offset_c[i] + (size_t)next_c[i] * ld_c : zeros(),
+                                    s_c[buf] + (i * kWaves + wave) * 1024u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kCodes; ++i) {
+                    const uint32_t col = code_col(i) < p.cols ? code_col(i) : 0u;
+                    const bool in = next_x[i] != ~0u;
+                    const size_t row = in ? next_x[i] : 0u;
+                    codes[i] = *reinterpret_cast<const v4u*>(in ? p.c + row * ld_c + col : zeros());
+                    const uint8_t* const sc = p.c_scales + row * p.c_groups;
+                    // two scales of 8 columns each, the same where a group is wider
+                    code_scale[i] = in ? sc[col / p.c_group] | (uint32_t)sc[(col + 8u) / p.c_group] << 8 : 0u;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kCopiesR; ++i)
+                if (kEvenR || i * kWaves + wave < kBytesR / 1024)
+                    copy_to_lds(next_r[i] != ~0u ? from_r[i] + (size_t)next_r[i] * ld_r : zeros(),
+                                s_r[buf] + (i * kWaves + wave) * 1024u);
+            find_sources(t + 1u);
+        }
+    };
+    // X8: the codes as bf16 numbers, with their power-of-two scales, into LDS
+    auto put_codes = [&](uint32_t buf) {
+        if constexpr (X8) {
+#pragma unroll
+            for (int i = 0; i < kCodes; ++i) {
+                const uint32_t at = i * 64u * kWaves + threadIdx.x, k = at / (TC / 16u), s = at % (TC / 16u);
+                const uint32_t word[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+                uint4 v[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float scale = as_float((code_scale[i] >> (8 * h) & 255u) << 23);
+                    v[h] = make_uint4(fp8_to_bf16<false>(word[2 * h], scale), fp8_to_bf16<true>(word[2 * h], scale),
+                                      fp8_to_bf16<false>(word[2 * h + 1], scale),
+                                      fp8_to_bf16<true>(word[2 * h + 1], scale));
+                }
+                char* const to = s_c[buf] + k * (TC * 2u) + (s ^ hash(k)) * 32u;
+                *reinterpret_cast<uint4*>(to) = v[0];
+                *reinterpret_cast<uint4*>(to + 16) = v[1];
+            }
+        }
+    };
+
+    v4f acc[NC][NR];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+            acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+    auto multiply = [&](uint32_t buf) {
+#pragma unroll
+        for (int h = 0; h < (int)kDepth / 32; ++h) {
+            v8b a[NC], b[NR];
+            const uint32_t k = 32u * h + 8u * q + (r >> 2); // the transposing reads' row
+            const uint32_t key = (r >> 2) | (q & 1u) << 2;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const uint32_t tile = wc * NC + i;
+                if constexpr (!kCT)
+                    a[i] = *reinterpret_cast<const v8b*>(s_c[buf] + (tile * 16u + r) * 128u +
+                                                         ((4u * h + q) ^ (r & 7u)) * 16u);
+                else
+                    a[i] = read_transposed(s_c[buf] + k * (TC * 2u) + (tile ^ key) * 32u + (r & 3u) * 8u, TC * 2u);
+            }
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                const uint32_t tile = wr * NR + j;
+                if constexpr (!kRT)
+                    b[j] = *reinterpret_cast<const v8b*>(s_r[buf] + (tile * 16u + r) * 128u +
+                                                         ((4u * h + q) ^ (r & 7u)) * 16u);
+                else
+                    b[j] = read_transposed(s_r[buf] + k * (TR * 2u) + (tile ^ key) * 32u + (r & 3u) * 8u, TR * 2u);
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int j = 0; j < NR; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+        }
+    };
+
+    // ---- the steps: one on its way while the one before it is multiplied
+    const uint32_t steps = (depth + kDepth - 1) / kDepth;
+    if (steps) {
+        find_sources(0);
+        fetch(0, 0);
+        put_codes(0);
+    }
+#pragma clang loop unroll(disable) // (nor peeled)
+    for (uint32_t t = 0; t < steps; ++t) {
+        copies_done<0>();
+        __syncthreads(); // step t is there, and nobody reads step t - 1 any more
+        const uint32_t buf = t & 1u;
+        if (t + 1u < steps)
+            fetch(t + 1u, buf ^ 1u);
+        multiply(buf);
+        put_codes(buf ^ 1u); // (past the last step unused: a branch here would draw the products behind it)
+    }
+
+    // ---- results: a lane has four columns of a row
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        const uint32_t row = 16u * (wr * NR + j) + r;
+        if (row >= rows)
+            continue;
+        const size_t line = ((size_t)(KIND == kWgrad ? expert * (size_t)p.out_rows : 0u) + row0 + row) * p.cols;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const uint32_t col = col0 + 16u * (wc * NC + i) + 4u * q;
+            if (col >= p.cols)
+                continue;
+            v4f v = acc[i][j];
+            if (p.out_bf16) {
+                v4b* const to = reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + line + col);
+                if (KIND == kWgrad && p.accumulate) {
+                    const v4b old = *to;
+                    v += v4f{(float)old[0], (float)old[1], (float)old[2], (float)old[3]};
+                }
+                *to = v4b{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+            } else {
+                v4f* const to = reinterpret_cast<v4f*>(static_cast<float*>(p.out) + line + col);
+                if (KIND == kWgrad && p.accumulate)
+                    v += *to;
+                *to = v;
+            }
+        }
+    }
+}
+
+// Launches the kernel with tiles of TR rows by TC columns.
+template <int KIND, int TC, int TR, int WC, int WR, bool X8 = false>
+tk_status launch(const GemmParams& p, hipStream_t s)
+{
+    const uint64_t col_tiles = ((uint64_t)p.cols + TC - 1) / TC;
+    const uint64_t most = p.n_rows < p.experts ? p.n_rows : p.experts;
+    const uint64_t row_tiles = KIND == kWgrad ? (uint64_t)p.experts * (((uint64_t)p.out_rows + TR - 1) / TR)
+                                              : p.n_rows / TR + most; // at most so many, however the rows lie
+    const uint64_t blocks = (row_tiles * col_tiles + kXcds - 1) / kXcds * kXcds;
+    if (!launchable(blocks, 64 * WC * WR))
+        return TK_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((gemm_kernel<KIND, TC, TR, WC, WR, X8>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0, s, p);
+    return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
+}
+
+} // namespace
+
+namespace tk_gemm {
+
+tk_status launch_forward(const GemmParams& p, hipStream_t s)
+{
+    const uint32_t load = p.n_rows / p.experts; // an expert's rows on average
+    if (load >= 128)
+        return launch<kForward, 256, 256, 2, 4>(p, s);
+    if (load >= 32)
+        return launch<kForward, 128, 64, 2, 2>(p, s);
+    return launch<kForward, 64, 16, 4, 1>(p, s);
+}
+
+} // namespace tk_gemm
+
+extern "C" tk_status tk_expert_gemm_dgrad(const void* dy, int64_t dy_rows, const int32_t* row_index,
+                                          const int32_t* expert_offsets, int64_t n_rows, const void* w,
+                                          int64_t experts, int64_t out_features, int64_t in_features,
+                                          tk_dtype out_dtype, void* dx, void* stream)
+{
+    const bool out_bf16 = (int)out_dtype == TK_DTYPE_BF16;
+    const RowsArgs rows = {dy_rows, row_index};
+    if (!valid_rows(rows, expert_offsets, n_rows, experts) || !valid_shape(out_features, in_features, 8) ||
+        (!out_bf16 && (int)out_dtype != TK_DTYPE_FP32))
+        return TK_ERR_INVALID_ARG;
+    if (n_rows > 0 && (!dy || !w || !dx))
+        return TK_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(dx, 16))
+        return TK_ERR_INVALID_ARG;
+    if (experts > kMaxExperts)
+        return TK_ERR_UNSUPPORTED;
+    const size_t o_bytes = (size_t)n_rows * (size_t)in_features * (out_bf16 ? 2u : 4u);
+    if (overlaps(dx, o_bytes, dy, (size_t)dy_rows * (size_t)out_features * 2u) ||
+        overlaps(dx, o_bytes, w, (size_t)experts * (size_t)out_features * (size_t)in_features * 2u) ||
+        overlaps_rows(dx, o_bytes, row_index, expert_offsets, n_rows, experts))
+        return TK_ERR_INVALID_ARG;
+    if (n_rows == 0)
+        return TK_OK;
+    GemmParams p{};
+    p.c = static_cast<const char*>(w);
+    p.r = static_cast<const char*>(dy);
+    p.r_index = row_index;
+    p.r_rows = (uint32_t)dy_rows;
+    p.offsets = expert_offsets;
+    p.n_rows = (uint32_t)n_rows;
+    p.experts = (uint32_t)experts;
+    p.cols = (uint32_t)in_features;
+    p.depth = (uint32_t)out_features;
+    p.out = dx;
+    p.out_bf16 = out_bf16;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (p.n_rows / p.experts >= 128)
+        return launch<kDgrad, 256, 256, 2, 4>(p, s);
+    return launch<kDgrad, 128, 64, 2, 2>(p, s);
+}
+
+extern "C" tk_status tk_expert_gemm_wgrad(const void* dy, int64_t dy_rows, const int32_t* dy_index, const void* x,
+                                          const void* x_scales, int x_dtype, int64_t x_group, int64_t x_rows,
+                                          const int32_t* x_index, const int32_t* expert_offsets, int64_t n_rows,
+                                          int64_t experts, int64_t out_features, int64_t in_features, int accumulate,
+                                          tk_dtype out_dtype, void* dw, void* stream)
+{
+    const bool out_bf16 = (int)out_dtype == TK_DTYPE_BF16, fp8 = x_dtype == TK_DTYPE_FP8;
+    if (!valid_rows({dy_rows, dy_index}, expert_offsets, n_rows, experts) ||
+        !valid_rows({x_rows, x_index}, expert_offsets, n_rows, experts) ||
+        !valid_shape(out_features, in_features, fp8 ? 16 : 8) || (!fp8 && x_dtype != TK_DTYPE_BF16) ||
+        (!out_bf16 && (int)out_dtype != TK_DTYPE_FP32) || (accumulate != 0 && accumulate != 1))
+        return TK_ERR_INVALID_ARG;
+    if (fp8 && (x_group < 0 || (x_group && in_features % x_group != 0)))
+        return TK_ERR_INVALID_ARG;
+    if (!dw || (n_rows > 0 && (!dy || !x || (fp8 && !x_scales))))
+        return TK_ERR_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16))
+        return TK_ERR_INVALID_ARG;
+    if (experts > kMaxExperts || (fp8 && x_group % 8 != 0))
+        return TK_ERR_UNSUPPORTED;
+    const int64_t group = fp8 && x_group ? x_group : in_features;
+    const size_t o_bytes = (size_t)experts * (size_t)out_features * (size_t)in_features * (out_bf16 ? 2u : 4u);
+    if (overlaps(dw, o_bytes, dy, (size_t)dy_rows * (size_t)out_features * 2u) ||
+        overlaps(dw, o_bytes, x, (size_t)x_rows * (size_t)in_features * (fp8 ? 1u : 2u)) ||
+        (fp8 && overlaps(dw, o_bytes, x_scales, (size_t)x_rows * (size_t)(in_features / group))) ||
+        overlaps_rows(dw, o_bytes, dy_index, expert_offsets, n_rows, experts) ||
+        overlaps_rows(dw, o_bytes, x_index, nullptr, n_rows, experts))
+        return TK_ERR_INVALID_ARG;
+    if (n_rows == 0 && accumulate)
+        return TK_OK;
+    GemmParams p{};
+    p.c = static_cast<const char*>(x);
+    p.c_scales = static_cast<const uint8_t*>(x_scales);
+    p.c_group = (uint32_t)group;
+    p.c_groups = (uint32_t)(in_features / group);
+    p.c_index = x_index;
+    p.c_rows = (uint32_t)x_rows;
+    p.r = static_cast<const char*>(dy);
+    p.r_index = dy_index;
+    p.r_rows = (uint32_t)dy_rows;
+    p.offsets = n_rows ? expert_offsets : nullptr;
+    p.n_rows = (uint32_t)n_rows;
+    p.experts = (uint32_t)experts;
+    p.cols = (uint32_t)in_features;
+    p.out_rows = (uint32_t)out_features;
+    p.out = dw;
+    p.out_bf16 = out_bf16;
+    p.accumulate = accumulate;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (fp8)
+        return launch<kWgrad, 128, 128, 2, 2, true>(p, s);
+    return launch<kWgrad, 128, 128, 2, 2>(p, s);
+}

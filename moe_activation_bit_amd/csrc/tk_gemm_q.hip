@@ -1,0 +1,437 @@
+// tk_gemm_q.hip -- the experts' matrix products of FP8 rows with FP8 or FP4
+// weights over ragged rows, and the entry point tk_expert_gemm of
+// include/tk_expert.h.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "tk_gemm_host.h"
+#include "tk_gemm_tile.h"
+
+namespace {
+
+using namespace tk_gemm;
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kDepth = 128; // k of a step and of a matrix instruction
+
+// How an operand is scaled: one scale a row (applied to the finished sum), power-of-two scales of groups of 32 k
+// or a multiple (in the instruction), fp32 scales of groups of 128 k or a multiple (on each step's sum).
+constexpr int kScaleRow = 0, kScaleMx = 1, kScaleStep = 2;
+
+struct Scales {
+    const void* at; // row-major
+    uint32_t groups;
+    uint32_t width; // kScaleMx: blocks of 32 k a group; kScaleStep: steps
+    int kind;
+    int u8;
+    int words; // kScaleMx: groups of 32 whose bytes can be read four at a time
+};
+
+struct QuantParams {
+    const char* w;
+    const char* x;
+    const int32_t* index;
+    const int32_t* offsets;
+    void* out;
+    Scales ws, xs;
+    uint32_t x_rows, n_rows, experts, cols, depth;
+};
+
+__device__ __forceinline__ float e8m0_value(uint32_t b)
+{
+    return b == 0u ? 0x1p-127f : as_float(b == 255u ? 0x7FC00000u : b << 23);
+}
+
+// W4: weights in FP4.  MX: some operand has power-of-two scales of groups.  STEP: some operand has fp32 ones.
+template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
+__global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
+{
+    constexpr uint32_t kWaves = WC * WR, kThr = 64 * kWaves;
+    constexpr int NC = TC / WC / 16, NR = TR / WR / 16;
+    constexpr uint32_t kRowC = W4 ? 64 : 128; // bytes of a weight row's step
+    constexpr uint32_t kBytesC = TC * kRowC, kBytesR = TR * 128;
+    constexpr int kCopiesC = (kBytesC / 1024 + kWaves - 1) / kWaves, kCopiesR = (kBytesR / 1024 + kWaves - 1) / kWaves;
+    constexpr bool kEvenC = kBytesC / 1024 % kWaves == 0, kEvenR = kBytesR / 1024 % kWaves == 0;
+    constexpr bool kBounded = NC * NR >= 16;
+    constexpr int kOwn = (TC + TR + kThr - 1) / kThr; // rows whose scales a thread fetches
+    __shared__ __attribute__((aligned(1024))) char s_c[2][kBytesC];
+    __shared__ __attribute__((aligned(1024))) char s_r[2][kBytesR];
+    __shared__ uint32_t s_mx[MX ? 2 : 1][MX ? TC + TR : 1];
+    __shared__ __attribute__((aligned(16))) float s_step[STEP ? 2 : 1][STEP ? TC + TR : 1];
+
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1), r = lane & 15u, q = lane >> 4;
+    const uint32_t wave = uniform(threadIdx.x / kWaveSize), wc = wave % WC, wr = wave / WC;
+
+    // ---- this workgroup's tile
+    const uint32_t col_tiles = (p.cols + TC - 1) / TC;
+    Group g;
+    uint32_t t = 0;
+    if (!find_group(p.offsets, p.experts, p.n_rows, TR,
+                    [&](uint32_t total) {
+                        t = xcd_tile(blockIdx.x, total * col_tiles);
+                        return t / col_tiles;
+                    },
+                    g))
+        return;
+    const uint32_t in = t - g.first * col_tiles;
+    const uint32_t row0 = g.row0 + in % g.tiles * TR, rows = min((uint32_t)TR, g.rows - in % g.tiles * TR);
+    const uint32_t col0 = in / g.tiles * TC, depth = p.depth;
+    const size_t w_row0 = (size_t)g.expert * p.cols + col0;
+
+    auto source = [&](uint32_t row) { // x's row for a row of the tile; x_rows or more: none
+        const uint32_t at = row0 + min(row, rows - 1u);
+        return p.index ? (uint32_t)p.index[at] : at;
+    };
+
+    // ---- where each lane's copies come from (the 16 bytes c of row i lie at c ^ (i & 7); of an FP4 row's 64 bytes
+    // at c ^ (-(i / 4) & 3): the 16 rows of a fragment meet in no bank)
+    const uint32_t ld_c = W4 ? depth / 2u : depth;
+    const char* const base_c = p.w + w_row0 * ld_c;
+    uint32_t offset_c[kCopiesC], piece_c[kCopiesC], piece_r[kCopiesR], bad = 0;
+    const char* from_r[kCopiesR];
+#pragma unroll
+    for (int i = 0; i < kCopiesC; ++i) {
+        const uint32_t no = i * kWaves + wave;
+        const uint32_t row = no * (W4 ? 16u : 8u) + (W4 ? lane >> 2 : lane >> 3);
+        const uint32_t c = W4 ? (lane & 3u) ^ (-(lane >> 4) & 3u) : (lane & 7u) ^ (lane >> 3);
+        piece_c[i] = c * (W4 ? 32u : 16u); // its first k
+        offset_c[i] = min(row, p.cols - 1u - col0) * ld_c + c * 16u;
+    }
+#pragma unroll
+    for (int i = 0; i < kCopiesR; ++i) {
+        const uint32_t row = (i * kWaves + wave) * 8u + (lane >> 3), c = (lane & 7u) ^ (lane >> 3);
+        uint32_t at = source(row);
+        if (at >= p.x_rows) {
+            at = 0;
+            bad |= 1u << i;
+        }
+        piece_r[i] = c * 16u;
+        from_r[i] = p.x + (size_t)at * depth + c * 16u;
+    }
+    const bool any_bad = __builtin_amdgcn_ballot_w64(bad != 0) != 0;
+
+    auto fetch = [&](uint32_t t, uint32_t buf) {
+        const bool whole = (t + 1u) * kDepth <= depth && !any_bad; // wave-uniform
+        const size_t step_c = (size_t)t * kRowC, step_r = (size_t)t * 128u;
+        auto each = [&](auto&& copy_c, auto&& copy_r) {
+#pragma unroll
+            for (int i = 0; i < kCopiesC; ++i)
+                if (kEvenC || i * kWaves + wave < kBytesC / 1024)
+                    copy_c(i, s_c[buf] + (i * kWaves + wave) * 1024u);
+#pragma unroll
+            for (int i = 0; i < kCopiesR; ++i)
+                if (kEvenR || i * kWaves + wave < kBytesR / 1024)
+                    copy_r(i, s_r[buf] + (i * kWaves + wave) * 1024u);
+        };
+        if (whole)
+            each([&](int i, char* to) { copy_to_lds(base_c + step_c, offset_c[i], to); },
+                 [&](int i, char* to) { copy_to_lds(from_r[i] + step_r, to); });
+        else
+            each(
+                [&](int i, char* to) {
+                    copy_to_lds(t * kDepth + piece_c[i] < depth ? base_c + step_c + offset_c[i] : zeros(), to);
+                },
+                [&](int i, char* to) {
+                    copy_to_lds(t * kDepth + piece_r[i] < depth && !(bad >> i & 1u) ? from_r[i] + step_r : zeros(), to);
+                });
+    };
+
+    // ---- scales of the tile's rows (weights, then x): a thread fetches a row's of a step, and they meet in LDS
+    uint32_t own_mx[kOwn];
+    float own_step[kOwn];
+    size_t own_row[kOwn]; // x: x_rows or more for none
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const uint32_t row = i * kThr + threadIdx.x;
+        own_row[i] = row < TC ? w_row0 + min(row, p.cols - 1u - col0) : min(source(row - TC), p.x_rows);
+    }
+    auto fetch_scales = [&](uint32_t t) {
+        if constexpr (MX || STEP) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                const uint32_t row = i * kThr + threadIdx.x;
+                const bool weights = row < TC; // the same for the whole wave
+                const Scales& s = weights ? p.ws : p.xs;
+                const bool none = row >= TC + TR || (!weights && own_row[i] >= p.x_rows);
+                own_mx[i] = 0x7F7F7F7Fu;
+                own_step[i] = 1.0f;
+                if (none)
+                    continue;
+                if (MX && s.kind == kScaleMx) {
+                    const uint8_t* const at = static_cast<const uint8_t*>(s.at) + own_row[i] * s.groups;
+                    const uint32_t block = 4u * t, last = depth / 32u - 1u;
+                    if (s.words && block + 3u <= last)
+                        own_mx[i] = *reinterpret_cast<const uint32_t*>(at + block);
+                    else if (s.width % 4u == 0)
+                        own_mx[i] = at[t / (s.width / 4u)] * 0x01010101u;
+                    else {
+                        uint32_t v = 0;
+                        for (uint32_t b = 0; b < 4u; ++b)
+                            v |= (block + b <= last ? (uint32_t)at[(block + b) / s.width] : 127u) << (8u * b);
+                        own_mx[i] = v;
+                    }
+                }
+                if (STEP && s.kind == kScaleStep)
+                    own_step[i] = static_cast<const float*>(s.at)[own_row[i] * s.groups + t / s.width];
+            }
+        }
+    };
+    auto put_scales = [&](uint32_t buf) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const uint32_t row = i * kThr + threadIdx.x;
+            if (kOwn * kThr == TC + TR || row < TC + TR) {
+                if constexpr (MX)
+                    s_mx[buf][row] = own_mx[i];
+                if constexpr (STEP)
+                    s_step[buf][row] = own_step[i];
+            }
+        }
+    };
+
+    v4f acc[NC][NR];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+            acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+    auto join = [](v4u lo, v4u hi) { return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w}; };
+    auto multiply = [&](uint32_t buf) {
+        v8i b[NR];
+        int b_mx[NR];
+        float b_step[NR];
+        // FP8: a lane's k are 16q .. and 64 + 16q .., FP4: 32q ..; its scale is that of the 32 from 32q on
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const uint32_t row = 16u * (wr * NR + j) + r;
+            const char* const at = s_r[buf] + row * 128u;
+            b[j] = join(*reinterpret_cast<const v4u*>(at + (q ^ (r & 7u)) * 16u),
+                        *reinterpret_cast<const v4u*>(at + ((q + 4u) ^ (r & 7u)) * 16u));
+            b_mx[j] = MX ? reinterpret_cast<const uint8_t*>(s_mx[buf] + TC + row)[q] : 127;
+            b_step[j] = STEP ? s_step[buf][TC + row] : 1.0f;
+        }
+        struct Weights {
+            v8i v;
+            int mx;
+            v4f step;
+        };
+        auto weights = [&](int i) {
+            const uint32_t row = 16u * (wc * NC + i) + r;
+            Weights a;
+            if constexpr (W4) {
+                const v4u v = *reinterpret_cast<const v4u*>(s_c[buf] + row * 64u + (q ^ (-(r >> 2) & 3u)) * 16u);
+                a.v = join(v, v4u{0, 0, 0, 0});
+            } else {
+                const char* const at = s_c[buf] + row * 128u;
+                a.v = join(*reinterpret_cast<const v4u*>(at + (q ^ (r & 7u)) * 16u),
+                           *reinterpret_cast<const v4u*>(at + ((q + 4u) ^ (r & 7u)) * 16u));
+            }
+            a.mx = MX ? reinterpret_cast<const uint8_t*>(s_mx[buf] + row)[q] : 127;
+            a.step = STEP ? *reinterpret_cast<const v4f*>(s_step[buf] + 16u * (wc * NC + i) + 4u * q)
+                          : v4f{1.0f, 1.0f, 1.0f, 1.0f};
+            return a;
+        };
+        Weights ahead = weights(0);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            // the next weights' reads under these products, and no others: with all of them at once the large tiles'
+            // registers overflow
+            if (kBounded)
+                __builtin_amdgcn_sched_barrier(0);
+            const Weights a = ahead;
+            if (i + 1 < NC)
+                ahead = weights(i + 1);
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                const v4f c = STEP ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
+                const v4f d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b[j], c, W4 ? 4 : 0, 0, 0, a.mx, 0,
+                                                                              b_mx[j]);
+                if constexpr (STEP) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][j][e] = __builtin_fmaf(d[e], a.step[e] * b_step[j], acc[i][j][e]);
+                } else {
+                    acc[i][j] = d;
+                }
+            }
+        }
+    };
+
+    // ---- the steps: one on its way while the one before it is multiplied
+    const uint32_t steps = (depth + kDepth - 1) / kDepth;
+    fetch(0, 0);
+    fetch_scales(0);
+    put_scales(0);
+#pragma clang loop unroll(disable) // (nor peeled)
+    for (uint32_t t = 0; t < steps; ++t) {
+        copies_done<0>();
+        __syncthreads(); // step t is there, and nobody reads step t - 1 any more
+        const uint32_t buf = t & 1u;
+        if (t + 1u < steps) {
+            fetch(t + 1u, buf ^ 1u);
+            fetch_scales(t + 1u);
+        }
+        multiply(buf);
+        put_scales(buf ^ 1u); // (past the last step unused: a branch here would draw the products behind it)
+    }
+
+    // ---- whole rows' scales, and the results: a lane has four columns of a row
+    auto row_scale = [](const Scales& s, size_t row) {
+        return s.kind != kScaleRow ? 1.0f
+               : s.u8              ? e8m0_value(static_cast<const uint8_t*>(s.at)[row])
+                                   : static_cast<const float*>(s.at)[row];
+    };
+    float c_scale[NC][4];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e)
+            c_scale[i][e] = row_scale(p.ws, w_row0 + min(16u * (wc * NC + i) + 4u * q + e, p.cols - 1u - col0));
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        const uint32_t row = 16u * (wr * NR + j) + r;
+        if (row >= rows)
+            continue;
+        const uint32_t at = source(row);
+        const float r_scale = at < p.x_rows ? row_scale(p.xs, at) : 0.0f;
+        const size_t line = (size_t)(row0 + row) * p.cols;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const uint32_t col = col0 + 16u * (wc * NC + i) + 4u * q;
+            if (col >= p.cols)
+                continue;
+            v4b v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = (__bf16)(acc[i][j][e] * r_scale * c_scale[i][e]);
+            *reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + line + col) = v;
+        }
+    }
+}
+
+template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
+tk_status launch(const QuantParams& p, hipStream_t s)
+{
+    const uint64_t col_tiles = ((uint64_t)p.cols + TC - 1) / TC;
+    const uint64_t most = p.n_rows < p.experts ? p.n_rows : p.experts;
+    const uint64_t blocks = ((p.n_rows / TR + most) * col_tiles + kXcds - 1) / kXcds * kXcds;
+    if (!launchable(blocks, 64 * WC * WR))
+        return TK_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((gemm_q_kernel<W4, MX, STEP, TC, TR, WC, WR>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0, s,
+                       p);
+    return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
+}
+
+template <bool W4, bool MX, bool STEP>
+tk_status launch_size(const QuantParams& p, hipStream_t s)
+{
+    const uint32_t load = p.n_rows / p.experts; // an expert's rows on average
+    if (load >= 128)
+        return launch<W4, MX, STEP, 256, 256, 2, 4>(p, s);
+    if (load >= 32)
+        return launch<W4, MX, STEP, 128, 64, 2, 2>(p, s);
+    return launch<W4, MX, STEP, 64, 16, 4, 1>(p, s);
+}
+
+// The scales of rows of `depth` columns in groups of `group` (0: the row).  False: not taken.
+bool scales_of(const void* at, int fmt, int64_t group, int64_t depth, Scales& s)
+{
+    s.at = at;
+    s.u8 = fmt == TK_SCALE_UE8M0;
+    s.kind = kScaleRow;
+    s.groups = s.width = 1;
+    s.words = 0;
+    if (group == 0 || group == depth)
+        return true;
+    if (group % (s.u8 ? 32 : 128) != 0)
+        return false;
+    s.kind = s.u8 ? kScaleMx : kScaleStep;
+    s.groups = (uint32_t)(depth / group);
+    s.width = (uint32_t)(group / (s.u8 ? 32 : 128));
+    s.words = s.u8 && s.width == 1 && s.groups % 4 == 0 && aligned(at, 4);
+    return true;
+}
+
+} // namespace
+
+extern "C" tk_status tk_expert_gemm(const void* x, const void* x_scales, int x_dtype, tk_scale_fmt x_scale_fmt,
+                                    int64_t x_group, int64_t x_rows, const int32_t* row_index,
+                                    const int32_t* expert_offsets, int64_t n_rows, const void* w, const void* w_scales,
+                                    int w_dtype, tk_scale_fmt w_scale_fmt, int64_t w_group, int64_t experts,
+                                    int64_t out_features, int64_t in_features, tk_dtype out_dtype, void* out,
+                                    void* stream)
+{
+    const bool x8 = x_dtype == TK_DTYPE_FP8, w8 = w_dtype == TK_DTYPE_FP8, w4 = w_dtype == TK_DTYPE_FP4;
+    const bool out_bf16 = (int)out_dtype == TK_DTYPE_BF16;
+    if (!valid_rows({x_rows, row_index}, expert_offsets, n_rows, experts) ||
+        !valid_shape(out_features, in_features, x8 || w8 || w4 ? 32 : 8) || (!x8 && x_dtype != TK_DTYPE_BF16) ||
+        (!w8 && !w4 && w_dtype != TK_DTYPE_BF16) || (!out_bf16 && (int)out_dtype != TK_DTYPE_FP32))
+        return TK_ERR_INVALID_ARG;
+    auto bad_scales = [&](int fmt, int64_t group) {
+        return fmt < TK_SCALE_FP32 || fmt > TK_SCALE_UE8M0_PACKED || group < 0 || (group && in_features % group != 0);
+    };
+    if ((x8 && bad_scales((int)x_scale_fmt, x_group)) || ((w8 || w4) && bad_scales((int)w_scale_fmt, w_group)))
+        return TK_ERR_INVALID_ARG;
+    if (n_rows > 0 && (!x || !w || !out || (x8 && !x_scales) || ((w8 || w4) && !w_scales)))
+        return TK_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) ||
+        (x8 && (int)x_scale_fmt == TK_SCALE_FP32 && !aligned(x_scales, 4)) ||
+        ((w8 || w4) && (int)w_scale_fmt == TK_SCALE_FP32 && !aligned(w_scales, 4)))
+        return TK_ERR_INVALID_ARG;
+    if (experts > kMaxExperts || x8 != (w8 || w4) || (x8 && !out_bf16))
+        return TK_ERR_UNSUPPORTED;
+    Scales xs{}, ws{};
+    if (x8 && ((int)x_scale_fmt > TK_SCALE_UE8M0 || (int)w_scale_fmt > TK_SCALE_UE8M0 ||
+               !scales_of(x_scales, x_scale_fmt, x_group, in_features, xs) ||
+               !scales_of(w_scales, w_scale_fmt, w_group, in_features, ws)))
+        return TK_ERR_UNSUPPORTED;
+    const size_t o_bytes = (size_t)n_rows * (size_t)out_features * (out_bf16 ? 2u : 4u);
+    const size_t w_rows = (size_t)experts * (size_t)out_features;
+    if (overlaps(out, o_bytes, x, (size_t)x_rows * (size_t)in_features * (x8 ? 1u : 2u)) ||
+        overlaps(out, o_bytes, w, w_rows * (size_t)in_features * 2u / (w4 ? 4u : w8 ? 2u : 1u)) ||
+        overlaps_rows(out, o_bytes, row_index, expert_offsets, n_rows, experts) ||
+        (x8 && (overlaps(out, o_bytes, x_scales, (size_t)x_rows * xs.groups * (xs.u8 ? 1u : 4u)) ||
+                overlaps(out, o_bytes, w_scales, w_rows * ws.groups * (ws.u8 ? 1u : 4u)))))
+        return TK_ERR_INVALID_ARG;
+    if (n_rows == 0)
+        return TK_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (!x8) {
+        GemmParams p{};
+        p.c = static_cast<const char*>(w);
+        p.r = static_cast<const char*>(x);
+        p.r_index = row_index;
+        p.r_rows = (uint32_t)x_rows;
+        p.offsets = expert_offsets;
+        p.n_rows = (uint32_t)n_rows;
+        p.experts = (uint32_t)experts;
+        p.cols = (uint32_t)out_features;
+        p.depth = (uint32_t)in_features;
+        p.out = out;
+        p.out_bf16 = out_bf16;
+        return launch_forward(p, s);
+    }
+    QuantParams p{};
+    p.w = static_cast<const char*>(w);
+    p.x = static_cast<const char*>(x);
+    p.index = row_index;
+    p.offsets = expert_offsets;
+    p.out = out;
+    p.ws = ws;
+    p.xs = xs;
+    p.x_rows = (uint32_t)x_rows;
+    p.n_rows = (uint32_t)n_rows;
+    p.experts = (uint32_t)experts;
+    p.cols = (uint32_t)out_features;
+    p.depth = (uint32_t)in_features;
+    const bool mx = xs.kind == kScaleMx || ws.kind == kScaleMx, step = xs.kind == kScaleStep || ws.kind == kScaleStep;
+    if (w4)
+        return mx ? (step ? launch_size<true, true, true>(p, s) : launch_size<true, true, false>(p, s))
+                  : (step ? launch_size<true, false, true>(p, s) : launch_size<true, false, false>(p, s));
+    return mx ? (step ? launch_size<false, true, true>(p, s) : launch_size<false, true, false>(p, s))
+              : (step ? launch_size<false, false, true>(p, s) : launch_size<false, false, false>(p, s));
+}

@@ -1,6 +1,6 @@
 /* tk_py.c -- the CPython extension module `_tkpy`: argument marshalling from
- * Python objects to the C ABI of include/tk.h and include/tk_layer.h, one function per entry point
- * under the same name.  Nothing else happens here: every function converts its
+ * Python objects to the C ABI of include/tk.h, include/tk_layer.h and include/tk_expert.h, one
+ * function per entry point under the same name.  Nothing else happens here: every function converts its
  * arguments and calls the library.
  *
  * Conversions:
@@ -20,6 +20,7 @@
 #include <Python.h>
 
 #include "tk.h"
+#include "tk_expert.h"
 #include "tk_layer.h"
 
 static PyObject* g_stream_getter = NULL; /* callable returning a stream handle */
@@ -340,6 +341,103 @@ static PyObject* py_tk_expert_gemv_fp4(PyObject* self, PyObject* args)
     return status(rc);
 }
 
+static PyObject* py_tk_expert_gemm(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *x, *x_scales, *index, *offsets, *w, *w_scales, *out, *stream = NULL;
+    long long x_group, x_rows, n_rows, w_group, experts, out_features, in_features;
+    int x_dtype, x_sfmt, w_dtype, w_sfmt, out_dtype;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&O&iiLLO&O&LO&O&iiLLLLiO&|O", as_ptr, &x, as_ptr, &x_scales, &x_dtype, &x_sfmt,
+                          &x_group, &x_rows, as_ptr, &index, as_ptr, &offsets, &n_rows, as_ptr, &w, as_ptr, &w_scales,
+                          &w_dtype, &w_sfmt, &w_group, &experts, &out_features, &in_features, &out_dtype, as_ptr, &out,
+                          &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_expert_gemm(x, x_scales, x_dtype, (tk_scale_fmt)x_sfmt, x_group, x_rows, (const int32_t*)index,
+                               (const int32_t*)offsets, n_rows, w, w_scales, w_dtype, (tk_scale_fmt)w_sfmt, w_group,
+                               experts, out_features, in_features, (tk_dtype)out_dtype, out, stream));
+    return status(rc);
+}
+
+static PyObject* py_tk_expert_gemm_dgrad(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *dy, *index, *offsets, *w, *dx, *stream = NULL;
+    long long dy_rows, n_rows, experts, out_features, in_features;
+    int out_dtype;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&LO&O&LO&LLLiO&|O", as_ptr, &dy, &dy_rows, as_ptr, &index, as_ptr, &offsets, &n_rows,
+                          as_ptr, &w, &experts, &out_features, &in_features, &out_dtype, as_ptr, &dx, &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_expert_gemm_dgrad(dy, dy_rows, (const int32_t*)index, (const int32_t*)offsets, n_rows, w, experts,
+                                     out_features, in_features, (tk_dtype)out_dtype, dx, stream));
+    return status(rc);
+}
+
+static PyObject* py_tk_expert_gemm_wgrad(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *dy, *dy_index, *x, *x_scales, *x_index, *offsets, *dw, *stream = NULL;
+    long long dy_rows, x_group, x_rows, n_rows, experts, out_features, in_features;
+    int x_dtype, accumulate, out_dtype;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&LO&O&O&iLLO&O&LLLLpiO&|O", as_ptr, &dy, &dy_rows, as_ptr, &dy_index, as_ptr, &x,
+                          as_ptr, &x_scales, &x_dtype, &x_group, &x_rows, as_ptr, &x_index, as_ptr, &offsets, &n_rows,
+                          &experts, &out_features, &in_features, &accumulate, &out_dtype, as_ptr, &dw, &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_expert_gemm_wgrad(dy, dy_rows, (const int32_t*)dy_index, x, x_scales, x_dtype, x_group, x_rows,
+                                     (const int32_t*)x_index, (const int32_t*)offsets, n_rows, experts, out_features,
+                                     in_features, accumulate, (tk_dtype)out_dtype, dw, stream));
+    return status(rc);
+}
+
+static PyObject* py_tk_swiglu_checkpoint_fp8(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *x, *w, *codes, *scales, *x_codes, *x_scales, *stream = NULL;
+    long long n, hidden, group;
+    float clamp;
+    int sfmt;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&O&LLLfiO&O&O&O&|O", as_ptr, &x, as_ptr, &w, &n, &hidden, &group, &clamp, &sfmt,
+                          as_ptr, &codes, as_ptr, &scales, as_ptr, &x_codes, as_ptr, &x_scales, &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_swiglu_checkpoint_fp8(x, (const float*)w, n, hidden, group, clamp, (tk_scale_fmt)sfmt, codes,
+                                         scales, x_codes, x_scales, stream));
+    return status(rc);
+}
+
+static PyObject* py_tk_swiglu_backward(PyObject* self, PyObject* args)
+{
+    (void)self;
+    void *dy, *h, *h_scales, *w, *dh, *dweight, *y, *stream = NULL;
+    long long group, n, hidden;
+    float clamp;
+    int h_dtype, sfmt;
+    PyObject* so = Py_None;
+    if (!PyArg_ParseTuple(args, "O&O&O&iiLO&LLfO&O&O&|O", as_ptr, &dy, as_ptr, &h, as_ptr, &h_scales, &h_dtype, &sfmt,
+                          &group, as_ptr, &w, &n, &hidden, &clamp, as_ptr, &dh, as_ptr, &dweight, as_ptr, &y, &so))
+        return NULL;
+    if (!as_stream(so, &stream))
+        return NULL;
+    tk_status rc;
+    TK_CALL(rc, tk_swiglu_backward(dy, h, h_scales, h_dtype, (tk_scale_fmt)sfmt, group, (const float*)w, n, hidden,
+                                   clamp, dh, (float*)dweight, y, stream));
+    return status(rc);
+}
+
 static PyMethodDef kMethods[] = {
     {"_set_stream_getter", py_set_stream_getter, METH_O, "set the callable that supplies the default stream"},
     {"tk_init", py_tk_init, METH_VARARGS, "tk_init(device)"},
@@ -377,6 +475,21 @@ static PyMethodDef kMethods[] = {
     {"tk_expert_gemv_fp4", py_tk_expert_gemv_fp4, METH_VARARGS,
      "tk_expert_gemv_fp4(x, x_scales, x_dtype, x_scale_fmt, x_group, topk_idx, tokens, k, x_slots, codes, scales, "
      "scale_fmt, group_size, experts, out_features, in_features, out_dtype, out, stream=None)"},
+    {"tk_expert_gemm", py_tk_expert_gemm, METH_VARARGS,
+     "tk_expert_gemm(x, x_scales, x_dtype, x_scale_fmt, x_group, x_rows, row_index, expert_offsets, n_rows, w, "
+     "w_scales, w_dtype, w_scale_fmt, w_group, experts, out_features, in_features, out_dtype, out, stream=None)"},
+    {"tk_expert_gemm_dgrad", py_tk_expert_gemm_dgrad, METH_VARARGS,
+     "tk_expert_gemm_dgrad(dy, dy_rows, row_index, expert_offsets, n_rows, w, experts, out_features, in_features, "
+     "out_dtype, dx, stream=None)"},
+    {"tk_expert_gemm_wgrad", py_tk_expert_gemm_wgrad, METH_VARARGS,
+     "tk_expert_gemm_wgrad(dy, dy_rows, dy_index, x, x_scales, x_dtype, x_group, x_rows, x_index, expert_offsets, "
+     "n_rows, experts, out_features, in_features, accumulate, out_dtype, dw, stream=None)"},
+    {"tk_swiglu_checkpoint_fp8", py_tk_swiglu_checkpoint_fp8, METH_VARARGS,
+     "tk_swiglu_checkpoint_fp8(x, topk_weight, n, hidden, group_size, clamp_limit, scale_fmt, codes, scales, x_codes, "
+     "x_scales, stream=None)"},
+    {"tk_swiglu_backward", py_tk_swiglu_backward, METH_VARARGS,
+     "tk_swiglu_backward(dy, h, h_scales, h_dtype, scale_fmt, group_size, topk_weight, n, hidden, clamp_limit, dh, "
+     "dweight, y, stream=None)"},
     {NULL, NULL, 0, NULL},
 };
 

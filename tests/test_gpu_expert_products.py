@@ -1,0 +1,328 @@
+"""The grouped products of include/tk_expert.h against plain statements in 64
+bits: whole numbers, whose sums are exact, bit for bit, over every tile size and
+ragged layout; numbers in general within their roundings."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import expert_ref as ex
+import layer_ref as ref
+import moe_activation_bit_amd as tk
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+OK = tk.TkStatus.TK_OK
+BF16, FP32, FP8, FP4 = tk.TK_DTYPE_BF16, tk.TK_DTYPE_FP32, tk.TK_DTYPE_FP8, tk.TK_DTYPE_FP4
+
+
+def say(*a):
+    print("[gpu-case]", *a, flush=True)
+
+
+def dev(a):
+    if a is None:
+        return None
+    return torch.from_numpy(np.ascontiguousarray(a.view(np.int16) if a.dtype == np.uint16 else a)).to(DEV)
+
+
+def bf16(a):
+    return dev(ref.bf16_bits(a))
+
+
+def host(t, bf):
+    torch.cuda.synchronize()
+    a = t.cpu().numpy()
+    return ref.bf16_value(a.view(np.uint16)) if bf else a
+
+
+def whole(rng, shape, most=4):
+    return rng.integers(-most, most + 1, shape).astype(np.float32)
+
+
+def offsets_of(counts, first=0):
+    return np.concatenate([[first], first + np.cumsum(counts)]).astype(np.int32)
+
+
+def index_of(rng, n, rows, bad):
+    """A row of `rows` for each of n; some name none."""
+    i = rng.integers(0, rows, n).astype(np.int32)
+    if bad:
+        i[rng.random(n) < 0.1] = rng.choice([-1, rows, 2 ** 31 - 1, -2 ** 31])
+    return i
+
+
+def same_or(got, want, bf):
+    """Exact results, rounded once for bf16."""
+    w = want.astype(np.float32)
+    assert np.array_equal(w.astype(np.float64), want)  # the case's sums fit fp32
+    assert np.array_equal(got, ref.round_bf16(w) if bf else w)
+
+
+# Each layout: rows of each expert, rows past the last, the first row.  Averages choose the tile sizes.
+LAYOUTS = {
+    "one": ([1], 0, 0),
+    "few": ([3, 0, 1, 5], 0, 0),
+    "few_behind": ([0, 17, 16, 0, 2], 9, 3),
+    "mid": ([33, 64, 0, 65, 40, 71], 5, 0),
+    "empty": ([0, 0, 0], 7, 0),
+    "large": ([256, 0, 300, 1, 513], 30, 2),
+    "large_one": ([391], 0, 0),
+    "many": ([int(v) for v in (np.arange(160) * 7) % 5], 3, 0),
+}
+SHAPES = [(8, 8), (24, 72), (264, 64), (136, 200), (520, 328)]
+
+
+def layout(name):
+    counts, behind, first = LAYOUTS[name]
+    return offsets_of(counts, first), int(first + sum(counts) + behind), len(counts)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("name", LAYOUTS)
+def test_forward_whole_numbers(name, shape, gather):
+    say("forward", name, shape, gather)
+    rng = np.random.default_rng(len(name) * 131 + shape[0] + shape[1])
+    off, n, e = layout(name)
+    out_f, in_f = shape
+    rows = 37 if gather else n
+    index = index_of(rng, n, rows, True) if gather else None
+    x, w = whole(rng, (rows, in_f)), whole(rng, (e, out_f, in_f))
+    for bf in (False, True):
+        start = whole(rng, (n, out_f), 100)
+        out = bf16(start) if bf else dev(start)
+        rc = tk.tk_expert_gemm(bf16(x), None, BF16, 0, 0, rows, dev(index), dev(off), n, bf16(w), None, BF16, 0, 0, e,
+                               out_f, in_f, BF16 if bf else FP32, out)
+        assert rc == OK
+        same_or(host(out, bf), ex.gemm(x, index, off, n, w, start)[0], bf)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("name", LAYOUTS)
+def test_dgrad_whole_numbers(name, shape, gather):
+    say("dgrad", name, shape, gather)
+    rng = np.random.default_rng(len(name) * 137 + shape[0] + shape[1])
+    off, n, e = layout(name)
+    in_f, out_f = shape
+    rows = 41 if gather else n
+    index = index_of(rng, n, rows, True) if gather else None
+    dy, w = whole(rng, (rows, out_f)), whole(rng, (e, out_f, in_f))
+    for bf in (False, True):
+        start = whole(rng, (n, in_f), 100)
+        dx = bf16(start) if bf else dev(start)
+        rc = tk.tk_expert_gemm_dgrad(bf16(dy), rows, dev(index), dev(off), n, bf16(w), e, out_f, in_f,
+                                     BF16 if bf else FP32, dx)
+        assert rc == OK
+        same_or(host(dx, bf), ex.dgrad(dy, index, off, n, w, start)[0], bf)
+
+
+def whole_codes(rng, shape):
+    """E4M3 codes of whole numbers -4 .. 4."""
+    v = rng.integers(-4, 5, shape)
+    code = np.array([0x00, 0x38, 0x40, 0x44, 0x48], np.uint8)[np.abs(v)]
+    return np.where(v < 0, code | 0x80, code).astype(np.uint8)
+
+
+@pytest.mark.parametrize("accumulate", [0, 1])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("shape", [(8, 16), (24, 80), (264, 64), (136, 208), (520, 336)], ids=str)
+@pytest.mark.parametrize("name", LAYOUTS)
+def test_wgrad_whole_numbers(name, shape, fp8, accumulate):
+    say("wgrad", name, shape, fp8, accumulate)
+    rng = np.random.default_rng(len(name) * 139 + shape[0] + shape[1])
+    off, n, e = layout(name)
+    out_f, in_f = shape
+    for gather_dy, gather_x in ((False, True), (True, False)):
+        dy_rows, x_rows = 29 if gather_dy else n, 31 if gather_x else n
+        dyi = index_of(rng, n, dy_rows, True) if gather_dy else None
+        xi = index_of(rng, n, x_rows, True) if gather_x else None
+        dy = whole(rng, (dy_rows, out_f))
+        if fp8:
+            group = rng.choice([g for g in (0, 8, 16, 40, 104) if in_f % (g or 1) == 0])
+            codes = whole_codes(rng, (x_rows, in_f))
+            scales = rng.integers(125, 130, (x_rows, in_f // (group or in_f))).astype(np.uint8)
+            x = ex.coded(codes, scales, True)
+            xd, sd = dev(codes), dev(scales)
+        else:
+            group, x = 0, whole(rng, (x_rows, in_f))
+            xd, sd = bf16(x), None
+        for bf in (False, True):
+            start = whole(rng, (e, out_f, in_f), 100)
+            dw = bf16(start) if bf else dev(start)
+            rc = tk.tk_expert_gemm_wgrad(bf16(dy), dy_rows, dev(dyi), xd, sd, FP8 if fp8 else BF16, int(group), x_rows,
+                                         dev(xi), dev(off), n, e, out_f, in_f, accumulate, BF16 if bf else FP32, dw)
+            assert rc == OK
+            want = ex.wgrad(dy, dyi, x, xi, off, n, start if accumulate else np.zeros_like(start))[0]
+            same_or(host(dw, bf), want, bf)
+
+
+KINDS = [("ue8m0", 0), ("ue8m0", 32), ("ue8m0", 96), ("ue8m0", 128), ("ue8m0", 64), ("fp32", 0), ("fp32", 128),
+         ("fp32", 256)]
+
+
+def fp8_operand(rng, rows, cols, kind, group, fp4=False, exact=True):
+    if fp4:
+        codes = rng.integers(0, 256, (rows, cols // 2)).astype(np.uint8)
+    elif exact:
+        codes = whole_codes(rng, (rows, cols))
+    else:
+        codes = rng.integers(0, 256, (rows, cols)).astype(np.uint8)
+        codes[(codes & 0x7F) == 0x7F] = 0
+    g = cols // (group or cols)
+    if kind == "ue8m0":
+        scales = rng.integers(125, 130, (rows, g)).astype(np.uint8)
+    elif exact:
+        scales = (2.0 ** rng.integers(-2, 3, (rows, g))).astype(np.float32)
+    else:
+        scales = rng.uniform(0.01, 1.0, (rows, g)).astype(np.float32)
+    return codes, scales, ex.coded(codes, scales, kind == "ue8m0", fp4)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("w_kind", KINDS, ids=str)
+@pytest.mark.parametrize("x_kind", KINDS, ids=str)
+@pytest.mark.parametrize("name", ["few_behind", "mid", "large"])
+def test_codes_whole_numbers(name, x_kind, w_kind, fp4):
+    """Codes of whole (FP4: half) numbers with power-of-two scales: no sum is rounded before bf16."""
+    say("codes", name, x_kind, w_kind, fp4)
+    rng = np.random.default_rng(len(name) + 7 * x_kind[1] + 11 * w_kind[1] + fp4)
+    off, n, e = layout(name)
+    groups = [g for g in (x_kind[1], w_kind[1]) if g]
+    in_f = int(np.lcm.reduce(groups + [32])) * (2 if name == "mid" else 1)
+    in_f += in_f if in_f < 256 else 0
+    out_f = 72 if name != "large" else 264
+    rows = 37
+    index = index_of(rng, n, rows, True)
+    xc, xs, x = fp8_operand(rng, rows, in_f, *x_kind)
+    wc, ws, w = fp8_operand(rng, e * out_f, in_f, *w_kind, fp4=fp4)
+    w = w.reshape(e, out_f, in_f)
+    start = whole(rng, (n, out_f), 100)
+    out = bf16(start)
+    rc = tk.tk_expert_gemm(dev(xc), dev(xs), FP8, 1 if x_kind[0] == "ue8m0" else 0, x_kind[1], rows, dev(index),
+                           dev(off), n, dev(wc), dev(ws), FP4 if fp4 else FP8, 1 if w_kind[0] == "ue8m0" else 0,
+                           w_kind[1], e, out_f, in_f, BF16, out)
+    assert rc == OK
+    same_or(host(out, True), ex.gemm(x, index, off, n, w, start)[0], True)
+
+
+def test_codes_of_every_width():
+    """Widths that end inside a step of 128 columns, every kind of scale that they admit."""
+    for in_f, (xk, wk), fp4, name in itertools.product((32, 96, 160, 416), ((0, 0), (1, 0), (0, 1), (1, 1)),
+                                                       (False, True), ("few", "mid", "large_one")):
+        say("width", in_f, xk, wk, fp4, name)
+        rng = np.random.default_rng(in_f + xk + 2 * wk)
+        off, n, e = layout(name)
+        out_f = 40
+        kinds = [("ue8m0", 32), ("fp32", 0)]
+        xc, xs, x = fp8_operand(rng, n, in_f, *kinds[xk])
+        wc, ws, w = fp8_operand(rng, e * out_f, in_f, *kinds[wk], fp4=fp4)
+        start = whole(rng, (n, out_f), 100)
+        out = bf16(start)
+        rc = tk.tk_expert_gemm(dev(xc), dev(xs), FP8, 1 - xk, kinds[xk][1], n, None, dev(off), n, dev(wc), dev(ws),
+                               FP4 if fp4 else FP8, 1 - wk, kinds[wk][1], e, out_f, in_f, BF16, out)
+        assert rc == OK
+        same_or(host(out, True), ex.gemm(x, None, off, n, w.reshape(e, out_f, in_f), start)[0], True)
+
+
+# Numbers in general.  bf16: K exact products summed in fp32, each addition off by at most a step (2^-23) of a
+# partial sum that the terms' magnitudes bound, then one rounding.
+def check_sum(got, bf, want, mag, depth, more=0.0):
+    tol = (depth + 2) * 2.0 ** -23 * mag + more
+    if bf:
+        tol = tol * (1 + ref.UB16) + ref.UB16 * np.abs(want)
+    bad = np.abs(got - want) > tol
+    assert not bad.any(), (np.argwhere(bad)[:3], np.abs(got - want)[bad][:3], tol[bad][:3])
+
+
+@pytest.mark.parametrize("bf", [False, True])
+@pytest.mark.parametrize("name,out_f,in_f", [("few_behind", 200, 1000), ("mid", 264, 520), ("large", 264, 520)])
+def test_numbers(name, out_f, in_f, bf):
+    say("numbers", name, out_f, in_f, bf)
+    rng = np.random.default_rng(in_f)
+    off, n, e = layout(name)
+    x = ref.round_bf16(rng.standard_normal((n, in_f)) * np.exp(rng.standard_normal((n, 1))))
+    dy = ref.round_bf16(rng.standard_normal((n, out_f)))
+    w = ref.round_bf16(rng.standard_normal((e, out_f, in_f)) * in_f ** -0.5)
+    kind = BF16 if bf else FP32
+
+    def buffer(*shape):
+        return torch.zeros(shape, dtype=torch.int16 if bf else torch.float32, device=DEV)
+
+    out, dx, dw = buffer(n, out_f), buffer(n, in_f), buffer(e, out_f, in_f)
+    assert tk.tk_expert_gemm(bf16(x), None, BF16, 0, 0, n, None, dev(off), n, bf16(w), None, BF16, 0, 0, e, out_f, in_f,
+                             kind, out) == OK
+    assert tk.tk_expert_gemm_dgrad(bf16(dy), n, None, dev(off), n, bf16(w), e, out_f, in_f, kind, dx) == OK
+    assert tk.tk_expert_gemm_wgrad(bf16(dy), n, None, bf16(x), None, BF16, 0, n, None, dev(off), n, e, out_f, in_f, 0,
+                                   kind, dw) == OK
+    check_sum(host(out, bf), bf, *ex.gemm(x, None, off, n, w, np.zeros((n, out_f))), in_f)
+    check_sum(host(dx, bf), bf, *ex.dgrad(dy, None, off, n, w, np.zeros((n, in_f))), out_f)
+    check_sum(host(dw, bf), bf, *ex.wgrad(dy, None, x, None, off, n, np.zeros(w.shape)),
+              max(b - a for a, b in ex.spans(off, n)))
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("x_kind,w_kind", [(("ue8m0", 32), ("ue8m0", 32)), (("fp32", 128), ("fp32", 128)),
+                                           (("fp32", 128), ("ue8m0", 32)), (("fp32", 0), ("fp32", 0))], ids=str)
+def test_codes_numbers(x_kind, w_kind, fp4):
+    """Random codes: of 128 products, each may lose what lies 2^-13 below the largest of them (the instruction
+    keeps them to 14 bits or more below it); scaling and adding the steps' sums round three times a step."""
+    say("codes", x_kind, w_kind, fp4)
+    rng = np.random.default_rng(5)
+    off, n, e = layout("large")
+    in_f, out_f = 640, 136
+    xc, xs, x = fp8_operand(rng, n, in_f, *x_kind, exact=False)
+    wc, ws, w = fp8_operand(rng, e * out_f, in_f, *w_kind, fp4=fp4, exact=False)
+    w = w.reshape(e, out_f, in_f)
+    out = torch.zeros((n, out_f), dtype=torch.int16, device=DEV)
+    rc = tk.tk_expert_gemm(dev(xc), dev(xs), FP8, 1 if x_kind[0] == "ue8m0" else 0, x_kind[1], n, None, dev(off), n,
+                           dev(wc), dev(ws), FP4 if fp4 else FP8, 1 if w_kind[0] == "ue8m0" else 0, w_kind[1], e,
+                           out_f, in_f, BF16, out)
+    assert rc == OK
+    want, mag = ex.gemm(x, None, off, n, w, np.zeros((n, out_f)))
+    lost = np.zeros_like(want)
+    for k in range(0, in_f, 128):
+        for i, (lo, hi) in enumerate(ex.spans(off, n)):
+            a, b = np.abs(x[lo:hi, k:k + 128]), np.abs(w[i][:, k:k + 128])
+            for r in range(lo, hi):
+                lost[r] += 128 * 2.0 ** -13 * (a[r - lo] * b).max(1)
+    check_sum(host(out, True), True, want, mag, 3 * in_f // 128, lost)
+
+
+@pytest.mark.parametrize("bad", [[0, 40, 20, 60], [-5, 10, 10, 1000], [50, 40, 30, 20], [2 ** 31 - 1, -1, 64, 64]],
+                         ids=str)
+def test_offsets_out_of_order(bad):
+    """Entries outside 0 .. n count as these, an entry below the one before it as an expert without rows."""
+    say("offsets", bad)
+    rng = np.random.default_rng(3)
+    n, e, out_f, in_f = 64, 3, 72, 40
+    off = np.array(bad, np.int32)
+    x, w, dy = whole(rng, (n, in_f)), whole(rng, (e, out_f, in_f)), whole(rng, (n, out_f))
+    dw = torch.zeros((e, out_f, in_f), device=DEV)
+    assert tk.tk_expert_gemm_wgrad(bf16(dy), n, None, bf16(x), None, BF16, 0, n, None, dev(off), n, e, out_f, in_f, 0,
+                                   FP32, dw) == OK
+    same_or(host(dw, False), ex.wgrad(dy, None, x, None, off, n, np.zeros(w.shape))[0], False)
+    if any(a > b for a, b in zip(ex.spans(off, n)[:-1], ex.spans(off, n)[1:])):
+        return  # rows of two experts: either's result
+    out = torch.zeros((n, out_f), device=DEV)
+    assert tk.tk_expert_gemm(bf16(x), None, BF16, 0, 0, n, None, dev(off), n, bf16(w), None, BF16, 0, 0, e, out_f, in_f,
+                             FP32, out) == OK
+    same_or(host(out, False), ex.gemm(x, None, off, n, w, np.zeros((n, out_f)))[0], False)
+
+
+def test_no_offsets_and_no_rows():
+    rng = np.random.default_rng(8)
+    x, w = whole(rng, (130, 64)), whole(rng, (1, 48, 64))
+    out = torch.zeros((130, 48), device=DEV)
+    assert tk.tk_expert_gemm(bf16(x), None, BF16, 0, 0, 130, None, None, 130, bf16(w), None, BF16, 0, 0, 1, 48, 64, FP32,
+                             out) == OK
+    same_or(host(out, False), x.astype(np.float64) @ w[0].T, False)
+    dw = torch.ones((2, 48, 64), device=DEV)
+    assert tk.tk_expert_gemm_wgrad(None, 0, None, None, None, BF16, 0, 0, None, dev(np.zeros(3, np.int32)), 0, 2, 48, 64,
+                                   1, FP32, dw) == OK
+    assert host(dw, False).min() == 1
+    assert tk.tk_expert_gemm_wgrad(None, 0, None, None, None, BF16, 0, 0, None, dev(np.zeros(3, np.int32)), 0, 2, 48, 64,
+                                   0, FP32, dw) == OK
+    assert not host(dw, False).any()
