@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "tk_gemm_host.h"
 #include "tk_gemm_tile.h"
@@ -28,6 +29,25 @@ __device__ __forceinline__ v8b read_transposed(const char* at, uint32_t pitch)
     const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at));
     const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4u * pitch));
     return __builtin_bit_cast(v8b, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Four columns of a row, rounded once; ADD: to what is there, when asked.
+template <bool ADD>
+__device__ __forceinline__ void store_result(const GemmParams& p, size_t at, v4f v)
+{
+    if (p.out_bf16) {
+        v4b* const to = reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + at);
+        if (ADD && p.accumulate) {
+            const v4b old = *to;
+            v += v4f{(float)old[0], (float)old[1], (float)old[2], (float)old[3]};
+        }
+        *to = v4b{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    } else {
+        v4f* const to = reinterpret_cast<v4f*>(static_cast<float*>(p.out) + at);
+        if (ADD && p.accumulate)
+            v += *to;
+        *to = v;
+    }
 }
 
 template <int KIND, int TC, int TR, int WC, int WR, bool X8>
@@ -74,12 +94,11 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
                         },
                         g))
             return;
-        // rows first: the row tiles of a few columns share their weights in the L2
-        const uint32_t in = t - g.first * col_tiles;
         expert = g.expert;
-        row0 = g.row0 + in % g.tiles * TR;
-        rows = min((uint32_t)TR, g.rows - in % g.tiles * TR);
-        col0 = in / g.tiles * TC;
+        const uint2 at = tile_in_group(t - g.first * col_tiles, g.tiles, col_tiles);
+        row0 = g.row0 + at.x * TR;
+        rows = min((uint32_t)TR, g.rows - at.x * TR);
+        col0 = at.y * TC;
         depth = p.depth;
     }
 
@@ -317,36 +336,384 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
             const uint32_t col = col0 + 16u * (wc * NC + i) + 4u * q;
             if (col >= p.cols)
                 continue;
-            v4f v = acc[i][j];
-            if (p.out_bf16) {
-                v4b* const to = reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + line + col);
-                if (KIND == kWgrad && p.accumulate) {
-                    const v4b old = *to;
-                    v += v4f{(float)old[0], (float)old[1], (float)old[2], (float)old[3]};
-                }
-                *to = v4b{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-            } else {
-                v4f* const to = reinterpret_cast<v4f*>(static_cast<float*>(p.out) + line + col);
-                if (KIND == kWgrad && p.accumulate)
-                    v += *to;
-                *to = v;
-            }
+            store_result<KIND == kWgrad>(p, line + col, acc[i][j]);
         }
     }
 }
 
-// Launches the kernel with tiles of TR rows by TC columns.
+// The same for tiles of 256 x 256 by eight waves, 64 columns x 128 rows each.  A
+// step's 64 k are two halves.  While the first half is multiplied, the second's
+// fragments are read; then the waves meet (every one has read all of this step,
+// and the next one is in LDS); while the second half is multiplied, the next
+// step's first fragments are read and the step after that is copied over this
+// one.
+template <int KIND, bool X8>
+__global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
+{
+    constexpr uint32_t TC = 256, TR = 256, kWaves = 8;
+    constexpr bool kCT = KIND != kForward, kRT = KIND == kWgrad;
+    constexpr int kBlocks = 4;           // of 16 columns a wave
+    constexpr int kCopies = 4;           // 1 KiB pieces of an operand's step a wave
+    constexpr uint32_t kBytes = TC * kDepth * 2;
+    constexpr int kCodes = X8 ? 2 : 1;   // 16-code pieces of x a thread
+    __shared__ __attribute__((aligned(1024))) char s_c[2][kBytes];
+    __shared__ __attribute__((aligned(1024))) char s_r[2][kBytes];
+
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1), r = lane & 15u, q = lane >> 4;
+    const uint32_t wave = uniform(threadIdx.x / kWaveSize), wc = wave & 3u, wr = wave >> 2;
+
+    // ---- this workgroup's tile
+    const uint32_t col_tiles = (p.cols + TC - 1) / TC;
+    uint32_t expert, row_base = 0, row0, rows, col0, depth;
+    if constexpr (KIND == kWgrad) {
+        const uint32_t row_tiles = (p.out_rows + TR - 1) / TR, per = row_tiles * col_tiles;
+        const uint32_t t = xcd_tile(blockIdx.x, p.experts * per);
+        if (t >= p.experts * per)
+            return;
+        expert = t / per;
+        const uint32_t in = t - expert * per;
+        row0 = in / col_tiles * TR;
+        rows = min(TR, p.out_rows - row0);
+        col0 = in % col_tiles * TC;
+        expert_rows(p.offsets, expert, p.n_rows, row_base, depth);
+        row_base = uniform(row_base);
+        depth = uniform(depth);
+        if (p.accumulate && depth == 0)
+            return;
+    } else {
+        Group g;
+        uint32_t t = 0;
+        if (!find_group(p.offsets, p.experts, p.n_rows, TR,
+                        [&](uint32_t total) {
+                            t = xcd_tile(blockIdx.x, total * col_tiles);
+                            return t / col_tiles;
+                        },
+                        g))
+            return;
+        expert = g.expert;
+        const uint2 at = tile_in_group(t - g.first * col_tiles, g.tiles, col_tiles);
+        row0 = g.row0 + at.x * TR;
+        rows = min(TR, g.rows - at.x * TR);
+        col0 = at.y * TC;
+        depth = p.depth;
+    }
+    const uint32_t steps = (depth + kDepth - 1) / kDepth;
+
+    // ---- where each lane's copies come from (layouts in LDS as in gemm_kernel)
+    auto hash = [](uint32_t k) { return (k & 3u) | ((k >> 1) & 4u); };
+    const uint32_t ld_c = (KIND == kForward ? p.depth : p.cols) * (X8 ? 1u : 2u);
+    const uint32_t ld_r = (kRT ? p.out_rows : p.depth) * 2u;
+    const char* base_c = p.c;
+    if constexpr (KIND == kForward)
+        base_c += ((size_t)expert * p.cols + col0) * ld_c;
+    if constexpr (KIND == kDgrad)
+        base_c += (size_t)expert * p.depth * ld_c;
+    const uint32_t row_k = ((lane & 7u) ^ (lane >> 3)) * 8u; // [row][k]: the lane's first k of a step
+    auto k_of = [&](int i) { return (i * kWaves + wave) * 2u + (lane >> 5); }; // [k][column]: its row k of copy i
+    auto col_of = [&](int i) {                                                // ... and its column
+        const uint32_t s = lane & 31u;
+        return (((s >> 1) ^ hash(k_of(i))) * 2u + (s & 1u)) * 8u;
+    };
+    uint32_t offset_c[kCopies], offset_r[kCopies], row_r[kCopies];
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const uint32_t row = (i * kWaves + wave) * 8u + lane / 8u;
+        if constexpr (!kCT) {
+            offset_c[i] = min(row, p.cols - 1u - col0) * ld_c + row_k * 2u;
+        } else {
+            uint32_t col = col0 + col_of(i);
+            col = col < p.cols ? col : 0u; // not stored
+            offset_c[i] = (KIND == kDgrad ? k_of(i) * ld_c : 0u) + col * 2u;
+        }
+        if constexpr (!kRT) {
+            uint32_t at = row0 + min(row, rows - 1u);
+            if (p.r_index)
+                at = (uint32_t)p.r_index[at];
+            row_r[i] = at < p.r_rows ? at : 0u; // (a row that is none: any, and zeros as its result)
+            offset_r[i] = row_r[i] * ld_r + row_k * 2u;
+        } else {
+            const uint32_t col = row0 + col_of(i);
+            offset_r[i] = (col < p.out_rows ? col : 0u) * 2u;
+        }
+    }
+
+    // wgrad: the row of x or dy for the expert's row k, to be looked at only when it is used: until then it may
+    // be on its way
+    auto source = [&](const int32_t* index, uint32_t k) -> uint32_t {
+        const uint32_t at = row_base + min(k, depth - 1u);
+        return index ? (uint32_t)index[at] : at;
+    };
+    uint32_t next_c[kCopies], next_r[kCopies], next_x[kCodes]; // of the coming copies
+    auto find_rows = [&](uint32_t t) {
+        if constexpr (KIND == kWgrad) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                if constexpr (!X8)
+                    next_c[i] = source(p.c_index, t * kDepth + k_of(i));
+                next_r[i] = source(p.r_index, t * kDepth + k_of(i));
+            }
+        }
+    };
+    // X8: a thread takes the 16 codes s of the rows i * 32 + threadIdx / 16
+    const uint32_t code_s = threadIdx.x & 15u, code_k = threadIdx.x >> 4;
+    const uint32_t code_col = X8 && col0 + code_s * 16u < p.cols ? col0 + code_s * 16u : 0u;
+    const uint32_t code_g0 = X8 ? code_col / p.c_group : 0u, code_g1 = X8 ? (code_col + 8u) / p.c_group : 0u;
+    v4u codes[kCodes];
+    uint8_t scale0[kCodes], scale1[kCodes];
+    auto find_code_rows = [&](uint32_t t) {
+        if constexpr (X8)
+#pragma unroll
+            for (int i = 0; i < kCodes; ++i)
+                next_x[i] = source(p.c_index, t * kDepth + i * 32u + code_k);
+    };
+    auto load_codes = [&](uint32_t t) {
+        if constexpr (X8)
+#pragma unroll
+            for (int i = 0; i < kCodes; ++i) {
+                const bool in = next_x[i] < p.c_rows && t * kDepth + i * 32u + code_k < depth;
+                const size_t row = in ? next_x[i] : 0u;
+                codes[i] = *reinterpret_cast<const v4u*>(in ? p.c + row * ld_c + code_col : zeros());
+                const uint8_t* const sc = p.c_scales + row * p.c_groups;
+                scale0[i] = sc[code_g0];
+                scale1[i] = sc[code_g1];
+            }
+    };
+    auto put_codes = [&](int i, uint32_t buf) { // as bf16 numbers, with their power-of-two scales
+        if constexpr (X8) {
+            const uint32_t k = i * 32u + code_k;
+            const uint32_t word[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+            char* const to = s_c[buf] + k * (TC * 2u) + (code_s ^ hash(k)) * 32u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float scale = as_float((uint32_t)(h ? scale1[i] : scale0[i]) << 23);
+                *reinterpret_cast<uint4*>(to + 16 * h) =
+                    make_uint4(fp8_to_bf16<false>(word[2 * h], scale), fp8_to_bf16<true>(word[2 * h], scale),
+                               fp8_to_bf16<false>(word[2 * h + 1], scale), fp8_to_bf16<true>(word[2 * h + 1], scale));
+            }
+        }
+    };
+
+    // Copy i of an operand's step t.  FAST: whole steps whose offsets fit 32 bits, from a base that is the same for
+    // the whole wave (past the last step that one again, unused); else past the depth, and for rows that are none,
+    // zeros.
+    auto copy_c = [&](auto fast, uint32_t t, uint32_t buf, int i) {
+        char* const to = s_c[buf] + (i * kWaves + wave) * 1024u;
+        if constexpr (KIND == kWgrad) {
+            if constexpr (!X8)
+                copy_to_lds(next_c[i] < p.c_rows && t * kDepth + k_of(i) < depth
+                                ? p.c + (size_t)next_c[i] * ld_c + offset_c[i]
+                                : zeros(),
+                            to);
+        } else {
+            const uint32_t u = decltype(fast)::value ? min(t, steps - 1u) : t, k = t * kDepth + (kCT ? k_of(i) : row_k);
+            const size_t step = kCT ? (size_t)u * kDepth * ld_c : (size_t)u * (kDepth * 2u);
+            if constexpr (decltype(fast)::value)
+                copy_to_lds(base_c + step, offset_c[i], to);
+            else
+                copy_to_lds(k < depth ? base_c + step + offset_c[i] : zeros(), to);
+        }
+    };
+    auto copy_r = [&](auto fast, uint32_t t, uint32_t buf, int i) {
+        char* const to = s_r[buf] + (i * kWaves + wave) * 1024u;
+        if constexpr (KIND == kWgrad) {
+            copy_to_lds(next_r[i] < p.r_rows && t * kDepth + k_of(i) < depth
+                            ? p.r + (size_t)next_r[i] * ld_r + offset_r[i]
+                            : zeros(),
+                        to);
+        } else if constexpr (decltype(fast)::value) {
+            copy_to_lds(p.r + (size_t)min(t, steps - 1u) * (kDepth * 2u), offset_r[i], to);
+        } else {
+            copy_to_lds(t * kDepth + row_k < depth ? p.r + (size_t)row_r[i] * ld_r + (t * kDepth + row_k) * 2u : zeros(),
+                        to);
+        }
+    };
+
+    // fragments of half h of a step; the wave's row blocks are every second one, so that a tile of few rows is
+    // shared evenly
+    const uint32_t key = (r >> 2) | (q & 1u) << 2;
+    auto read_c = [&](uint32_t buf, int h, int i) -> v8b {
+        const uint32_t tile = wc * kBlocks + i;
+        if constexpr (!kCT)
+            return *reinterpret_cast<const v8b*>(s_c[buf] + (tile * 16u + r) * 128u + ((4u * h + q) ^ (r & 7u)) * 16u);
+        else
+            return read_transposed(s_c[buf] + (32u * h + 8u * q + (r >> 2)) * (TC * 2u) + (tile ^ key) * 32u +
+                                       (r & 3u) * 8u,
+                                   TC * 2u);
+    };
+    auto read_r = [&](uint32_t buf, int h, int j) -> v8b {
+        const uint32_t tile = 2u * j + wr;
+        if constexpr (!kRT)
+            return *reinterpret_cast<const v8b*>(s_r[buf] + (tile * 16u + r) * 128u + ((4u * h + q) ^ (r & 7u)) * 16u);
+        else
+            return read_transposed(s_r[buf] + (32u * h + 8u * q + (r >> 2)) * (TR * 2u) + (tile ^ key) * 32u +
+                                       (r & 3u) * 8u,
+                                   TR * 2u);
+    };
+
+    // ---- the steps, and the results, with N row blocks a wave
+    auto run = [&](auto n_blocks, auto fast) {
+        constexpr int N = decltype(n_blocks)::value;
+        constexpr int kCopiesR = kRT ? kCopies : N / 2; // [row][k]: the rows that the blocks have
+        v4f acc[kBlocks][N];
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (steps) {
+            v8b a[2][kBlocks], b[2][N]; // of the half at hand and of the next
+            // codes of steps 0 and 1 by way of registers, then the copies, then the codes of step 2
+            if constexpr (X8)
+#pragma unroll
+                for (uint32_t t = 0; t < 2; ++t) {
+                    find_code_rows(t);
+                    load_codes(t);
+#pragma unroll
+                    for (int i = 0; i < kCodes; ++i)
+                        put_codes(i, t);
+                }
+#pragma unroll
+            for (uint32_t t = 0; t < 2; ++t) {
+                find_rows(t);
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    copy_c(fast, t, t, i);
+                    if (i < kCopiesR)
+                        copy_r(fast, t, t, i);
+                }
+            }
+            find_rows(2);
+            find_code_rows(2);
+            load_codes(2);
+            find_code_rows(3);
+            copies_done<0>();
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i)
+                a[0][i] = read_c(0, 0, i);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                b[0][j] = read_r(0, 0, j);
+            // Fragments of a half in the order that the products need them, some beside each row block's products and
+            // none beside the last ones, under which they arrive; the copies behind the products.
+            constexpr int kReadsEach = N >= 8 ? 2 : 3, kCopiesEach = (kCopies + kCopiesR + N - 1) / N;
+            auto read_some = [&](int group, int set, uint32_t from, int half) {
+#pragma unroll
+                for (int n = group * kReadsEach; n < (group + 1) * kReadsEach; ++n) {
+                    if (n == 1)
+                        b[set][0] = read_r(from, half, 0);
+                    else if (n <= kBlocks)
+                        a[set][n ? n - 1 : 0] = read_c(from, half, n ? n - 1 : 0);
+                    else if (n < kBlocks + N)
+                        b[set][n - kBlocks] = read_r(from, half, n - kBlocks);
+                }
+            };
+#pragma clang loop unroll(disable) // (nor peeled)
+            for (uint32_t t = 0; t < steps; ++t) {
+                const uint32_t buf = t & 1u;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    read_some(j, 1, buf, 1);
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[0][i], b[0][j], acc[i][j], 0, 0, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                copies_done<0>();
+                __syncthreads(); // step t + 1 is there, and every wave has read all of step t
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    read_some(j, 0, buf ^ 1u, 0);
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[1][i], b[1][j], acc[i][j], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (X8 && j < kCodes)
+                        put_codes(j, buf);
+#pragma unroll
+                    for (int n = j * kCopiesEach; n < (j + 1) * kCopiesEach; ++n) {
+                        if (n < kCopies)
+                            copy_c(fast, t + 2u, buf, n);
+                        else if (n < kCopies + kCopiesR)
+                            copy_r(fast, t + 2u, buf, n - kCopies);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                // what the next copies need, on its way until the waves meet again
+                find_rows(t + 3u);
+                load_codes(t + 3u);
+                find_code_rows(t + 4u);
+            }
+        }
+
+        // ---- results: a lane has four columns of a row
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint32_t row = 16u * (2u * j + wr) + r;
+            if (row >= rows)
+                continue;
+            const bool none = KIND != kWgrad && p.r_index && (uint32_t)p.r_index[row0 + row] >= p.r_rows;
+            const size_t line = ((size_t)(KIND == kWgrad ? expert * (size_t)p.out_rows : 0u) + row0 + row) * p.cols;
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                const uint32_t col = col0 + 16u * (wc * kBlocks + i) + 4u * q;
+                if (col >= p.cols)
+                    continue;
+                store_result<KIND == kWgrad>(p, line + col, none ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j]);
+            }
+        }
+    };
+    using std::integral_constant;
+    using std::bool_constant;
+    auto run_blocks = [&](auto fast) {
+        const uint32_t blocks = KIND == kWgrad ? 8u : uniform((rows + 31u) / 32u);
+        if (blocks > 6)
+            run(integral_constant<int, 8>{}, fast);
+        if constexpr (KIND != kWgrad) {
+            if (blocks > 4 && blocks <= 6)
+                run(integral_constant<int, 6>{}, fast);
+            else if (blocks > 2 && blocks <= 4)
+                run(integral_constant<int, 4>{}, fast);
+            else if (blocks <= 2)
+                run(integral_constant<int, 2>{}, fast);
+        }
+    };
+    if (KIND != kWgrad && depth % kDepth == 0 && (uint64_t)p.r_rows * ld_r < (1ull << 32))
+        run_blocks(bool_constant<true>{});
+    else
+        run_blocks(bool_constant<false>{});
+}
+
+// At most how many tiles of TR rows by TC columns there are, however the rows lie, in workgroups of whole turns
+// over the XCDs.
+template <int KIND>
+uint64_t workgroups(const GemmParams& p, uint32_t tc, uint32_t tr)
+{
+    const uint64_t col_tiles = ((uint64_t)p.cols + tc - 1) / tc, most = p.n_rows < p.experts ? p.n_rows : p.experts;
+    const uint64_t row_tiles =
+        KIND == kWgrad ? (uint64_t)p.experts * (((uint64_t)p.out_rows + tr - 1) / tr) : p.n_rows / tr + most;
+    return (row_tiles * col_tiles + kXcds - 1) / kXcds * kXcds;
+}
+
 template <int KIND, int TC, int TR, int WC, int WR, bool X8 = false>
 tk_status launch(const GemmParams& p, hipStream_t s)
 {
-    const uint64_t col_tiles = ((uint64_t)p.cols + TC - 1) / TC;
-    const uint64_t most = p.n_rows < p.experts ? p.n_rows : p.experts;
-    const uint64_t row_tiles = KIND == kWgrad ? (uint64_t)p.experts * (((uint64_t)p.out_rows + TR - 1) / TR)
-                                              : p.n_rows / TR + most; // at most so many, however the rows lie
-    const uint64_t blocks = (row_tiles * col_tiles + kXcds - 1) / kXcds * kXcds;
+    const uint64_t blocks = workgroups<KIND>(p, TC, TR);
     if (!launchable(blocks, 64 * WC * WR))
         return TK_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((gemm_kernel<KIND, TC, TR, WC, WR, X8>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0, s, p);
+    return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
+}
+
+template <int KIND, bool X8 = false>
+tk_status launch_big(const GemmParams& p, hipStream_t s)
+{
+    const uint64_t blocks = workgroups<KIND>(p, 256, 256);
+    if (!launchable(blocks, 512))
+        return TK_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((gemm_big_kernel<KIND, X8>), dim3((uint32_t)blocks), dim3(512), 0, s, p);
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
 
@@ -358,7 +725,7 @@ tk_status launch_forward(const GemmParams& p, hipStream_t s)
 {
     const uint32_t load = p.n_rows / p.experts; // an expert's rows on average
     if (load >= 128)
-        return launch<kForward, 256, 256, 2, 4>(p, s);
+        return launch_big<kForward>(p, s);
     if (load >= 32)
         return launch<kForward, 128, 64, 2, 2>(p, s);
     return launch<kForward, 64, 16, 4, 1>(p, s);
@@ -391,7 +758,7 @@ extern "C" tk_status tk_expert_gemm_dgrad(const void* dy, int64_t dy_rows, const
         return TK_OK;
     GemmParams p{};
     p.c = static_cast<const char*>(w);
-    p.r = static_cast<const char*>(dy);
+    p.r = static_cast<const char*>(dy_rows ? dy : w); // (no row: what is read in its place is not used)
     p.r_index = row_index;
     p.r_rows = (uint32_t)dy_rows;
     p.offsets = expert_offsets;
@@ -403,7 +770,7 @@ extern "C" tk_status tk_expert_gemm_dgrad(const void* dy, int64_t dy_rows, const
     p.out_bf16 = out_bf16;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (p.n_rows / p.experts >= 128)
-        return launch<kDgrad, 256, 256, 2, 4>(p, s);
+        return launch_big<kDgrad>(p, s);
     return launch<kDgrad, 128, 64, 2, 2>(p, s);
 }
 
@@ -456,6 +823,8 @@ extern "C" tk_status tk_expert_gemm_wgrad(const void* dy, int64_t dy_rows, const
     p.out_bf16 = out_bf16;
     p.accumulate = accumulate;
     hipStream_t s = static_cast<hipStream_t>(stream);
+    if (p.out_rows >= 192 && p.cols >= 192)
+        return fp8 ? launch_big<kWgrad, true>(p, s) : launch_big<kWgrad>(p, s);
     if (fp8)
         return launch<kWgrad, 128, 128, 2, 2, true>(p, s);
     return launch<kWgrad, 128, 128, 2, 2>(p, s);

@@ -76,9 +76,9 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
                     },
                     g))
         return;
-    const uint32_t in = t - g.first * col_tiles;
-    const uint32_t row0 = g.row0 + in % g.tiles * TR, rows = min((uint32_t)TR, g.rows - in % g.tiles * TR);
-    const uint32_t col0 = in / g.tiles * TC, depth = p.depth;
+    const uint2 tile = tile_in_group(t - g.first * col_tiles, g.tiles, col_tiles);
+    const uint32_t row0 = g.row0 + tile.x * TR, rows = min((uint32_t)TR, g.rows - tile.x * TR);
+    const uint32_t col0 = tile.y * TC, depth = p.depth;
     const size_t w_row0 = (size_t)g.expert * p.cols + col0;
 
     auto source = [&](uint32_t row) { // x's row for a row of the tile; x_rows or more: none
@@ -403,7 +403,7 @@ extern "C" tk_status tk_expert_gemm(const void* x, const void* x_scales, int x_d
     if (!x8) {
         GemmParams p{};
         p.c = static_cast<const char*>(w);
-        p.r = static_cast<const char*>(x);
+        p.r = static_cast<const char*>(x_rows ? x : w); // (no row: what is read in its place is not used)
         p.r_index = row_index;
         p.r_rows = (uint32_t)x_rows;
         p.offsets = expert_offsets;

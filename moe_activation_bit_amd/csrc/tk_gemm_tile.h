@@ -169,6 +169,17 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t block, uint32_t total)
     return i < run ? (block % kXcds) * run + i : total;
 }
 
+// (row tile, column tile) of an expert's tile: eight row tiles by all column
+// tiles at a time, rows first, so that the 32 tiles which an XCD's CUs have at
+// hand are about as many rows as columns and share them in its L2.
+__device__ __forceinline__ uint2 tile_in_group(uint32_t tile, uint32_t row_tiles, uint32_t col_tiles)
+{
+    constexpr uint32_t kHeight = 8;
+    const uint32_t band = tile / (kHeight * col_tiles), in = tile - band * (kHeight * col_tiles);
+    const uint32_t height = min(kHeight, row_tiles - band * kHeight);
+    return make_uint2(band * kHeight + in % height, in / height);
+}
+
 // 64-bit number of a tile in bounds for a launch
 inline bool launchable(uint64_t blocks, uint32_t threads) { return blocks * threads < (1ull << 32); }
 
