@@ -646,6 +646,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
                 load_codes(t + 3u);
                 find_code_rows(t + 4u);
             }
+            copies_done<0>(); // no copy outlives the workgroup's LDS
         }
 
         // ---- results: a lane has four columns of a row

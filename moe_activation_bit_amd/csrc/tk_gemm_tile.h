@@ -49,10 +49,11 @@ __device__ __forceinline__ void copy_to_lds(const char* from, const char* to)
                  : "v"(from), "s"(lds_address(to))
                  : "memory");
 }
-// ... from `base` (the same for the whole wave) + the lane's offset
+// ... from `base` (the same for the whole wave) + the lane's offset.  (A vector instruction that wrote the base,
+// which the compiler would keep five instructions before a load that it can see, may come right before this.)
 __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t offset, const char* to)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
                  : "v"(offset), "s"(base), "s"(lds_address(to))
                  : "memory");
