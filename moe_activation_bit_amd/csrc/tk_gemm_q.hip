@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "tk_gemm_host.h"
 #include "tk_gemm_tile.h"
@@ -27,7 +28,7 @@ struct Scales {
     uint32_t width; // kScaleMx: blocks of 32 k a group; kScaleStep: steps
     int kind;
     int u8;
-    int words; // kScaleMx: groups of 32 whose bytes can be read four at a time
+    int words; // kScaleMx: bytes can be read four at a time
 };
 
 struct QuantParams {
@@ -163,7 +164,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
                 if (MX && s.kind == kScaleMx) {
                     const uint8_t* const at = static_cast<const uint8_t*>(s.at) + own_row[i] * s.groups;
                     const uint32_t block = 4u * t, last = depth / 32u - 1u;
-                    if (s.words && block + 3u <= last)
+                    if (s.words && s.width == 1)
                         own_mx[i] = *reinterpret_cast<const uint32_t*>(at + block);
                     else if (s.width % 4u == 0)
                         own_mx[i] = at[t / (s.width / 4u)] * 0x01010101u;
@@ -313,12 +314,332 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
     }
 }
 
+// The same for tiles of 256 x 256 by eight waves, 64 columns x 128 rows each.  The
+// weights' fragments of a step stay in registers, the rows' go by one ahead of
+// their products.  Scales come four steps (a turn) at a time: a thread fetches
+// those of one of the 512 rows, and they meet in LDS, power-of-two ones with a
+// lane's four steps in one word, from which the instruction picks a byte.
+struct NoScale {
+    uint32_t mx;
+    float one;
+};
+__device__ const NoScale g_no_scale = {0x7F7F7F7Fu, 1.0f};
+
+template <bool W4, bool MX, bool STEP>
+__global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
+{
+    constexpr uint32_t TC = 256, TR = 256, WC = 4, kWaves = 8;
+    constexpr int kBlocks = 4; // of 16 columns a wave
+    constexpr uint32_t kRowC = W4 ? 64 : 128, kBytesC = TC * kRowC, kBytesR = TR * 128;
+    constexpr int kCopiesC = kBytesC / 1024 / kWaves, kCopies = kBytesR / 1024 / kWaves;
+    __shared__ __attribute__((aligned(1024))) char s_c[2][kBytesC];
+    __shared__ __attribute__((aligned(1024))) char s_r[2][kBytesR];
+    __shared__ __attribute__((aligned(16))) uint32_t s_mx[MX ? 2 : 1][MX ? (TC + TR) * 4 : 1];  // [row][q], four steps
+    __shared__ __attribute__((aligned(16))) float s_step[STEP ? 2 : 1][4][STEP ? TC + TR : 1]; // [step][row]
+
+    const uint32_t lane = threadIdx.x & (kWaveSize - 1), r = lane & 15u, q = lane >> 4;
+    const uint32_t wave = uniform(threadIdx.x / kWaveSize), wc = wave % WC, wr = wave / WC;
+
+    // ---- this workgroup's tile
+    const uint32_t col_tiles = (p.cols + TC - 1) / TC;
+    Group g;
+    uint32_t t0 = 0;
+    if (!find_group(p.offsets, p.experts, p.n_rows, TR,
+                    [&](uint32_t total) {
+                        t0 = xcd_tile(blockIdx.x, total * col_tiles);
+                        return t0 / col_tiles;
+                    },
+                    g))
+        return;
+    const uint2 tile = tile_in_group(t0 - g.first * col_tiles, g.tiles, col_tiles);
+    const uint32_t row0 = g.row0 + tile.x * TR, rows = min(TR, g.rows - tile.x * TR);
+    const uint32_t col0 = tile.y * TC, depth = p.depth, steps = (depth + kDepth - 1) / kDepth;
+    const size_t w_row0 = (size_t)g.expert * p.cols + col0;
+    auto source = [&](uint32_t row) { // x's row for a row of the tile; x_rows or more: none
+        const uint32_t at = row0 + min(row, rows - 1u);
+        return p.index ? (uint32_t)p.index[at] : at;
+    };
+
+    // ---- where each lane's copies come from (layouts in LDS as in gemm_q_kernel)
+    const uint32_t ld_c = W4 ? depth / 2u : depth;
+    const char* const base_c = p.w + w_row0 * ld_c;
+    const uint32_t lane_c = W4 ? (lane & 3u) ^ (-(lane >> 4) & 3u) : (lane & 7u) ^ (lane >> 3);
+    const uint32_t lane_r = (lane & 7u) ^ (lane >> 3);
+    const uint32_t k_c = lane_c * (W4 ? 32u : 16u), k_r = lane_r * 16u; // the lane's first k of a step
+    uint32_t offset_c[kCopiesC], offset_r[kCopies], row_r[kCopies];
+#pragma unroll
+    for (int i = 0; i < kCopiesC; ++i) {
+        const uint32_t row = (i * kWaves + wave) * (W4 ? 16u : 8u) + (W4 ? lane >> 2 : lane >> 3);
+        offset_c[i] = min(row, p.cols - 1u - col0) * ld_c + lane_c * 16u;
+    }
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const uint32_t at = source((i * kWaves + wave) * 8u + (lane >> 3));
+        row_r[i] = at < p.x_rows ? at : 0u; // (a row that is none: any, and zeros as its result)
+        offset_r[i] = row_r[i] * depth + k_r;
+    }
+    // FAST: whole steps whose offsets fit 32 bits; past the depth, else, zeros
+    auto copy_c = [&](auto fast, uint32_t t, uint32_t buf, int i) {
+        char* const to = s_c[buf] + (i * kWaves + wave) * 1024u;
+        if constexpr (decltype(fast)::value)
+            copy_to_lds(base_c + (size_t)t * kRowC, offset_c[i], to);
+        else
+            copy_to_lds(t * kDepth + k_c < depth ? base_c + (size_t)t * kRowC + offset_c[i] : zeros(), to);
+    };
+    auto copy_r = [&](auto fast, uint32_t t, uint32_t buf, int i) {
+        char* const to = s_r[buf] + (i * kWaves + wave) * 1024u;
+        if constexpr (decltype(fast)::value)
+            copy_to_lds(p.x + (size_t)t * 128u, offset_r[i], to);
+        else
+            copy_to_lds(t * kDepth + k_r < depth ? p.x + (size_t)row_r[i] * depth + t * kDepth + k_r : zeros(), to);
+    };
+
+    // ---- scales: thread i has those of row i of the weights, or of row i - TC of x.  Every kind is read by the same
+    // loads, those that there are not from a constant: a branch here would draw the products behind it.
+    const bool weights = threadIdx.x < TC;
+    const Scales& own = weights ? p.ws : p.xs;
+    size_t own_row = 0;
+    if constexpr (MX || STEP) {
+        if (weights) {
+            own_row = w_row0 + min(threadIdx.x, p.cols - 1u - col0);
+        } else {
+            const uint32_t at = source(threadIdx.x - TC);
+            own_row = at < p.x_rows ? at : 0u;
+        }
+    }
+    const bool is_mx = MX && own.kind == kScaleMx, by_block = is_mx && own.width == 1;
+    const char* const own_mx = is_mx ? static_cast<const char*>(own.at) + own_row * own.groups
+                                     : reinterpret_cast<const char*>(&g_no_scale.mx);
+    const uint32_t mx_turn = by_block ? 16u : is_mx ? 4u : 0u, mx_last = is_mx ? own.groups - 4u : 0u;
+    const bool is_step = STEP && own.kind == kScaleStep;
+    const float* const own_step = is_step ? static_cast<const float*>(own.at) + own_row * own.groups : &g_no_scale.one;
+    const uint32_t step_magic = is_step ? (1u << 31) / own.width : 0u;
+    uint32_t turn_mx[4];
+    float turn_step[4];
+    auto fetch_scales = [&](uint32_t turn) { // of steps 4 turn ..
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            if constexpr (MX)
+                turn_mx[i] = *reinterpret_cast<const uint32_t*>(own_mx + min(turn * mx_turn + (by_block ? 4u * i : 0u), mx_last));
+            if constexpr (STEP) // (2 s + 1) floor(2^31 / width) / 2^32, rounded down, is s / width
+                turn_step[i] = own_step[__umulhi(2u * min(4u * turn + i, steps - 1u) + 1u, step_magic)];
+        }
+    };
+    auto put_scales = [&](uint32_t buf) {
+        if constexpr (MX) {
+            // a word a step with a byte for each q -> a word for each q with a byte a step
+            const uint32_t a = __builtin_amdgcn_perm(turn_mx[1], turn_mx[0], 0x05010400u);
+            const uint32_t b = __builtin_amdgcn_perm(turn_mx[3], turn_mx[2], 0x05010400u);
+            const uint32_t c = __builtin_amdgcn_perm(turn_mx[1], turn_mx[0], 0x07030602u);
+            const uint32_t d = __builtin_amdgcn_perm(turn_mx[3], turn_mx[2], 0x07030602u);
+            const v4u v = {by_block ? __builtin_amdgcn_perm(b, a, 0x05040100u) : turn_mx[0],
+                           by_block ? __builtin_amdgcn_perm(b, a, 0x07060302u) : turn_mx[0],
+                           by_block ? __builtin_amdgcn_perm(d, c, 0x05040100u) : turn_mx[0],
+                           by_block ? __builtin_amdgcn_perm(d, c, 0x07060302u) : turn_mx[0]};
+            *reinterpret_cast<v4u*>(s_mx[buf] + threadIdx.x * 4u) = v;
+        }
+        if constexpr (STEP)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s_step[buf][i][threadIdx.x] = turn_step[i];
+    };
+
+    auto join = [](v4u lo, v4u hi) {
+        return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    auto read_c = [&](uint32_t buf, int i) { // FP8: a lane's k are 16q .. and 64 + 16q .., FP4: 32q ..
+        const uint32_t row = 16u * (wc * kBlocks + i) + r;
+        if constexpr (W4) {
+            const v4u v = *reinterpret_cast<const v4u*>(s_c[buf] + row * 64u + (q ^ (-(r >> 2) & 3u)) * 16u);
+            return join(v, v4u{0, 0, 0, 0});
+        } else {
+            const char* const at = s_c[buf] + row * 128u;
+            return join(*reinterpret_cast<const v4u*>(at + (q ^ (r & 7u)) * 16u),
+                        *reinterpret_cast<const v4u*>(at + ((q + 4u) ^ (r & 7u)) * 16u));
+        }
+    };
+    auto row_of = [&](int j) { return 16u * (2u * j + wr); }; // every second block: few rows are shared evenly
+    auto read_r = [&](uint32_t buf, int j) {
+        const char* const at = s_r[buf] + (row_of(j) + r) * 128u;
+        return join(*reinterpret_cast<const v4u*>(at + (q ^ (r & 7u)) * 16u),
+                    *reinterpret_cast<const v4u*>(at + ((q + 4u) ^ (r & 7u)) * 16u));
+    };
+
+    auto run = [&](auto n_blocks, auto fast) {
+        constexpr int N = decltype(n_blocks)::value, kCopiesR = N / 2;
+        v4f acc[kBlocks][N];
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t a_mx[kBlocks], b_mx[N]; // four steps' scales of a lane
+#pragma unroll
+        for (int n = 0; n < kCopiesC; ++n)
+            copy_c(fast, 0, 0, n);
+#pragma unroll
+        for (int n = 0; n < kCopiesR; ++n)
+            copy_r(fast, 0, 0, n);
+        fetch_scales(0);
+        put_scales(0);
+        auto step = [&](auto number, uint32_t t) { // step t, number t % 4 of its turn
+            constexpr int u = decltype(number)::value;
+            const uint32_t buf = t & 1u, turn = t / 4u;
+            copies_done<0>();
+            __syncthreads(); // step t is there, and nobody reads step t - 1 any more
+            const uint32_t next = min(t + 1u, steps - 1u); // (past the last step that one again, unused)
+            if constexpr (MX) {
+                if constexpr (u == 0) {
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+                        a_mx[i] = s_mx[turn & 1u][(16u * (wc * kBlocks + i) + r) * 4u + q];
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        b_mx[j] = s_mx[turn & 1u][(TC + row_of(j) + r) * 4u + q];
+                }
+            }
+            v8i a[kBlocks], b = read_r(buf, 0);
+            v4f a_step[kBlocks];
+            float b_step = STEP ? s_step[turn & 1u][u][TC + row_of(0) + r] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                a[i] = read_c(buf, i);
+                a_step[i] = STEP ? *reinterpret_cast<const v4f*>(&s_step[turn & 1u][u][16u * (wc * kBlocks + i) + 4u * q])
+                                 : v4f{1.0f, 1.0f, 1.0f, 1.0f};
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                __builtin_amdgcn_sched_barrier(0);
+                const v8i now = b;
+                const float now_step = b_step;
+                if (j + 1 < N) {
+                    b = read_r(buf, j + 1);
+                    b_step = STEP ? s_step[turn & 1u][u][TC + row_of(j + 1) + r] : 1.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) {
+                    const v4f c = STEP ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
+                    const v4f d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        a[i], now, c, W4 ? 4 : 0, 0, MX ? u : 0, MX ? (int)a_mx[i] : 127, MX ? u : 0,
+                        MX ? (int)b_mx[j] : 127);
+                    if constexpr (STEP) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][j][e] = __builtin_fmaf(d[e], a_step[i][e] * now_step, acc[i][j][e]);
+                    } else {
+                        acc[i][j] = d;
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int n = 0; n < kCopiesC + kCopiesR; ++n) // spread over the row blocks
+                    if (n * N / (kCopiesC + kCopiesR) == j) {
+                        if (n < kCopiesC)
+                            copy_c(fast, next, buf ^ 1u, n);
+                        else
+                            copy_r(fast, next, buf ^ 1u, n - kCopiesC);
+                    }
+            }
+            if constexpr (STEP) // (the sums are done with here: left to the compiler, products move behind the branch)
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+                        asm volatile("" : "+v"(acc[i][j]));
+            // the next turn's scales, fetched during one step and put in place during the next
+            if constexpr (u == 1)
+                fetch_scales(turn + 1u);
+            if constexpr (u == 2)
+                put_scales((turn + 1u) & 1u);
+        };
+        using std::integral_constant;
+#pragma clang loop unroll(disable) // (nor peeled)
+        for (uint32_t t = 0; t < steps; t += 4) {
+            step(integral_constant<int, 0>{}, t);
+            if (t + 1u < steps)
+                step(integral_constant<int, 1>{}, t + 1u);
+            if (t + 2u < steps)
+                step(integral_constant<int, 2>{}, t + 2u);
+            if (t + 3u < steps)
+                step(integral_constant<int, 3>{}, t + 3u);
+        }
+        copies_done<0>(); // no copy outlives the workgroup's LDS
+
+        // ---- whole rows' scales, and the results: a lane has four columns of a row
+        auto row_scale = [](const Scales& s, size_t row) {
+            return s.kind != kScaleRow ? 1.0f
+                   : s.u8              ? e8m0_value(static_cast<const uint8_t*>(s.at)[row])
+                                       : static_cast<const float*>(s.at)[row];
+        };
+        float c_scale[kBlocks][4];
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+                c_scale[i][e] = row_scale(p.ws, w_row0 + min(16u * (wc * kBlocks + i) + 4u * q + e, p.cols - 1u - col0));
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint32_t row = row_of(j) + r;
+            if (row >= rows)
+                continue;
+            const uint32_t at = source(row);
+            const bool none = at >= p.x_rows;
+            const float r_scale = none ? 0.0f : row_scale(p.xs, at);
+            const size_t line = (size_t)(row0 + row) * p.cols;
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                const uint32_t col = col0 + 16u * (wc * kBlocks + i) + 4u * q;
+                if (col >= p.cols)
+                    continue;
+                v4b v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = (__bf16)(none ? 0.0f : acc[i][j][e] * r_scale * c_scale[i][e]);
+                *reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + line + col) = v;
+            }
+        }
+    };
+    using std::bool_constant;
+    using std::integral_constant;
+    auto run_blocks = [&](auto fast) {
+        const uint32_t blocks = uniform((rows + 31u) / 32u);
+        if (blocks > 6)
+            run(integral_constant<int, 8>{}, fast);
+        else if (blocks > 4)
+            run(integral_constant<int, 6>{}, fast);
+        else if (blocks > 2)
+            run(integral_constant<int, 4>{}, fast);
+        else
+            run(integral_constant<int, 2>{}, fast);
+    };
+    if (depth % kDepth == 0 && (uint64_t)p.x_rows * depth < (1ull << 32))
+        run_blocks(bool_constant<true>{});
+    else
+        run_blocks(bool_constant<false>{});
+}
+
+// At most how many tiles of tr rows by tc columns there are, however the rows lie, in workgroups of whole turns over
+// the XCDs.
+uint64_t workgroups(const QuantParams& p, uint32_t tc, uint32_t tr)
+{
+    const uint64_t col_tiles = ((uint64_t)p.cols + tc - 1) / tc, most = p.n_rows < p.experts ? p.n_rows : p.experts;
+    return ((p.n_rows / tr + most) * col_tiles + kXcds - 1) / kXcds * kXcds;
+}
+
+template <bool W4, bool MX, bool STEP>
+tk_status launch_big(const QuantParams& p, hipStream_t s)
+{
+    const uint64_t blocks = workgroups(p, 256, 256);
+    if (!launchable(blocks, 512))
+        return TK_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((gemm_q_big_kernel<W4, MX, STEP>), dim3((uint32_t)blocks), dim3(512), 0, s, p);
+    return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
+}
+
 template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
 tk_status launch(const QuantParams& p, hipStream_t s)
 {
-    const uint64_t col_tiles = ((uint64_t)p.cols + TC - 1) / TC;
-    const uint64_t most = p.n_rows < p.experts ? p.n_rows : p.experts;
-    const uint64_t blocks = ((p.n_rows / TR + most) * col_tiles + kXcds - 1) / kXcds * kXcds;
+    const uint64_t blocks = workgroups(p, TC, TR);
     if (!launchable(blocks, 64 * WC * WR))
         return TK_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((gemm_q_kernel<W4, MX, STEP, TC, TR, WC, WR>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0, s,
@@ -330,8 +651,10 @@ template <bool W4, bool MX, bool STEP>
 tk_status launch_size(const QuantParams& p, hipStream_t s)
 {
     const uint32_t load = p.n_rows / p.experts; // an expert's rows on average
-    if (load >= 128)
-        return launch<W4, MX, STEP, 256, 256, 2, 4>(p, s);
+    // (the large tiles take the scales of 32 and of 128 columns, four steps' at a time)
+    auto turns = [](const Scales& a) { return a.kind != kScaleMx || (a.words && (a.width == 1 || a.width == 4)); };
+    if (load >= 128 && turns(p.ws) && turns(p.xs))
+        return launch_big<W4, MX, STEP>(p, s);
     if (load >= 32)
         return launch<W4, MX, STEP, 128, 64, 2, 2>(p, s);
     return launch<W4, MX, STEP, 64, 16, 4, 1>(p, s);
@@ -352,7 +675,7 @@ bool scales_of(const void* at, int fmt, int64_t group, int64_t depth, Scales& s)
     s.kind = s.u8 ? kScaleMx : kScaleStep;
     s.groups = (uint32_t)(depth / group);
     s.width = (uint32_t)(group / (s.u8 ? 32 : 128));
-    s.words = s.u8 && s.width == 1 && s.groups % 4 == 0 && aligned(at, 4);
+    s.words = s.u8 && s.groups % 4 == 0 && aligned(at, 4);
     return true;
 }
 
@@ -417,7 +740,7 @@ extern "C" tk_status tk_expert_gemm(const void* x, const void* x_scales, int x_d
     }
     QuantParams p{};
     p.w = static_cast<const char*>(w);
-    p.x = static_cast<const char*>(x);
+    p.x = static_cast<const char*>(x_rows ? x : w); // (no row: what is read in its place is not used)
     p.index = row_index;
     p.offsets = expert_offsets;
     p.out = out;
@@ -428,6 +751,8 @@ extern "C" tk_status tk_expert_gemm(const void* x, const void* x_scales, int x_d
     p.experts = (uint32_t)experts;
     p.cols = (uint32_t)out_features;
     p.depth = (uint32_t)in_features;
+    if (x_rows == 0) // nor are there scales
+        p.xs.kind = kScaleRow;
     const bool mx = xs.kind == kScaleMx || ws.kind == kScaleMx, step = xs.kind == kScaleStep || ws.kind == kScaleStep;
     if (w4)
         return mx ? (step ? launch_size<true, true, true>(p, s) : launch_size<true, true, false>(p, s))
