@@ -653,16 +653,27 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const uint32_t row = 16u * (2u * j + wr) + r;
-            if (row >= rows)
-                continue;
-            const bool none = KIND != kWgrad && p.r_index && (uint32_t)p.r_index[row0 + row] >= p.r_rows;
+            const bool none = KIND != kWgrad && p.r_index && row < rows && (uint32_t)p.r_index[row0 + row] >= p.r_rows;
             const size_t line = ((size_t)(KIND == kWgrad ? expert * (size_t)p.out_rows : 0u) + row0 + row) * p.cols;
+            if (none)
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i)
+                    acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            if (p.out_bf16 && !(KIND == kWgrad && p.accumulate)) { // the same for every thread
+#pragma unroll
+                for (int i = 0; i < kBlocks; i += 2) {
+                    const v4u v = pair_columns(acc[i][j], acc[i + 1][j]);
+                    const uint32_t col = col0 + 16u * (wc * kBlocks + i + (q & 1u)) + 8u * (q >> 1);
+                    if (row < rows && col < p.cols)
+                        *reinterpret_cast<v4u*>(static_cast<__bf16*>(p.out) + line + col) = v;
+                }
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
                 const uint32_t col = col0 + 16u * (wc * kBlocks + i) + 4u * q;
-                if (col >= p.cols)
-                    continue;
-                store_result<KIND == kWgrad>(p, line + col, none ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j]);
+                if (row < rows && col < p.cols)
+                    store_result<KIND == kWgrad>(p, line + col, acc[i][j]);
             }
         }
     };

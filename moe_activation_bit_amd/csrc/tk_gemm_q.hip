@@ -507,6 +507,15 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
                 a_step[i] = STEP ? *reinterpret_cast<const v4f*>(&s_step[turn & 1u][u][16u * (wc * kBlocks + i) + 4u * q])
                                  : v4f{1.0f, 1.0f, 1.0f, 1.0f};
             }
+            v4f before[kBlocks];
+            float before_step = 0.0f;
+            auto add_step = [&](int j, const v4f(&d)[kBlocks], float r_step) {
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][j][e] = __builtin_fmaf(d[i][e], a_step[i][e] * r_step, acc[i][j][e]);
+            };
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -516,19 +525,23 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
                     b = read_r(buf, j + 1);
                     b_step = STEP ? s_step[turn & 1u][u][TC + row_of(j + 1) + r] : 1.0f;
                 }
+                v4f d[kBlocks];
 #pragma unroll
                 for (int i = 0; i < kBlocks; ++i) {
                     const v4f c = STEP ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
-                    const v4f d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        a[i], now, c, W4 ? 4 : 0, 0, MX ? u : 0, MX ? (int)a_mx[i] : 127, MX ? u : 0,
-                        MX ? (int)b_mx[j] : 127);
-                    if constexpr (STEP) {
+                    d[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], now, c, W4 ? 4 : 0, 0, MX ? u : 0,
+                                                                            MX ? (int)a_mx[i] : 127, MX ? u : 0,
+                                                                            MX ? (int)b_mx[j] : 127);
+                    if constexpr (!STEP)
+                        acc[i][j] = d[i];
+                }
+                if constexpr (STEP) { // the block before this one's, under this one's products
+                    if (j > 0)
+                        add_step(j - 1, before, before_step);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[i][j][e] = __builtin_fmaf(d[e], a_step[i][e] * now_step, acc[i][j][e]);
-                    } else {
-                        acc[i][j] = d;
-                    }
+                    for (int i = 0; i < kBlocks; ++i)
+                        before[i] = d[i];
+                    before_step = now_step;
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -540,12 +553,14 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
                             copy_r(fast, next, buf ^ 1u, n - kCopiesC);
                     }
             }
-            if constexpr (STEP) // (the sums are done with here: left to the compiler, products move behind the branch)
+            if constexpr (STEP) { // (the sums are done with here: left to the compiler, products move behind the branch)
+                add_step(N - 1, before, before_step);
 #pragma unroll
                 for (int j = 0; j < N; ++j)
 #pragma unroll
                     for (int i = 0; i < kBlocks; ++i)
                         asm volatile("" : "+v"(acc[i][j]));
+            }
             // the next turn's scales, fetched during one step and put in place during the next
             if constexpr (u == 1)
                 fetch_scales(turn + 1u);
@@ -565,7 +580,7 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
         }
         copies_done<0>(); // no copy outlives the workgroup's LDS
 
-        // ---- whole rows' scales, and the results: a lane has four columns of a row
+        // ---- whole rows' scales, and the results
         auto row_scale = [](const Scales& s, size_t row) {
             return s.kind != kScaleRow ? 1.0f
                    : s.u8              ? e8m0_value(static_cast<const uint8_t*>(s.at)[row])
@@ -579,23 +594,22 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
                 c_scale[i][e] = row_scale(p.ws, w_row0 + min(16u * (wc * kBlocks + i) + 4u * q + e, p.cols - 1u - col0));
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const uint32_t row = row_of(j) + r;
-            if (row >= rows)
-                continue;
-            const uint32_t at = source(row);
+            const uint32_t row = row_of(j) + r, at = source(row);
             const bool none = at >= p.x_rows;
             const float r_scale = none ? 0.0f : row_scale(p.xs, at);
             const size_t line = (size_t)(row0 + row) * p.cols;
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i) {
-                const uint32_t col = col0 + 16u * (wc * kBlocks + i) + 4u * q;
-                if (col >= p.cols)
-                    continue;
-                v4b v;
+            for (int i = 0; i < kBlocks; i += 2) {
+                v4f v[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = (__bf16)(none ? 0.0f : acc[i][j][e] * r_scale * c_scale[i][e]);
-                *reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + line + col) = v;
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[h][e] = none ? 0.0f : acc[i + h][j][e] * r_scale * c_scale[i + h][e];
+                const v4u pair = pair_columns(v[0], v[1]);
+                const uint32_t col = col0 + 16u * (wc * kBlocks + i + (q & 1u)) + 8u * (q >> 1);
+                if (row < rows && col < p.cols)
+                    *reinterpret_cast<v4u*>(static_cast<__bf16*>(p.out) + line + col) = pair;
             }
         }
     };

@@ -72,6 +72,19 @@ __device__ __forceinline__ uint32_t fp8_to_bf16(uint32_t codes, float scale)
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, UPPER));
 }
 
+// Results of a row, x of block i and y of block i + 1, four columns a lane (4q ..)
+// -> eight columns a lane in bf16: 8 (q / 2) .. of block i + (q & 1).  Lanes whose
+// q differ in the lowest bit exchange a half, so that a row's 64 bytes are
+// stored together.
+__device__ __forceinline__ v4u pair_columns(v4f x, v4f y)
+{
+    typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+    auto pack = [](float a, float b) { return __builtin_bit_cast(uint32_t, v2b{(__bf16)a, (__bf16)b}); };
+    const auto lo = __builtin_amdgcn_permlane16_swap(pack(x[0], x[1]), pack(y[0], y[1]), false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(pack(x[2], x[3]), pack(y[2], y[3]), false, false);
+    return v4u{lo[0], hi[0], lo[1], hi[1]};
+}
+
 // A number that is the same for the whole wave, in a scalar register
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
