@@ -347,7 +347,8 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
 // and the next one is in LDS); while the second half is multiplied, the next
 // step's first fragments are read and the step after that is copied over this
 // one.
-template <int KIND, bool X8>
+// X8: x in FP8 (wgrad).  XI, DI: wgrad's rows of x and of dy are found by an index.
+template <int KIND, bool X8, bool XI, bool DI>
 __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
 {
     constexpr uint32_t TC = 256, TR = 256, kWaves = 8;
@@ -414,6 +415,11 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
         const uint32_t s = lane & 31u;
         return (((s >> 1) ^ hash(k_of(i))) * 2u + (s & 1u)) * 8u;
     };
+    auto wgrad_offset_r = [&](int i, uint32_t ln) {
+        const uint32_t k = (i * kWaves + wave) * 2u + (ln >> 5), sl = ln & 31u;
+        const uint32_t col = row0 + (((sl >> 1) ^ hash(k)) * 2u + (sl & 1u)) * 8u;
+        return (DI ? 0u : k * ld_r) + (col < p.out_rows ? col : 0u) * 2u; // (columns past the last are not stored)
+    };
     uint32_t offset_c[kCopies], offset_r[kCopies], row_r[kCopies];
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
@@ -423,7 +429,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
         } else {
             uint32_t col = col0 + col_of(i);
             col = col < p.cols ? col : 0u; // not stored
-            offset_c[i] = (KIND == kDgrad ? k_of(i) * ld_c : 0u) + col * 2u;
+            offset_c[i] = (KIND == kDgrad || !XI ? k_of(i) * ld_c : 0u) + col * 2u;
         }
         if constexpr (!kRT) {
             uint32_t at = row0 + min(row, rows - 1u);
@@ -432,25 +438,22 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
             row_r[i] = at < p.r_rows ? at : 0u; // (a row that is none: any, and zeros as its result)
             offset_r[i] = row_r[i] * ld_r + row_k * 2u;
         } else {
-            const uint32_t col = row0 + col_of(i);
-            offset_r[i] = (col < p.out_rows ? col : 0u) * 2u;
+            offset_r[i] = wgrad_offset_r(i, lane);
         }
     }
 
-    // wgrad: the row of x or dy for the expert's row k, to be looked at only when it is used: until then it may
-    // be on its way
-    auto source = [&](const int32_t* index, uint32_t k) -> uint32_t {
-        const uint32_t at = row_base + min(k, depth - 1u);
-        return index ? (uint32_t)index[at] : at;
-    };
+    // wgrad: the row of x or dy for the expert's row k by its index, to be looked at only when it is used: until then
+    // it may be on its way
+    auto indexed = [&](const int32_t* index, uint32_t k) { return (uint32_t)index[row_base + min(k, depth - 1u)]; };
     uint32_t next_c[kCopies], next_r[kCopies], next_x[kCodes]; // of the coming copies
     auto find_rows = [&](uint32_t t) {
-        if constexpr (KIND == kWgrad) {
+        if constexpr (KIND == kWgrad && (DI || (XI && !X8))) {
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
-                if constexpr (!X8)
-                    next_c[i] = source(p.c_index, t * kDepth + k_of(i));
-                next_r[i] = source(p.r_index, t * kDepth + k_of(i));
+                if constexpr (XI && !X8)
+                    next_c[i] = indexed(p.c_index, t * kDepth + k_of(i));
+                if constexpr (DI)
+                    next_r[i] = indexed(p.r_index, t * kDepth + k_of(i));
             }
         }
     };
@@ -461,18 +464,20 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
     v4u codes[kCodes];
     uint8_t scale0[kCodes], scale1[kCodes];
     auto find_code_rows = [&](uint32_t t) {
-        if constexpr (X8)
+        if constexpr (X8 && XI)
 #pragma unroll
             for (int i = 0; i < kCodes; ++i)
-                next_x[i] = source(p.c_index, t * kDepth + i * 32u + code_k);
+                next_x[i] = indexed(p.c_index, t * kDepth + i * 32u + code_k);
     };
+    bool code_in[kCodes];
     auto load_codes = [&](uint32_t t) {
         if constexpr (X8)
 #pragma unroll
             for (int i = 0; i < kCodes; ++i) {
-                const bool in = next_x[i] < p.c_rows && t * kDepth + i * 32u + code_k < depth;
-                const size_t row = in ? next_x[i] : 0u;
-                codes[i] = *reinterpret_cast<const v4u*>(in ? p.c + row * ld_c + code_col : zeros());
+                const uint32_t k = t * kDepth + i * 32u + code_k, at = XI ? next_x[i] : row_base + min(k, depth - 1u);
+                code_in[i] = k < depth && at < p.c_rows;
+                const size_t row = at < p.c_rows ? at : 0u;
+                codes[i] = *reinterpret_cast<const v4u*>(p.c + row * ld_c + code_col);
                 const uint8_t* const sc = p.c_scales + row * p.c_groups;
                 scale0[i] = sc[code_g0];
                 scale1[i] = sc[code_g1];
@@ -480,8 +485,8 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
     };
     auto put_codes = [&](int i, uint32_t buf) { // as bf16 numbers, with their power-of-two scales
         if constexpr (X8) {
-            const uint32_t k = i * 32u + code_k;
-            const uint32_t word[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+            const uint32_t k = i * 32u + code_k, keep = code_in[i] ? ~0u : 0u;
+            const uint32_t word[4] = {codes[i].x & keep, codes[i].y & keep, codes[i].z & keep, codes[i].w & keep};
             char* const to = s_c[buf] + k * (TC * 2u) + (code_s ^ hash(k)) * 32u;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -496,34 +501,38 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
     // Copy i of an operand's step t.  FAST: whole steps whose offsets fit 32 bits, from a base that is the same for
     // the whole wave (past the last step that one again, unused); else past the depth, and for rows that are none,
     // zeros.
+    auto row_of_copy = [&](bool by_index, const char* base, uint32_t at, uint32_t all, uint32_t ld, uint32_t t, int i,
+                           uint32_t offset) -> const char* { // wgrad; offset: of the column, and of the row in the step
+        const uint32_t k = t * kDepth + k_of(i);
+        if (by_index)
+            return at < all && k < depth ? base + (size_t)at * ld + offset : zeros();
+        return k < depth ? base + (size_t)(row_base + t * kDepth) * ld + here(offset) : zeros();
+    };
     auto copy_c = [&](auto fast, uint32_t t, uint32_t buf, int i) {
         char* const to = s_c[buf] + (i * kWaves + wave) * 1024u;
         if constexpr (KIND == kWgrad) {
             if constexpr (!X8)
-                copy_to_lds(next_c[i] < p.c_rows && t * kDepth + k_of(i) < depth
-                                ? p.c + (size_t)next_c[i] * ld_c + offset_c[i]
-                                : zeros(),
-                            to);
+                copy_to_lds(row_of_copy(XI, p.c, next_c[i], p.c_rows, ld_c, t, i, offset_c[i]), to);
         } else {
             const uint32_t u = decltype(fast)::value ? min(t, steps - 1u) : t, k = t * kDepth + (kCT ? k_of(i) : row_k);
             const size_t step = kCT ? (size_t)u * kDepth * ld_c : (size_t)u * (kDepth * 2u);
             if constexpr (decltype(fast)::value)
                 copy_to_lds(base_c + step, offset_c[i], to);
             else
-                copy_to_lds(k < depth ? base_c + step + offset_c[i] : zeros(), to);
+                copy_to_lds(k < depth ? base_c + step + here(offset_c[i]) : zeros(), to);
         }
     };
     auto copy_r = [&](auto fast, uint32_t t, uint32_t buf, int i) {
         char* const to = s_r[buf] + (i * kWaves + wave) * 1024u;
         if constexpr (KIND == kWgrad) {
-            copy_to_lds(next_r[i] < p.r_rows && t * kDepth + k_of(i) < depth
-                            ? p.r + (size_t)next_r[i] * ld_r + offset_r[i]
-                            : zeros(),
+            // X8: computed again each time, its registers are full
+            copy_to_lds(row_of_copy(DI, p.r, next_r[i], p.r_rows, ld_r, t, i,
+                                    X8 ? wgrad_offset_r(i, here(lane)) : offset_r[i]),
                         to);
         } else if constexpr (decltype(fast)::value) {
             copy_to_lds(p.r + (size_t)min(t, steps - 1u) * (kDepth * 2u), offset_r[i], to);
         } else {
-            copy_to_lds(t * kDepth + row_k < depth ? p.r + (size_t)row_r[i] * ld_r + (t * kDepth + row_k) * 2u : zeros(),
+            copy_to_lds(t * kDepth + row_k < depth ? p.r + (size_t)here(row_r[i]) * ld_r + (t * kDepth + row_k) * 2u : zeros(),
                         to);
         }
     };
@@ -719,13 +728,13 @@ tk_status launch(const GemmParams& p, hipStream_t s)
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
 
-template <int KIND, bool X8 = false>
+template <int KIND, bool X8 = false, bool XI = false, bool DI = false>
 tk_status launch_big(const GemmParams& p, hipStream_t s)
 {
     const uint64_t blocks = workgroups<KIND>(p, 256, 256);
     if (!launchable(blocks, 512))
         return TK_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((gemm_big_kernel<KIND, X8>), dim3((uint32_t)blocks), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((gemm_big_kernel<KIND, X8, XI, DI>), dim3((uint32_t)blocks), dim3(512), 0, s, p);
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
 
@@ -814,6 +823,8 @@ extern "C" tk_status tk_expert_gemm_wgrad(const void* dy, int64_t dy_rows, const
         overlaps_rows(dw, o_bytes, dy_index, expert_offsets, n_rows, experts) ||
         overlaps_rows(dw, o_bytes, x_index, nullptr, n_rows, experts))
         return TK_ERR_INVALID_ARG;
+    if (dy_rows == 0 || x_rows == 0) // every row stands for zeros
+        n_rows = 0;
     if (n_rows == 0 && accumulate)
         return TK_OK;
     GemmParams p{};
@@ -835,8 +846,13 @@ extern "C" tk_status tk_expert_gemm_wgrad(const void* dy, int64_t dy_rows, const
     p.out_bf16 = out_bf16;
     p.accumulate = accumulate;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (p.out_rows >= 192 && p.cols >= 192)
-        return fp8 ? launch_big<kWgrad, true>(p, s) : launch_big<kWgrad>(p, s);
+    if (p.out_rows >= 192 && p.cols >= 192) {
+        if (fp8)
+            return x_index ? (dy_index ? launch_big<kWgrad, true, true, true>(p, s) : launch_big<kWgrad, true, true>(p, s))
+                           : (dy_index ? launch_big<kWgrad, true, false, true>(p, s) : launch_big<kWgrad, true>(p, s));
+        return x_index ? (dy_index ? launch_big<kWgrad, false, true, true>(p, s) : launch_big<kWgrad, false, true>(p, s))
+                       : (dy_index ? launch_big<kWgrad, false, false, true>(p, s) : launch_big<kWgrad>(p, s));
+    }
     if (fp8)
         return launch<kWgrad, 128, 128, 2, 2, true>(p, s);
     return launch<kWgrad, 128, 128, 2, 2>(p, s);

@@ -85,6 +85,14 @@ __device__ __forceinline__ v4u pair_columns(v4f x, v4f y)
     return v4u{lo[0], hi[0], lo[1], hi[1]};
 }
 
+// x, opaque to the compiler: what is derived from it inside a loop stays there
+// instead of being computed before the loop and held (or spilled) through it
+__device__ __forceinline__ uint32_t here(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // A number that is the same for the whole wave, in a scalar register
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
