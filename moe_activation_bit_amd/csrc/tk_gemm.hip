@@ -460,9 +460,9 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
     // X8: a thread takes the 16 codes s of the rows i * 32 + threadIdx / 16
     const uint32_t code_s = threadIdx.x & 15u, code_k = threadIdx.x >> 4;
     const uint32_t code_col = X8 && col0 + code_s * 16u < p.cols ? col0 + code_s * 16u : 0u;
-    const uint32_t code_g0 = X8 ? code_col / p.c_group : 0u, code_g1 = X8 ? (code_col + 8u) / p.c_group : 0u;
+    const uint32_t code_g = X8 ? code_col / p.c_group : 0u; // (a group is 16 columns or a multiple)
     v4u codes[kCodes];
-    uint8_t scale0[kCodes], scale1[kCodes];
+    uint8_t code_scale[kCodes];
     auto find_code_rows = [&](uint32_t t) {
         if constexpr (X8 && XI)
 #pragma unroll
@@ -478,9 +478,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
                 code_in[i] = k < depth && at < p.c_rows;
                 const size_t row = at < p.c_rows ? at : 0u;
                 codes[i] = *reinterpret_cast<const v4u*>(p.c + row * ld_c + code_col);
-                const uint8_t* const sc = p.c_scales + row * p.c_groups;
-                scale0[i] = sc[code_g0];
-                scale1[i] = sc[code_g1];
+                code_scale[i] = p.c_scales[row * p.c_groups + code_g];
             }
     };
     auto put_codes = [&](int i, uint32_t buf) { // as bf16 numbers, with their power-of-two scales
@@ -488,13 +486,12 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
             const uint32_t k = i * 32u + code_k, keep = code_in[i] ? ~0u : 0u;
             const uint32_t word[4] = {codes[i].x & keep, codes[i].y & keep, codes[i].z & keep, codes[i].w & keep};
             char* const to = s_c[buf] + k * (TC * 2u) + (code_s ^ hash(k)) * 32u;
+            const float scale = as_float((uint32_t)code_scale[i] << 23);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float scale = as_float((uint32_t)(h ? scale1[i] : scale0[i]) << 23);
+            for (int h = 0; h < 2; ++h)
                 *reinterpret_cast<uint4*>(to + 16 * h) =
                     make_uint4(fp8_to_bf16<false>(word[2 * h], scale), fp8_to_bf16<true>(word[2 * h], scale),
                                fp8_to_bf16<false>(word[2 * h + 1], scale), fp8_to_bf16<true>(word[2 * h + 1], scale));
-            }
         }
     };
 
@@ -846,7 +843,7 @@ extern "C" tk_status tk_expert_gemm_wgrad(const void* dy, int64_t dy_rows, const
     p.out_bf16 = out_bf16;
     p.accumulate = accumulate;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (p.out_rows >= 192 && p.cols >= 192) {
+    if (p.out_rows >= 192 && p.cols >= 192 && (!fp8 || group % 16 == 0)) {
         if (fp8)
             return x_index ? (dy_index ? launch_big<kWgrad, true, true, true>(p, s) : launch_big<kWgrad, true, true>(p, s))
                            : (dy_index ? launch_big<kWgrad, true, false, true>(p, s) : launch_big<kWgrad, true>(p, s));
