@@ -314,10 +314,10 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
     }
 }
 
-// The same for tiles of 256 x 256 by eight waves, 64 columns x 128 rows each.  The
+// The same where the scales' groups are 32 or 128 columns (or there are none).  The
 // weights' fragments of a step stay in registers, the rows' go by one ahead of
 // their products.  Scales come four steps (a turn) at a time: a thread fetches
-// those of one of the 512 rows, and they meet in LDS, power-of-two ones with a
+// those of one of the tile's rows, and they meet in LDS, power-of-two ones with a
 // lane's four steps in one word, from which the instruction picks a byte.
 struct NoScale {
     uint32_t mx;
@@ -325,17 +325,19 @@ struct NoScale {
 };
 __device__ const NoScale g_no_scale = {0x7F7F7F7Fu, 1.0f};
 
-template <bool W4, bool MX, bool STEP>
-__global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
+template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
+__global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p)
 {
-    constexpr uint32_t TC = 256, TR = 256, WC = 4, kWaves = 8;
-    constexpr int kBlocks = 4; // of 16 columns a wave
+    constexpr uint32_t kWaves = WC * WR, kThr = 64 * kWaves;
+    constexpr int kBlocks = TC / WC / 16, kRowBlocks = TR / WR / 16; // of 16 columns and of 16 rows a wave
+    static_assert(TC + TR <= (int)kThr, "a thread for each row's scales");
     constexpr uint32_t kRowC = W4 ? 64 : 128, kBytesC = TC * kRowC, kBytesR = TR * 128;
-    constexpr int kCopiesC = kBytesC / 1024 / kWaves, kCopies = kBytesR / 1024 / kWaves;
+    constexpr int kCopiesC = (kBytesC / 1024 + kWaves - 1) / kWaves, kCopies = (kBytesR / 1024 + kWaves - 1) / kWaves;
+    constexpr bool kEvenC = kBytesC / 1024 % kWaves == 0, kEvenR = kBytesR / 1024 % kWaves == 0;
     __shared__ __attribute__((aligned(1024))) char s_c[2][kBytesC];
     __shared__ __attribute__((aligned(1024))) char s_r[2][kBytesR];
-    __shared__ __attribute__((aligned(16))) uint32_t s_mx[MX ? 2 : 1][MX ? (TC + TR) * 4 : 1];  // [row][q], four steps
-    __shared__ __attribute__((aligned(16))) float s_step[STEP ? 2 : 1][4][STEP ? TC + TR : 1]; // [step][row]
+    __shared__ __attribute__((aligned(16))) uint32_t s_mx[MX ? 2 : 1][MX ? kThr * 4 : 1];  // [row][q], four steps
+    __shared__ __attribute__((aligned(16))) float s_step[STEP ? 2 : 1][4][STEP ? kThr : 1]; // [step][row]
 
     const uint32_t lane = threadIdx.x & (kWaveSize - 1), r = lane & 15u, q = lane >> 4;
     const uint32_t wave = uniform(threadIdx.x / kWaveSize), wc = wave % WC, wr = wave / WC;
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
                     g))
         return;
     const uint2 tile = tile_in_group(t0 - g.first * col_tiles, g.tiles, col_tiles);
-    const uint32_t row0 = g.row0 + tile.x * TR, rows = min(TR, g.rows - tile.x * TR);
+    const uint32_t row0 = g.row0 + tile.x * TR, rows = min((uint32_t)TR, g.rows - tile.x * TR);
     const uint32_t col0 = tile.y * TC, depth = p.depth, steps = (depth + kDepth - 1) / kDepth;
     const size_t w_row0 = (size_t)g.expert * p.cols + col0;
     auto source = [&](uint32_t row) { // x's row for a row of the tile; x_rows or more: none
@@ -381,6 +383,8 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
     // FAST: whole steps whose offsets fit 32 bits; past the depth, else, zeros
     auto copy_c = [&](auto fast, uint32_t t, uint32_t buf, int i) {
         char* const to = s_c[buf] + (i * kWaves + wave) * 1024u;
+        if (!kEvenC && i * kWaves + wave >= kBytesC / 1024) // the same for the whole wave
+            return;
         if constexpr (decltype(fast)::value)
             copy_to_lds(base_c + (size_t)t * kRowC, offset_c[i], to);
         else
@@ -388,6 +392,8 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
     };
     auto copy_r = [&](auto fast, uint32_t t, uint32_t buf, int i) {
         char* const to = s_r[buf] + (i * kWaves + wave) * 1024u;
+        if (!kEvenR && i * kWaves + wave >= kBytesR / 1024)
+            return;
         if constexpr (decltype(fast)::value)
             copy_to_lds(p.x + (size_t)t * 128u, offset_r[i], to);
         else
@@ -402,7 +408,7 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
     if constexpr (MX || STEP) {
         if (weights) {
             own_row = w_row0 + min(threadIdx.x, p.cols - 1u - col0);
-        } else {
+        } else { // (threads past the last row: some row's, unused)
             const uint32_t at = source(threadIdx.x - TC);
             own_row = at < p.x_rows ? at : 0u;
         }
@@ -458,7 +464,7 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
                         *reinterpret_cast<const v4u*>(at + ((q + 4u) ^ (r & 7u)) * 16u));
         }
     };
-    auto row_of = [&](int j) { return 16u * (2u * j + wr); }; // every second block: few rows are shared evenly
+    auto row_of = [&](int j) { return 16u * ((uint32_t)WR * j + wr); }; // every WR-th block: few rows are shared evenly
     auto read_r = [&](uint32_t buf, int j) {
         const char* const at = s_r[buf] + (row_of(j) + r) * 128u;
         return join(*reinterpret_cast<const v4u*>(at + (q ^ (r & 7u)) * 16u),
@@ -466,7 +472,8 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
     };
 
     auto run = [&](auto n_blocks, auto fast) {
-        constexpr int N = decltype(n_blocks)::value, kCopiesR = N / 2;
+        constexpr int N = decltype(n_blocks)::value; // row blocks
+        constexpr int kCopiesR = (int)(WR * N * 2 + kWaves - 1) / (int)kWaves;
         v4f acc[kBlocks][N];
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i)
@@ -599,32 +606,44 @@ __global__ __launch_bounds__(512) void gemm_q_big_kernel(QuantParams p)
             const float r_scale = none ? 0.0f : row_scale(p.xs, at);
             const size_t line = (size_t)(row0 + row) * p.cols;
 #pragma unroll
-            for (int i = 0; i < kBlocks; i += 2) {
-                v4f v[2];
+            for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = none ? 0.0f : acc[i][j][e] * r_scale * c_scale[i][e];
+            if constexpr (kBlocks % 2 == 0) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[h][e] = none ? 0.0f : acc[i + h][j][e] * r_scale * c_scale[i + h][e];
-                const v4u pair = pair_columns(v[0], v[1]);
-                const uint32_t col = col0 + 16u * (wc * kBlocks + i + (q & 1u)) + 8u * (q >> 1);
+                for (int i = 0; i < kBlocks; i += 2) {
+                    const v4u pair = pair_columns(acc[i][j], acc[i + 1][j]);
+                    const uint32_t col = col0 + 16u * (wc * kBlocks + i + (q & 1u)) + 8u * (q >> 1);
+                    if (row < rows && col < p.cols)
+                        *reinterpret_cast<v4u*>(static_cast<__bf16*>(p.out) + line + col) = pair;
+                }
+            } else {
+                const uint32_t col = col0 + 16u * wc + 4u * q;
+                const v4f v = acc[0][j];
+                static_assert(kBlocks % 2 == 0 || kBlocks == 1, "blocks in pairs");
                 if (row < rows && col < p.cols)
-                    *reinterpret_cast<v4u*>(static_cast<__bf16*>(p.out) + line + col) = pair;
+                    *reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + line + col) =
+                        v4b{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
             }
         }
     };
     using std::bool_constant;
     using std::integral_constant;
     auto run_blocks = [&](auto fast) {
-        const uint32_t blocks = uniform((rows + 31u) / 32u);
-        if (blocks > 6)
-            run(integral_constant<int, 8>{}, fast);
-        else if (blocks > 4)
-            run(integral_constant<int, 6>{}, fast);
-        else if (blocks > 2)
-            run(integral_constant<int, 4>{}, fast);
-        else
-            run(integral_constant<int, 2>{}, fast);
+        if constexpr (kRowBlocks == 8) { // large tiles: no more blocks than there are rows
+            const uint32_t blocks = uniform((rows + 16u * WR - 1u) / (16u * WR));
+            if (blocks > 6)
+                run(integral_constant<int, 8>{}, fast);
+            else if (blocks > 4)
+                run(integral_constant<int, 6>{}, fast);
+            else if (blocks > 2)
+                run(integral_constant<int, 4>{}, fast);
+            else
+                run(integral_constant<int, 2>{}, fast);
+        } else {
+            run(integral_constant<int, kRowBlocks>{}, fast);
+        }
     };
     if (depth % kDepth == 0 && (uint64_t)p.x_rows * depth < (1ull << 32))
         run_blocks(bool_constant<true>{});
@@ -640,13 +659,14 @@ uint64_t workgroups(const QuantParams& p, uint32_t tc, uint32_t tr)
     return ((p.n_rows / tr + most) * col_tiles + kXcds - 1) / kXcds * kXcds;
 }
 
-template <bool W4, bool MX, bool STEP>
-tk_status launch_big(const QuantParams& p, hipStream_t s)
+template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
+tk_status launch_turn(const QuantParams& p, hipStream_t s)
 {
-    const uint64_t blocks = workgroups(p, 256, 256);
-    if (!launchable(blocks, 512))
+    const uint64_t blocks = workgroups(p, TC, TR);
+    if (!launchable(blocks, 64 * WC * WR))
         return TK_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((gemm_q_big_kernel<W4, MX, STEP>), dim3((uint32_t)blocks), dim3(512), 0, s, p);
+    hipLaunchKernelGGL((gemm_q_turn_kernel<W4, MX, STEP, TC, TR, WC, WR>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0,
+                       s, p);
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
 
@@ -665,10 +685,14 @@ template <bool W4, bool MX, bool STEP>
 tk_status launch_size(const QuantParams& p, hipStream_t s)
 {
     const uint32_t load = p.n_rows / p.experts; // an expert's rows on average
-    // (the large tiles take the scales of 32 and of 128 columns, four steps' at a time)
     auto turns = [](const Scales& a) { return a.kind != kScaleMx || (a.words && (a.width == 1 || a.width == 4)); };
-    if (load >= 128 && turns(p.ws) && turns(p.xs))
-        return launch_big<W4, MX, STEP>(p, s);
+    if (turns(p.ws) && turns(p.xs)) {
+        if (load >= 128)
+            return launch_turn<W4, MX, STEP, 256, 256, 4, 2>(p, s);
+        if (load >= 32)
+            return launch_turn<W4, MX, STEP, 128, 64, 2, 2>(p, s);
+        return launch_turn<W4, MX, STEP, 64, 16, 4, 1>(p, s);
+    }
     if (load >= 32)
         return launch<W4, MX, STEP, 128, 64, 2, 2>(p, s);
     return launch<W4, MX, STEP, 64, 16, 4, 1>(p, s);
