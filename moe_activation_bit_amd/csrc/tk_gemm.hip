@@ -50,7 +50,8 @@ __device__ __forceinline__ void store_result(const GemmParams& p, size_t at, v4f
     }
 }
 
-template <int KIND, int TC, int TR, int WC, int WR, bool X8>
+// RING: steps in LDS, one of them being multiplied and the others on their way (wgrad: two).
+template <int KIND, int TC, int TR, int WC, int WR, bool X8, int RING>
 __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
 {
     constexpr uint32_t kWaves = WC * WR;
@@ -58,10 +59,13 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
     constexpr int NC = TC / WC / 16, NR = TR / WR / 16;
     constexpr uint32_t kBytesC = TC * kDepth * 2, kBytesR = TR * kDepth * 2;
     constexpr int kCopiesC = (kBytesC / 1024 + kWaves - 1) / kWaves, kCopiesR = (kBytesR / 1024 + kWaves - 1) / kWaves;
-    constexpr bool kEvenC = kBytesC / 1024 % kWaves == 0, kEvenR = kBytesR / 1024 % kWaves == 0;
+    static_assert(KIND != kWgrad || RING == 2, "wgrad's sources are found a step ahead");
+    // a copy's number; where there are fewer than waves, some make the same one, so that all count as many
+    auto copy_no_c = [](int i, uint32_t wave) { return (i * kWaves + wave) % (kBytesC / 1024); };
+    auto copy_no_r = [](int i, uint32_t wave) { return (i * kWaves + wave) % (kBytesR / 1024); };
     constexpr int kCodes = X8 ? TC * kDepth / 16 / (64 * kWaves) : 1; // 16-code pieces of x a thread
-    __shared__ __attribute__((aligned(1024))) char s_c[2][kBytesC];
-    __shared__ __attribute__((aligned(1024))) char s_r[2][kBytesR];
+    __shared__ __attribute__((aligned(1024))) char s_c[RING][kBytesC];
+    __shared__ __attribute__((aligned(1024))) char s_r[RING][kBytesR];
 
     const uint32_t lane = threadIdx.x & (kWaveSize - 1), r = lane & 15u, q = lane >> 4;
     const uint32_t wave = uniform(threadIdx.x / kWaveSize), wc = wave % WC, wr = wave / WC;
@@ -121,7 +125,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
     uint32_t bad = 0; // rows of the forward's and dgrad's row operand whose index names none
 #pragma unroll
     for (int i = 0; i < kCopiesC; ++i) {
-        const uint32_t no = i * kWaves + wave;
+        const uint32_t no = copy_no_c(i, wave);
         if constexpr (!kCT) {
             const uint32_t row = no * 8u + lane / 8u, k = ((lane & 7u) ^ (lane >> 3)) * 8u;
             piece_c[i] = k;
@@ -137,7 +141,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
     }
 #pragma unroll
     for (int i = 0; i < kCopiesR; ++i) {
-        const uint32_t no = i * kWaves + wave;
+        const uint32_t no = copy_no_r(i, wave);
         if constexpr (!kRT) {
             const uint32_t row = no * 8u + lane / 8u, k = ((lane & 7u) ^ (lane >> 3)) * 8u;
             uint32_t at = row0 + min(row, rows - 1u);
@@ -199,12 +203,10 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
             auto each = [&](auto&& copy_c, auto&& copy_r) {
 #pragma unroll
                 for (int i = 0; i < kCopiesC; ++i)
-                    if (kEvenC || i * kWaves + wave < kBytesC / 1024)
-                        copy_c(i, s_c[buf] + (i * kWaves + wave) * 1024u);
+                        copy_c(i, s_c[buf] + copy_no_c(i, wave) * 1024u);
 #pragma unroll
                 for (int i = 0; i < kCopiesR; ++i)
-                    if (kEvenR || i * kWaves + wave < kBytesR / 1024)
-                        copy_r(i, s_r[buf] + (i * kWaves + wave) * 1024u);
+                        copy_r(i, s_r[buf] + copy_no_r(i, wave) * 1024u);
             };
             if (whole)
                 each([&](int i, char* to) { copy_to_lds(base_c + step_c, offset_c[i], to); },
@@ -222,9 +224,8 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
             if constexpr (!X8) {
 #pragma unroll
                 for (int i = 0; i < kCopiesC; ++i)
-                    if (kEvenC || i * kWaves + wave < kBytesC / 1024)
                         copy_to_lds(next_c[i] != ~0u ? base_c + offset_c[i] + (size_t)next_c[i] * ld_c : zeros(),
-                                    s_c[buf] + (i * kWaves + wave) * 1024u);
+                                    s_c[buf] + copy_no_c(i, wave) * 1024u);
             } else {
 #pragma unroll
                 for (int i = 0; i < kCodes; ++i) {
@@ -239,9 +240,8 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
             }
 #pragma unroll
             for (int i = 0; i < kCopiesR; ++i)
-                if (kEvenR || i * kWaves + wave < kBytesR / 1024)
                     copy_to_lds(next_r[i] != ~0u ? from_r[i] + (size_t)next_r[i] * ld_r : zeros(),
-                                s_r[buf] + (i * kWaves + wave) * 1024u);
+                                s_r[buf] + copy_no_r(i, wave) * 1024u);
             find_sources(t + 1u);
         }
     };
@@ -306,23 +306,28 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
         }
     };
 
-    // ---- the steps: one on its way while the one before it is multiplied
+    // ---- the steps: RING - 1 on their way while one is multiplied
     const uint32_t steps = (depth + kDepth - 1) / kDepth;
+    constexpr int kStep = (X8 ? 0 : kCopiesC) + kCopiesR; // a wave's copies of a step
     if (steps) {
         find_sources(0);
-        fetch(0, 0);
+#pragma unroll
+        for (uint32_t t = 0; t + 1u < (uint32_t)RING; ++t) // (past the last step zeros, unused)
+            fetch(t, t);
         put_codes(0);
     }
+    uint32_t buf = 0, ahead = RING - 1u;
 #pragma clang loop unroll(disable) // (nor peeled)
     for (uint32_t t = 0; t < steps; ++t) {
-        copies_done<0>();
-        __syncthreads(); // step t is there, and nobody reads step t - 1 any more
-        const uint32_t buf = t & 1u;
-        if (t + 1u < steps)
-            fetch(t + 1u, buf ^ 1u);
+        copies_done<(RING - 2) * kStep>();
+        meet(); // step t is there, and nobody reads step t - 1 any more
+        fetch(t + RING - 1u, ahead);
         multiply(buf);
-        put_codes(buf ^ 1u); // (past the last step unused: a branch here would draw the products behind it)
+        buf = buf + 1u < (uint32_t)RING ? buf + 1u : 0u;
+        ahead = ahead + 1u < (uint32_t)RING ? ahead + 1u : 0u;
+        put_codes(buf); // (past the last step unused: a branch here would draw the products behind it)
     }
+    copies_done<0>(); // no copy outlives the workgroup's LDS
 
     // ---- results: a lane has four columns of a row
 #pragma unroll
@@ -715,13 +720,13 @@ uint64_t workgroups(const GemmParams& p, uint32_t tc, uint32_t tr)
     return (row_tiles * col_tiles + kXcds - 1) / kXcds * kXcds;
 }
 
-template <int KIND, int TC, int TR, int WC, int WR, bool X8 = false>
+template <int KIND, int TC, int TR, int WC, int WR, int RING, bool X8 = false>
 tk_status launch(const GemmParams& p, hipStream_t s)
 {
     const uint64_t blocks = workgroups<KIND>(p, TC, TR);
     if (!launchable(blocks, 64 * WC * WR))
         return TK_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((gemm_kernel<KIND, TC, TR, WC, WR, X8>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0, s, p);
+    hipLaunchKernelGGL((gemm_kernel<KIND, TC, TR, WC, WR, X8, RING>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0, s, p);
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
 
@@ -739,14 +744,21 @@ tk_status launch_big(const GemmParams& p, hipStream_t s)
 
 namespace tk_gemm {
 
+// Which tiles: the largest that the rows of an expert fill, of which there are enough for 256 CUs.  In us, 4096 ->
+// 4096 for one expert: 64 rows 50 with 256 x 256 tiles, 29 with 128 columns x 64 rows, 19 with 64 x 64, 15 with 64 x
+// 16; 256 rows 78, 30, 21, 35; 1024 rows 81, 45, 56, 133; 4096 rows 125, 200, 240, 494.  7168 -> 4096 for 64 experts:
+// 24 rows each 772, 668, 697, 859; 64 each 787, 694, 794, 1324; 128 each 793 (256 x 256), 942 (128 x 64).
 tk_status launch_forward(const GemmParams& p, hipStream_t s)
 {
-    const uint32_t load = p.n_rows / p.experts; // an expert's rows on average
-    if (load >= 128)
+    const uint64_t load = average_rows(p.n_rows, p.experts);
+    auto tiles = [&](uint32_t tr, uint32_t tc) { return tiles_of(load, p.experts, p.cols, tr, tc); };
+    if (load > 64 && tiles(256, 256) >= 128)
         return launch_big<kForward>(p, s);
-    if (load >= 32)
-        return launch<kForward, 128, 64, 2, 2>(p, s);
-    return launch<kForward, 64, 16, 4, 1>(p, s);
+    if (load > 16 && tiles(64, 128) >= 384)
+        return launch<kForward, 128, 64, 2, 2, 3>(p, s);
+    if (load > 16 && tiles(64, 64) >= 128)
+        return launch<kForward, 64, 64, 2, 2, 3>(p, s);
+    return launch<kForward, 64, 16, 4, 1, 4>(p, s);
 }
 
 } // namespace tk_gemm
@@ -787,9 +799,14 @@ extern "C" tk_status tk_expert_gemm_dgrad(const void* dy, int64_t dy_rows, const
     p.out = dx;
     p.out_bf16 = out_bf16;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (p.n_rows / p.experts >= 128)
+    // as launch_forward; tiles kept [k][column] have 128 columns or more
+    const uint64_t load = average_rows(p.n_rows, p.experts);
+    auto tiles = [&](uint32_t tr, uint32_t tc) { return tiles_of(load, p.experts, p.cols, tr, tc); };
+    if (load > 64 && tiles(256, 256) >= 128)
         return launch_big<kDgrad>(p, s);
-    return launch<kDgrad, 128, 64, 2, 2>(p, s);
+    if (load > 16 && tiles(64, 128) >= 128)
+        return launch<kDgrad, 128, 64, 2, 2, 2>(p, s);
+    return launch<kDgrad, 128, 16, 4, 1, 3>(p, s);
 }
 
 extern "C" tk_status tk_expert_gemm_wgrad(const void* dy, int64_t dy_rows, const int32_t* dy_index, const void* x,
@@ -851,6 +868,6 @@ extern "C" tk_status tk_expert_gemm_wgrad(const void* dy, int64_t dy_rows, const
                        : (dy_index ? launch_big<kWgrad, false, false, true>(p, s) : launch_big<kWgrad>(p, s));
     }
     if (fp8)
-        return launch<kWgrad, 128, 128, 2, 2, true>(p, s);
-    return launch<kWgrad, 128, 128, 2, 2>(p, s);
+        return launch<kWgrad, 128, 128, 2, 2, 2, true>(p, s);
+    return launch<kWgrad, 128, 128, 2, 2, 2>(p, s);
 }

@@ -57,6 +57,13 @@ inline bool overlaps_rows(const void* out, size_t bytes, const int32_t* index, c
     return overlaps(out, bytes, index, (size_t)n_rows * 4u) || overlaps(out, bytes, offsets, (size_t)(experts + 1) * 4u);
 }
 
+// An expert's rows on average, and how many tiles of tr rows by tc columns there are when all have as many.
+inline uint64_t average_rows(uint32_t rows, uint32_t experts) { return (rows + experts - 1u) / experts; }
+inline uint64_t tiles_of(uint64_t load, uint32_t experts, uint32_t cols, uint32_t tr, uint32_t tc)
+{
+    return experts * ((load + tr - 1u) / tr) * (((uint64_t)cols + tc - 1u) / tc);
+}
+
 // tk_expert_gemm with bf16 operands
 tk_status launch_forward(const GemmParams& p, hipStream_t s);
 

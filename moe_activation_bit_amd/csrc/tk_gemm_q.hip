@@ -325,7 +325,7 @@ struct NoScale {
 };
 __device__ const NoScale g_no_scale = {0x7F7F7F7Fu, 1.0f};
 
-template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
+template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR, int RING>
 __global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p)
 {
     constexpr uint32_t kWaves = WC * WR, kThr = 64 * kWaves;
@@ -333,9 +333,11 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p
     static_assert(TC + TR <= (int)kThr, "a thread for each row's scales");
     constexpr uint32_t kRowC = W4 ? 64 : 128, kBytesC = TC * kRowC, kBytesR = TR * 128;
     constexpr int kCopiesC = (kBytesC / 1024 + kWaves - 1) / kWaves, kCopies = (kBytesR / 1024 + kWaves - 1) / kWaves;
-    constexpr bool kEvenC = kBytesC / 1024 % kWaves == 0, kEvenR = kBytesR / 1024 % kWaves == 0;
-    __shared__ __attribute__((aligned(1024))) char s_c[2][kBytesC];
-    __shared__ __attribute__((aligned(1024))) char s_r[2][kBytesR];
+    // a copy's number; where there are fewer than waves, some make the same one, so that all count as many
+    auto copy_no_c = [](int i, uint32_t wave) { return (i * kWaves + wave) % (kBytesC / 1024); };
+    auto copy_no_r = [](int i, uint32_t wave) { return (i * kWaves + wave) % (kBytesR / 1024); };
+    __shared__ __attribute__((aligned(1024))) char s_c[RING][kBytesC];
+    __shared__ __attribute__((aligned(1024))) char s_r[RING][kBytesR];
     __shared__ __attribute__((aligned(16))) uint32_t s_mx[MX ? 2 : 1][MX ? kThr * 4 : 1];  // [row][q], four steps
     __shared__ __attribute__((aligned(16))) float s_step[STEP ? 2 : 1][4][STEP ? kThr : 1]; // [step][row]
 
@@ -371,29 +373,25 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p
     uint32_t offset_c[kCopiesC], offset_r[kCopies], row_r[kCopies];
 #pragma unroll
     for (int i = 0; i < kCopiesC; ++i) {
-        const uint32_t row = (i * kWaves + wave) * (W4 ? 16u : 8u) + (W4 ? lane >> 2 : lane >> 3);
+        const uint32_t row = copy_no_c(i, wave) * (W4 ? 16u : 8u) + (W4 ? lane >> 2 : lane >> 3);
         offset_c[i] = min(row, p.cols - 1u - col0) * ld_c + lane_c * 16u;
     }
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
-        const uint32_t at = source((i * kWaves + wave) * 8u + (lane >> 3));
+        const uint32_t at = source(copy_no_r(i, wave) * 8u + (lane >> 3));
         row_r[i] = at < p.x_rows ? at : 0u; // (a row that is none: any, and zeros as its result)
         offset_r[i] = row_r[i] * depth + k_r;
     }
     // FAST: whole steps whose offsets fit 32 bits; past the depth, else, zeros
     auto copy_c = [&](auto fast, uint32_t t, uint32_t buf, int i) {
-        char* const to = s_c[buf] + (i * kWaves + wave) * 1024u;
-        if (!kEvenC && i * kWaves + wave >= kBytesC / 1024) // the same for the whole wave
-            return;
+        char* const to = s_c[buf] + copy_no_c(i, wave) * 1024u;
         if constexpr (decltype(fast)::value)
             copy_to_lds(base_c + (size_t)t * kRowC, offset_c[i], to);
         else
             copy_to_lds(t * kDepth + k_c < depth ? base_c + (size_t)t * kRowC + offset_c[i] : zeros(), to);
     };
     auto copy_r = [&](auto fast, uint32_t t, uint32_t buf, int i) {
-        char* const to = s_r[buf] + (i * kWaves + wave) * 1024u;
-        if (!kEvenR && i * kWaves + wave >= kBytesR / 1024)
-            return;
+        char* const to = s_r[buf] + copy_no_r(i, wave) * 1024u;
         if constexpr (decltype(fast)::value)
             copy_to_lds(p.x + (size_t)t * 128u, offset_r[i], to);
         else
@@ -473,6 +471,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p
 
     auto run = [&](auto n_blocks, auto fast) {
         constexpr int N = decltype(n_blocks)::value; // row blocks
+        auto last_step = [&](uint32_t t) { return min(t, steps - 1u); }; // (past the last step that one again, unused)
         constexpr int kCopiesR = (int)(WR * N * 2 + kWaves - 1) / (int)kWaves;
         v4f acc[kBlocks][N];
 #pragma unroll
@@ -482,19 +481,25 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p
                 acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         uint32_t a_mx[kBlocks], b_mx[N]; // four steps' scales of a lane
 #pragma unroll
-        for (int n = 0; n < kCopiesC; ++n)
-            copy_c(fast, 0, 0, n);
+        for (uint32_t t = 0; t + 1u < (uint32_t)RING; ++t) {
+            const uint32_t at = last_step(t);
 #pragma unroll
-        for (int n = 0; n < kCopiesR; ++n)
-            copy_r(fast, 0, 0, n);
+            for (int n = 0; n < kCopiesC; ++n)
+                copy_c(fast, at, t, n);
+#pragma unroll
+            for (int n = 0; n < kCopiesR; ++n)
+                copy_r(fast, at, t, n);
+        }
         fetch_scales(0);
         put_scales(0);
+        uint32_t at_step = 0; // t % 3
         auto step = [&](auto number, uint32_t t) { // step t, number t % 4 of its turn
             constexpr int u = decltype(number)::value;
-            const uint32_t buf = t & 1u, turn = t / 4u;
-            copies_done<0>();
-            __syncthreads(); // step t is there, and nobody reads step t - 1 any more
-            const uint32_t next = min(t + 1u, steps - 1u); // (past the last step that one again, unused)
+            const uint32_t turn = t / 4u, buf = RING == 3 ? at_step : u % RING;
+            const uint32_t ahead = RING == 3 ? (at_step ? at_step - 1u : 2u) : (u + RING - 1) % RING;
+            copies_done<(RING - 2) * (kCopiesC + kCopiesR)>();
+            meet(); // step t is there, and nobody reads step t - 1 any more
+            const uint32_t next = last_step(t + RING - 1u);
             if constexpr (MX) {
                 if constexpr (u == 0) {
 #pragma unroll
@@ -555,9 +560,9 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p
                 for (int n = 0; n < kCopiesC + kCopiesR; ++n) // spread over the row blocks
                     if (n * N / (kCopiesC + kCopiesR) == j) {
                         if (n < kCopiesC)
-                            copy_c(fast, next, buf ^ 1u, n);
+                            copy_c(fast, next, ahead, n);
                         else
-                            copy_r(fast, next, buf ^ 1u, n - kCopiesC);
+                            copy_r(fast, next, ahead, n - kCopiesC);
                     }
             }
             if constexpr (STEP) { // (the sums are done with here: left to the compiler, products move behind the branch)
@@ -573,6 +578,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p
                 fetch_scales(turn + 1u);
             if constexpr (u == 2)
                 put_scales((turn + 1u) & 1u);
+            at_step = at_step < 2u ? at_step + 1u : 0u;
         };
         using std::integral_constant;
 #pragma clang loop unroll(disable) // (nor peeled)
@@ -659,13 +665,13 @@ uint64_t workgroups(const QuantParams& p, uint32_t tc, uint32_t tr)
     return ((p.n_rows / tr + most) * col_tiles + kXcds - 1) / kXcds * kXcds;
 }
 
-template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
+template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR, int RING>
 tk_status launch_turn(const QuantParams& p, hipStream_t s)
 {
     const uint64_t blocks = workgroups(p, TC, TR);
     if (!launchable(blocks, 64 * WC * WR))
         return TK_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((gemm_q_turn_kernel<W4, MX, STEP, TC, TR, WC, WR>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0,
+    hipLaunchKernelGGL((gemm_q_turn_kernel<W4, MX, STEP, TC, TR, WC, WR, RING>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0,
                        s, p);
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
@@ -684,16 +690,19 @@ tk_status launch(const QuantParams& p, hipStream_t s)
 template <bool W4, bool MX, bool STEP>
 tk_status launch_size(const QuantParams& p, hipStream_t s)
 {
-    const uint32_t load = p.n_rows / p.experts; // an expert's rows on average
+    // as launch_forward; the large tiles for groups of 32 and of 128 columns (or none)
+    const uint64_t load = average_rows(p.n_rows, p.experts);
+    auto tiles = [&](uint32_t tr, uint32_t tc) { return tiles_of(load, p.experts, p.cols, tr, tc); };
     auto turns = [](const Scales& a) { return a.kind != kScaleMx || (a.words && (a.width == 1 || a.width == 4)); };
+    const bool mid = load > 16 && tiles(64, 128) >= 128;
     if (turns(p.ws) && turns(p.xs)) {
-        if (load >= 128)
-            return launch_turn<W4, MX, STEP, 256, 256, 4, 2>(p, s);
-        if (load >= 32)
-            return launch_turn<W4, MX, STEP, 128, 64, 2, 2>(p, s);
-        return launch_turn<W4, MX, STEP, 64, 16, 4, 1>(p, s);
+        if (load > 64 && tiles(256, 256) >= 128)
+            return launch_turn<W4, MX, STEP, 256, 256, 4, 2, 2>(p, s);
+        if (mid)
+            return launch_turn<W4, MX, STEP, 128, 64, 2, 2, 3>(p, s);
+        return launch_turn<W4, MX, STEP, 64, 16, 4, 1, 4>(p, s);
     }
-    if (load >= 32)
+    if (mid)
         return launch<W4, MX, STEP, 128, 64, 2, 2>(p, s);
     return launch<W4, MX, STEP, 64, 16, 4, 1>(p, s);
 }

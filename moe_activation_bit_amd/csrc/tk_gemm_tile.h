@@ -65,6 +65,16 @@ __device__ __forceinline__ void copies_done()
     asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
+// The waves of a workgroup meet: what each has read of LDS is read, what it has
+// written there is written.  (The language's barrier would also wait for every
+// copy.)
+__device__ __forceinline__ void meet()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // two of a word's four E4M3 codes, the lower or the upper ones, times a power of two
 template <bool UPPER>
 __device__ __forceinline__ uint32_t fp8_to_bf16(uint32_t codes, float scale)

@@ -71,7 +71,7 @@ LAYOUTS = {
     "large_one": ([391], 0, 0),
     "many": ([int(v) for v in (np.arange(160) * 7) % 5], 3, 0),
 }
-SHAPES = [(8, 8), (24, 72), (264, 64), (136, 200), (520, 328)]
+SHAPES = [(8, 8), (24, 72), (264, 64), (136, 200), (520, 328), (2056, 136), (8200, 72)]  # many columns: larger tiles
 
 
 def layout(name):
@@ -193,7 +193,7 @@ def test_codes_whole_numbers(name, x_kind, w_kind, fp4):
     groups = [g for g in (x_kind[1], w_kind[1]) if g]
     in_f = int(np.lcm.reduce(groups + [32])) * (2 if name == "mid" else 1)
     in_f += in_f if in_f < 256 else 0
-    out_f = 72 if name != "large" else 264
+    out_f = {"few_behind": 72, "mid": 2824, "large": 8200}[name]  # as many columns as each tile size asks for
     rows = 37
     index = index_of(rng, n, rows, True)
     xc, xs, x = fp8_operand(rng, rows, in_f, *x_kind)
@@ -238,7 +238,8 @@ def check_sum(got, bf, want, mag, depth, more=0.0):
 
 
 @pytest.mark.parametrize("bf", [False, True])
-@pytest.mark.parametrize("name,out_f,in_f", [("few_behind", 200, 1000), ("mid", 264, 520), ("large", 264, 520)])
+@pytest.mark.parametrize("name,out_f,in_f", [("few_behind", 200, 1000), ("mid", 264, 520), ("large", 264, 520),
+                                             ("large", 8200, 264), ("large", 264, 8200)])
 def test_numbers(name, out_f, in_f, bf):
     say("numbers", name, out_f, in_f, bf)
     rng = np.random.default_rng(in_f)
@@ -272,7 +273,7 @@ def test_codes_numbers(x_kind, w_kind, fp4):
     say("codes", x_kind, w_kind, fp4)
     rng = np.random.default_rng(5)
     off, n, e = layout("large")
-    in_f, out_f = 640, 136
+    in_f, out_f = 640, 8200
     xc, xs, x = fp8_operand(rng, n, in_f, *x_kind, exact=False)
     wc, ws, w = fp8_operand(rng, e * out_f, in_f, *w_kind, fp4=fp4, exact=False)
     w = w.reshape(e, out_f, in_f)
