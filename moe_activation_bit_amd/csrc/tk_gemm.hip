@@ -31,23 +31,26 @@ __device__ __forceinline__ v8b read_transposed(const char* at, uint32_t pitch)
     return __builtin_bit_cast(v8b, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Four columns of a row, rounded once; ADD: to what is there, when asked.
-template <bool ADD>
+// Four columns of a row, rounded once.
 __device__ __forceinline__ void store_result(const GemmParams& p, size_t at, v4f v)
 {
-    if (p.out_bf16) {
-        v4b* const to = reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + at);
-        if (ADD && p.accumulate) {
-            const v4b old = *to;
-            v += v4f{(float)old[0], (float)old[1], (float)old[2], (float)old[3]};
-        }
-        *to = v4b{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-    } else {
-        v4f* const to = reinterpret_cast<v4f*>(static_cast<float*>(p.out) + at);
-        if (ADD && p.accumulate)
-            v += *to;
-        *to = v;
-    }
+    if (p.out_bf16)
+        *reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + at) = v4b{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    else
+        *reinterpret_cast<v4f*>(static_cast<float*>(p.out) + at) = v;
+}
+
+// v[i] += the results in their places, from `at`(i); their loads are on their way together.
+template <typename T4, typename T, int N, typename F>
+__device__ __forceinline__ void add_result(const T* out, v4f* v, F&& at)
+{
+    T4 old[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        old[i] = *reinterpret_cast<const T4*>(out + at(i));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] += __builtin_convertvector(old[i], v4f);
 }
 
 // RING: steps in LDS, one of them being multiplied and the others on their way (wgrad: two).
@@ -330,19 +333,30 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
     copies_done<0>(); // no copy outlives the workgroup's LDS
 
     // ---- results: a lane has four columns of a row
+    const size_t first = (KIND == kWgrad ? expert * (size_t)p.out_rows : 0u) + row0;
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
         const uint32_t row = 16u * (wr * NR + j) + r;
         if (row >= rows)
             continue;
-        const size_t line = ((size_t)(KIND == kWgrad ? expert * (size_t)p.out_rows : 0u) + row0 + row) * p.cols;
+        const size_t line = (first + row) * p.cols;
+        v4f v[NC];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const uint32_t col = col0 + 16u * (wc * NC + i) + 4u * q;
-            if (col >= p.cols)
-                continue;
-            store_result<KIND == kWgrad>(p, line + col, acc[i][j]);
-        }
+        for (int i = 0; i < NC; ++i)
+            v[i] = acc[i][j];
+        auto column = [&](int i) { return col0 + 16u * (wc * NC + i) + 4u * q; };
+        if constexpr (KIND == kWgrad)
+            if (p.accumulate) {
+                auto at = [&](int i) { return line + min(column(i), p.cols - 4u); };
+                if (p.out_bf16)
+                    add_result<v4b, __bf16, NC>(static_cast<const __bf16*>(p.out), v, at);
+                else
+                    add_result<v4f, float, NC>(static_cast<const float*>(p.out), v, at);
+            }
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            if (column(i) < p.cols)
+                store_result(p, line + column(i), v[i]);
     }
 }
 
@@ -468,6 +482,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
     const uint32_t code_g = X8 ? code_col / p.c_group : 0u; // (a group is 16 columns or a multiple)
     v4u codes[kCodes];
     uint8_t code_scale[kCodes];
+    uint32_t scale_there[kCodes];
     auto find_code_rows = [&](uint32_t t) {
         if constexpr (X8 && XI)
 #pragma unroll
@@ -475,6 +490,18 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
                 next_x[i] = indexed(p.c_index, t * kDepth + i * 32u + code_k);
     };
     bool code_in[kCodes];
+    // what the loads above left in registers is there (after copies_done): the compiler, which does not count the
+    // copies, would wait for them too at the first use behind some
+    auto codes_there = [&] {
+        if constexpr (X8)
+#pragma unroll
+            for (int i = 0; i < kCodes; ++i) {
+                scale_there[i] = code_scale[i];
+                asm volatile("" : "+v"(codes[i]), "+v"(scale_there[i]));
+                if constexpr (XI)
+                    asm volatile("" : "+v"(next_x[i]));
+            }
+    };
     auto load_codes = [&](uint32_t t) {
         if constexpr (X8)
 #pragma unroll
@@ -491,7 +518,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
             const uint32_t k = i * 32u + code_k, keep = code_in[i] ? ~0u : 0u;
             const uint32_t word[4] = {codes[i].x & keep, codes[i].y & keep, codes[i].z & keep, codes[i].w & keep};
             char* const to = s_c[buf] + k * (TC * 2u) + (code_s ^ hash(k)) * 32u;
-            const float scale = as_float((uint32_t)code_scale[i] << 23);
+            const float scale = as_float(scale_there[i] << 23);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 *reinterpret_cast<uint4*>(to + 16 * h) =
@@ -579,6 +606,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
                 for (uint32_t t = 0; t < 2; ++t) {
                     find_code_rows(t);
                     load_codes(t);
+                    codes_there();
 #pragma unroll
                     for (int i = 0; i < kCodes; ++i)
                         put_codes(i, t);
@@ -632,6 +660,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 copies_done<0>();
+                codes_there();
                 __syncthreads(); // step t + 1 is there, and every wave has read all of step t
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
@@ -643,8 +672,14 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
                     __builtin_amdgcn_sched_barrier(0);
                     if (X8 && j < kCodes)
                         put_codes(j, buf);
+                    if (X8 && j == kCodes)
+                        load_codes(t + 3u);
+                    if (X8 && j == kCodes + 1)
+                        find_code_rows(t + 4u);
+                    if (X8 && j < kCopiesR)
+                        copy_r(fast, t + 2u, buf, j);
 #pragma unroll
-                    for (int n = j * kCopiesEach; n < (j + 1) * kCopiesEach; ++n) {
+                    for (int n = X8 ? kCopies + kCopiesR : j * kCopiesEach; n < (j + 1) * kCopiesEach; ++n) {
                         if (n < kCopies)
                             copy_c(fast, t + 2u, buf, n);
                         else if (n < kCopies + kCopiesR)
@@ -654,29 +689,37 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
                 __builtin_amdgcn_sched_barrier(0);
                 // what the next copies need, on its way until the waves meet again
                 find_rows(t + 3u);
-                load_codes(t + 3u);
-                find_code_rows(t + 4u);
             }
             copies_done<0>(); // no copy outlives the workgroup's LDS
         }
 
         // ---- results: a lane has four columns of a row
+        const size_t first = (KIND == kWgrad ? expert * (size_t)p.out_rows : 0u) + row0;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const uint32_t row = 16u * (2u * j + wr) + r;
             const bool none = KIND != kWgrad && p.r_index && row < rows && (uint32_t)p.r_index[row0 + row] >= p.r_rows;
-            const size_t line = ((size_t)(KIND == kWgrad ? expert * (size_t)p.out_rows : 0u) + row0 + row) * p.cols;
-            if (none)
+            const size_t line = (first + row) * p.cols;
+            v4f v[kBlocks];
 #pragma unroll
-                for (int i = 0; i < kBlocks; ++i)
-                    acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-            if (p.out_bf16 && !(KIND == kWgrad && p.accumulate)) { // the same for every thread
+            for (int i = 0; i < kBlocks; ++i)
+                v[i] = none ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
+            if constexpr (KIND == kWgrad)
+                if (p.accumulate) {
+                    const size_t from = (first + min(row, rows - 1u)) * p.cols;
+                    auto at = [&](int i) { return from + min(col0 + 16u * (wc * kBlocks + i) + 4u * q, p.cols - 4u); };
+                    if (p.out_bf16)
+                        add_result<v4b, __bf16, kBlocks>(static_cast<const __bf16*>(p.out), v, at);
+                    else
+                        add_result<v4f, float, kBlocks>(static_cast<const float*>(p.out), v, at);
+                }
+            if (p.out_bf16) { // the same for every thread
 #pragma unroll
                 for (int i = 0; i < kBlocks; i += 2) {
-                    const v4u v = pair_columns(acc[i][j], acc[i + 1][j]);
+                    const v4u pair = pair_columns(v[i], v[i + 1]);
                     const uint32_t col = col0 + 16u * (wc * kBlocks + i + (q & 1u)) + 8u * (q >> 1);
                     if (row < rows && col < p.cols)
-                        *reinterpret_cast<v4u*>(static_cast<__bf16*>(p.out) + line + col) = v;
+                        *reinterpret_cast<v4u*>(static_cast<__bf16*>(p.out) + line + col) = pair;
                 }
                 continue;
             }
@@ -684,7 +727,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
             for (int i = 0; i < kBlocks; ++i) {
                 const uint32_t col = col0 + 16u * (wc * kBlocks + i) + 4u * q;
                 if (row < rows && col < p.cols)
-                    store_result<KIND == kWgrad>(p, line + col, acc[i][j]);
+                    *reinterpret_cast<v4f*>(static_cast<float*>(p.out) + line + col) = v[i];
             }
         }
     };
