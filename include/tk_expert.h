@@ -29,12 +29,14 @@
  * Rows of the products.  expert_offsets is int32 [experts + 1]: expert e has the
  * rows expert_offsets[e] .. expert_offsets[e + 1] - 1 of n_rows.  Entries below 0
  * or above n_rows count as these, an entry below the one before it as an expert
- * without rows; NULL: one expert (experts is 1) has all n_rows.  Rows that no
+ * without rows (where that gives a row to two experts, the results of the call are
+ * unspecified, and nothing but its outputs is written); NULL: one expert (experts is 1) has all n_rows.  Rows that no
  * expert has, such as those from expert_offsets[experts] on, are not read and
  * their results are left as they were.  n_rows may thus be a capacity: tokens*k.
  * A row index is int32 [n_rows]: the row of x (or dy) that each row takes, e.g.
  * its token, with the number of those rows given; an entry outside 0 .. rows-1
- * stands for a row of zeros.  NULL: each row its own (the number of rows is then
+ * stands for a row of zeros, whose products with the weights are zeros whatever
+ * the weights hold.  NULL: each row its own (the number of rows is then
  * n_rows or more).
  */
 #ifndef TK_EXPERT_H_

@@ -3,6 +3,7 @@
 // and tk_expert_gemm_wgrad in include/tk_expert.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -167,6 +168,10 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
     }
     if constexpr (!kRT)
         any_bad = __builtin_amdgcn_ballot_w64(bad != 0) != 0;
+    uint32_t result_row[NR]; // the operand's row of each of the lane's results (read here, long before its use)
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+        result_row[j] = !kRT && p.r_index ? (uint32_t)p.r_index[row0 + min(16u * (wr * NR + j) + r, rows - 1u)] : 0u;
 
     // wgrad: the source row of the expert's row k, past whose last there are zeros
     auto source = [&](const int32_t* index, uint32_t k, uint32_t all) -> uint32_t {
@@ -340,10 +345,11 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
         if (row >= rows)
             continue;
         const size_t line = (first + row) * p.cols;
+        const bool none = !kRT && p.r_index && result_row[j] >= p.r_rows;
         v4f v[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-            v[i] = acc[i][j];
+            v[i] = none ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
         auto column = [&](int i) { return col0 + 16u * (wc * NC + i) + 4u * q; };
         if constexpr (KIND == kWgrad)
             if (p.accumulate) {
@@ -387,14 +393,15 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
     uint32_t expert, row_base = 0, row0, rows, col0, depth;
     if constexpr (KIND == kWgrad) {
         const uint32_t row_tiles = (p.out_rows + TR - 1) / TR, per = row_tiles * col_tiles;
-        const uint32_t t = xcd_tile(blockIdx.x, p.experts * per);
+        const uint32_t t = xcd_tile_in_turns(blockIdx.x, p.run);
         if (t >= p.experts * per)
             return;
         expert = t / per;
         const uint32_t in = t - expert * per;
-        row0 = in / col_tiles * TR;
+        const uint2 at = tile_in_group<4>(in, row_tiles, col_tiles);
+        row0 = at.x * TR;
         rows = min(TR, p.out_rows - row0);
-        col0 = in % col_tiles * TC;
+        col0 = at.y * TC;
         expert_rows(p.offsets, expert, p.n_rows, row_base, depth);
         row_base = uniform(row_base);
         depth = uniform(depth);
@@ -405,7 +412,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
         uint32_t t = 0;
         if (!find_group(p.offsets, p.experts, p.n_rows, TR,
                         [&](uint32_t total) {
-                            t = xcd_tile(blockIdx.x, total * col_tiles);
+                            t = xcd_tile_in_turns(blockIdx.x, p.run);
                             return t / col_tiles;
                         },
                         g))
@@ -591,7 +598,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
     // ---- the steps, and the results, with N row blocks a wave
     auto run = [&](auto n_blocks, auto fast) {
         constexpr int N = decltype(n_blocks)::value;
-        constexpr int kCopiesR = kRT ? kCopies : N / 2; // [row][k]: the rows that the blocks have
+        constexpr int kCopiesR = kRT ? kCopies : (N + 1) / 2; // [row][k]: the rows that the blocks have
         v4f acc[kBlocks][N];
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i)
@@ -733,15 +740,23 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
     };
     using std::integral_constant;
     using std::bool_constant;
+    // As many row blocks as the tile's rows need: of 64 experts with some 500 rows each, products of whole tiles would
+    // be a fifth more (1816 us; 1830 with even numbers of blocks only).
     auto run_blocks = [&](auto fast) {
         const uint32_t blocks = KIND == kWgrad ? 8u : uniform((rows + 31u) / 32u);
-        if (blocks > 6)
+        if (blocks > 7)
             run(integral_constant<int, 8>{}, fast);
         if constexpr (KIND != kWgrad) {
-            if (blocks > 4 && blocks <= 6)
+            if (blocks == 7)
+                run(integral_constant<int, 7>{}, fast);
+            else if (blocks == 6)
                 run(integral_constant<int, 6>{}, fast);
-            else if (blocks > 2 && blocks <= 4)
+            else if (blocks == 5)
+                run(integral_constant<int, 5>{}, fast);
+            else if (blocks == 4)
                 run(integral_constant<int, 4>{}, fast);
+            else if (blocks == 3)
+                run(integral_constant<int, 3>{}, fast);
             else if (blocks <= 2)
                 run(integral_constant<int, 2>{}, fast);
         }
@@ -753,14 +768,14 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
 }
 
 // At most how many tiles of TR rows by TC columns there are, however the rows lie, in workgroups of whole turns
-// over the XCDs.
+// over the XCDs, `run` tiles each.
 template <int KIND>
-uint64_t workgroups(const GemmParams& p, uint32_t tc, uint32_t tr)
+uint64_t workgroups(const GemmParams& p, uint32_t tc, uint32_t tr, uint32_t run = 1)
 {
     const uint64_t col_tiles = ((uint64_t)p.cols + tc - 1) / tc, most = p.n_rows < p.experts ? p.n_rows : p.experts;
     const uint64_t row_tiles =
         KIND == kWgrad ? (uint64_t)p.experts * (((uint64_t)p.out_rows + tr - 1) / tr) : p.n_rows / tr + most;
-    return (row_tiles * col_tiles + kXcds - 1) / kXcds * kXcds;
+    return (row_tiles * col_tiles + kXcds * run - 1) / (kXcds * run) * (kXcds * run);
 }
 
 template <int KIND, int TC, int TR, int WC, int WR, int RING, bool X8 = false>
@@ -774,9 +789,16 @@ tk_status launch(const GemmParams& p, hipStream_t s)
 }
 
 template <int KIND, bool X8 = false, bool XI = false, bool DI = false>
-tk_status launch_big(const GemmParams& p, hipStream_t s)
+tk_status launch_big(GemmParams p, hipStream_t s)
 {
-    const uint64_t blocks = workgroups<KIND>(p, 256, 256);
+    // Tiles that an XCD takes together.  wgrad's cost as much as their expert has rows: every XCD takes its part of each
+    // expert.  64 experts 4096 x 2048 of unlike popularity (141 .. 1098 rows) 1149 us with an eighth of all tiles an XCD,
+    // 981 .. 992 so; with 512 rows for each of 64, 7168 x 2048 1223 and 1130, 4096 x 7168 2332 and 2502.  Forward and
+    // dgrad, 2.5 row tiles an expert, the last one shorter: dgrad 1134 and 1111, forward 1851 and 1833.
+    const uint32_t per = ((p.out_rows + 255u) / 256u) * ((p.cols + 255u) / 256u);
+    const uint64_t tiles = KIND == kWgrad ? per : tiles_of(average_rows(p.n_rows, p.experts), p.experts, p.cols, 256, 256);
+    p.run = (uint32_t)std::min<uint64_t>((tiles + kXcds - 1u) / kXcds, KIND == kWgrad ? 64u : 32u);
+    const uint64_t blocks = workgroups<KIND>(p, 256, 256, p.run);
     if (!launchable(blocks, 512))
         return TK_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((gemm_big_kernel<KIND, X8, XI, DI>), dim3((uint32_t)blocks), dim3(512), 0, s, p);

@@ -30,6 +30,7 @@ struct GemmParams {
     uint32_t cols;          // of the result
     uint32_t out_rows;      // of the weights' gradient, for each expert
     uint32_t depth;         // of the sums (the weights' gradient: an expert's rows)
+    uint32_t run;           // tiles that an XCD takes together
     int out_bf16;
     int accumulate;
 };

@@ -298,7 +298,8 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
         if (row >= rows)
             continue;
         const uint32_t at = source(row);
-        const float r_scale = at < p.x_rows ? row_scale(p.xs, at) : 0.0f;
+        const bool none = at >= p.x_rows;
+        const float r_scale = none ? 0.0f : row_scale(p.xs, at);
         const size_t line = (size_t)(row0 + row) * p.cols;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -308,7 +309,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
             v4b v;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                v[e] = (__bf16)(acc[i][j][e] * r_scale * c_scale[i][e]);
+                v[e] = (__bf16)(none ? 0.0f : acc[i][j][e] * r_scale * c_scale[i][e]);
             *reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + line + col) = v;
         }
     }

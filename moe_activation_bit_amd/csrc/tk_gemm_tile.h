@@ -201,12 +201,20 @@ __device__ __forceinline__ uint32_t xcd_tile(uint32_t block, uint32_t total)
     return i < run ? (block % kXcds) * run + i : total;
 }
 
+// ... `run` of every 8 run tiles, so that experts with many rows do not all fall
+// to one XCD.
+__device__ __forceinline__ uint32_t xcd_tile_in_turns(uint32_t block, uint32_t run)
+{
+    const uint32_t i = block / kXcds;
+    return (i / run * kXcds + block % kXcds) * run + i % run;
+}
+
 // (row tile, column tile) of an expert's tile: eight row tiles by all column
 // tiles at a time, rows first, so that the 32 tiles which an XCD's CUs have at
 // hand are about as many rows as columns and share them in its L2.
+template <uint32_t kHeight = 8>
 __device__ __forceinline__ uint2 tile_in_group(uint32_t tile, uint32_t row_tiles, uint32_t col_tiles)
 {
-    constexpr uint32_t kHeight = 8;
     const uint32_t band = tile / (kHeight * col_tiles), in = tile - band * (kHeight * col_tiles);
     const uint32_t height = min(kHeight, row_tiles - band * kHeight);
     return make_uint2(band * kHeight + in % height, in / height);

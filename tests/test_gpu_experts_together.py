@@ -379,3 +379,39 @@ def test_rows_do_not_depend_on_others():
         row = host(y)[0]
         seen = row if seen is None else seen
         assert np.array_equal(row, seen)
+
+
+@pytest.mark.parametrize("counts,out_f", [([20, 13], 72), ([90, 40], 8200), ([700, 900], 4104)])
+def test_rows_of_none_are_zero_whatever_the_weights_hold(counts, out_f):
+    """Over every tile size; a NaN among the weights reaches the other rows."""
+    rng = np.random.default_rng(30)
+    e, in_f = 2, 128
+    off, n = products.offsets_of(counts), sum(counts)
+    index = rng.integers(0, n, n).astype(np.int32)
+    none = rng.random(n) < 0.3
+    index[none] = rng.choice([-1, n, 2**31 - 1], none.sum())
+    x = rng.standard_normal((n, in_f)).astype(np.float32)
+    w = rng.standard_normal((e, out_f, in_f)).astype(np.float32)
+    w[:, 5, 7] = np.nan
+    dw, di = products.dev(off), products.dev(index)
+    y = torch.ones((n, out_f), device=DEV)
+    assert tk.tk_expert_gemm(products.bf16(x), None, BF16, 0, 0, n, di, dw, n, products.bf16(w), None, BF16, 0, 0, e, out_f,
+                             in_f, FP32, y) == OK
+    y = host(y)
+    assert not y[none].any() and np.isnan(y[~none][:, 5]).all() and np.isfinite(np.delete(y[~none], 5, 1)).all()
+    wt = np.ascontiguousarray(np.swapaxes(w, 1, 2))  # [e, in_f, out_f]: rows of in_f values against it
+    y = torch.ones((n, out_f), device=DEV)
+    assert tk.tk_expert_gemm_dgrad(products.bf16(x), n, di, dw, n, products.bf16(wt), e, in_f, out_f, FP32, y) == OK
+    y = host(y)
+    assert not y[none].any() and np.isnan(y[~none][:, 5]).all() and np.isfinite(np.delete(y[~none], 5, 1)).all()
+    codes = rng.integers(0, 120, (n, in_f), dtype=np.uint8)
+    wcodes = rng.integers(0, 120, (e, out_f, in_f), dtype=np.uint8)
+    wcodes[:, 5, 7] = 0x7F
+    for group in (32, 64, 0):  # 64: the scales' own kernel
+        g = in_f // (group or in_f)
+        xs, ws = (torch.full((r, g), 127, dtype=torch.uint8, device=DEV) for r in (n, e * out_f))
+        out = torch.ones((n, out_f), dtype=torch.bfloat16, device=DEV)
+        assert tk.tk_expert_gemm(products.dev(codes), xs, FP8, 1, group, n, di, dw, n, products.dev(wcodes), ws, FP8, 1,
+                                 group, e, out_f, in_f, BF16, out) == OK
+        y = host(out)
+        assert not y[none].any() and np.isnan(y[~none][:, 5]).all() and np.isfinite(np.delete(y[~none], 5, 1)).all()
