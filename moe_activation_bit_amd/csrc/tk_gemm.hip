@@ -54,7 +54,14 @@ __device__ __forceinline__ void add_result(const T* out, v4f* v, F&& at)
         v[i] += __builtin_convertvector(old[i], v4f);
 }
 
-// RING: steps in LDS, one of them being multiplied and the others on their way (wgrad: two).
+// A tile of TC columns x TR rows by WC x WR waves, 64 k a step; a column's and a row's fragments meet in the
+// 16x16x32 instruction, so that a lane ends with four columns of a row.  The copies go straight into LDS and are
+// waited for when their step comes up.  RING: steps in LDS, one of them being multiplied and the others on their way
+// (wgrad: two).  For few rows, whose time is that of reading the weights: one row of each of 64 experts 7168 -> 4096
+// 600 us (3.76 GB, 6.2 TB/s), 34 tokens' rows of a 512 -> 1024 layer 5.0 us (the launch, and one trip to memory for
+// the indices and one for the first step).  More steps on their way are what few tiles need: 64 rows of 4096 -> 4096
+// 39 us with two steps, 15 with three or four and smaller tiles; with weights kept [k][column], whose smallest tile has
+// 128 columns, two (64 rows an expert) and three steps (16).
 template <int KIND, int TC, int TR, int WC, int WR, bool X8, int RING>
 __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
 {
@@ -371,7 +378,18 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_kernel(GemmParams p)
 // fragments are read; then the waves meet (every one has read all of this step,
 // and the next one is in LDS); while the second half is multiplied, the next
 // step's first fragments are read and the step after that is copied over this
-// one.
+// one.  The waves read each fragment of LDS two or four times, 192 KiB a step, in
+// some 1500 of the 2048 cycles that its matrix instructions take: 128 x 128 by
+// each of four waves reads a third less, but leaves a SIMD one wave (1359 us
+// against 894, 8192 x 8192 x 8192), and four steps of 32 k in LDS are no faster
+// (896 .. 910).
+//
+// Bound by the matrix units and the power that they and LDS take: 8192 x 8192 x
+// 8192 870 us forward, 795 dgrad (790 a library's; MFMA busy 65% of cycles at 1.83
+// GHz, at 1.98 without the copies and 2.2 without the reads), 840 .. 950 wgrad.
+// 4096 tokens' top-8 of 64 experts 7168 -> 4096 1820 us (1.04 PFLOP/s).  wgrad of
+// short sums by its stores too: 64 experts 4096 x 2048 from 502 rows each 992 us,
+// 416 of them what storing 2.1 GB takes by itself.
 // X8: x in FP8 (wgrad).  XI, DI: wgrad's rows of x and of dy are found by an index.
 template <int KIND, bool X8, bool XI, bool DI>
 __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)

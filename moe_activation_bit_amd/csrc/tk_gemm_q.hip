@@ -46,6 +46,10 @@ __device__ __forceinline__ float e8m0_value(uint32_t b)
     return b == 0u ? 0x1p-127f : as_float(b == 255u ? 0x7FC00000u : b << 23);
 }
 
+// Groups of any width (a scale of one step, read in front of its products, may serve many steps or a part of one), and
+// UE8M0 bytes at any address.  The layout and the pace of gemm_kernel (tk_gemm.hip) with 128 k a step and two steps in
+// LDS; bound by reading the scales: FP4 weights with scales of 32 columns, one row of each of 64 experts 7168 -> 4096,
+// 299 us where gemm_q_turn_kernel takes 227.
 // W4: weights in FP4.  MX: some operand has power-of-two scales of groups.  STEP: some operand has fp32 ones.
 template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
@@ -56,7 +60,6 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
     constexpr uint32_t kBytesC = TC * kRowC, kBytesR = TR * 128;
     constexpr int kCopiesC = (kBytesC / 1024 + kWaves - 1) / kWaves, kCopiesR = (kBytesR / 1024 + kWaves - 1) / kWaves;
     constexpr bool kEvenC = kBytesC / 1024 % kWaves == 0, kEvenR = kBytesR / 1024 % kWaves == 0;
-    constexpr bool kBounded = NC * NR >= 16;
     constexpr int kOwn = (TC + TR + kThr - 1) / kThr; // rows whose scales a thread fetches
     __shared__ __attribute__((aligned(1024))) char s_c[2][kBytesC];
     __shared__ __attribute__((aligned(1024))) char s_r[2][kBytesR];
@@ -239,11 +242,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
         Weights ahead = weights(0);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            // the next weights' reads under these products, and no others: with all of them at once the large tiles'
-            // registers overflow
-            if (kBounded)
-                __builtin_amdgcn_sched_barrier(0);
-            const Weights a = ahead;
+            const Weights a = ahead; // the next weights' reads under these products
             if (i + 1 < NC)
                 ahead = weights(i + 1);
 #pragma unroll
@@ -320,6 +319,15 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
 // their products.  Scales come four steps (a turn) at a time: a thread fetches
 // those of one of the tile's rows, and they meet in LDS, power-of-two ones with a
 // lane's four steps in one word, from which the instruction picks a byte.
+//
+// Bound by the matrix units and their power with scales of rows or powers of two:
+// 8192 x 8192 x 8192 FP8 415 us (2.64 PFLOP/s) with one scale a row, 470 with
+// UE8M0 ones, FP8 x FP4 416; by the two vector operations that fp32 scales of
+// groups take for each result and 128 k with those (600 us).  4096 tokens' top-8 of
+// 64 experts: 7168 -> 4096 FP8 x FP4 970 us, 2048 -> 7168 FP8 with fp32 scales of
+// 128 columns 775.  Scales fetched step by step, in front of the products, took
+// 1226 and 926.  Small tiles for few rows, bound by the weights' bytes: one row of
+// each of 64 experts 7168 -> 4096 FP8 345 us (5.4 TB/s), FP4 227.
 struct NoScale {
     uint32_t mx;
     float one;
