@@ -37,7 +37,8 @@
  * its token, with the number of those rows given; an entry outside 0 .. rows-1
  * stands for a row of zeros, whose products with the weights are zeros whatever
  * the weights hold.  NULL: each row its own (the number of rows is then
- * n_rows or more).
+ * n_rows or more).  Products of more tiles than one launch holds (2^23 of 256 x
+ * 256 results, or 2^24 of the smallest, 64 x 16): TK_ERR_UNSUPPORTED.
  */
 #ifndef TK_EXPERT_H_
 #define TK_EXPERT_H_
