@@ -188,3 +188,14 @@ def test_backward_empty_and_unsupported():
     assert backward(n=0) == OK
     assert backward(n=0, h_dtype=BF16, dh=B, y=A, h_scales=None, scale_fmt=7) == OK
     assert backward(n=0, dy=None, h=None, h_scales=None, dh=None, dweight=None, y=None, topk_weight=None) == OK
+
+
+def test_more_tiles_than_a_launch_holds():
+    """Refused before any HIP call, whichever tiles the sizes choose."""
+    far = 1 << 60
+    for rows, columns in ((2 ** 31 - 1, 2 ** 20), (2 ** 31 - 1, 2 ** 17)):
+        assert gemm(n_rows=rows, out_features=columns, out=far) == UNSUPPORTED
+        assert plain(n_rows=rows, out_features=columns, out=far) == UNSUPPORTED
+        assert dgrad(n_rows=rows, in_features=columns, dx=far) == UNSUPPORTED
+    assert plain(n_rows=2 ** 28, experts=512, out_features=2 ** 20, out=far, x_rows=2 ** 28) == UNSUPPORTED
+    assert wgrad(experts=512, out_features=2 ** 20, in_features=2 ** 20, dw=far, x_group=0) == UNSUPPORTED
