@@ -286,9 +286,10 @@ def test_codes_numbers(x_kind, w_kind, fp4):
     lost = np.zeros_like(want)
     for k in range(0, in_f, 128):
         for i, (lo, hi) in enumerate(ex.spans(off, n)):
-            a, b = np.abs(x[lo:hi, k:k + 128]), np.abs(w[i][:, k:k + 128])
-            for r in range(lo, hi):
-                lost[r] += 128 * 2.0 ** -13 * (a[r - lo] * b).max(1)
+            a, b = (torch.from_numpy(np.abs(v)).to(DEV) for v in (x[lo:hi, k:k + 128], w[i][:, k:k + 128]))
+            for r in range(lo, hi, 32):  # (in 64 bits)
+                most = (a[r - lo:r - lo + 32, None, :] * b).amax(-1)
+                lost[r:r + len(most)] += 128 * 2.0 ** -13 * most.cpu().numpy()
     check_sum(host(out, True), True, want, mag, 3 * in_f // 128, lost)
 
 
@@ -327,3 +328,26 @@ def test_no_offsets_and_no_rows():
     assert tk.tk_expert_gemm_wgrad(None, 0, None, None, None, BF16, 0, 0, None, dev(np.zeros(3, np.int32)), 0, 2, 48, 64,
                                    0, FP32, dw) == OK
     assert not host(dw, False).any()
+
+
+@pytest.mark.parametrize("depth", [128, 72])
+def test_every_number_of_row_blocks(depth):
+    """Large tiles with one to eight blocks of 32 rows, whole steps and a last one cut short."""
+    say("row blocks", depth)
+    rng = np.random.default_rng(depth)
+    counts = [20, 64, 96, 130, 160, 161, 223, 256, 290]
+    off, n, e, wide = offsets_of(counts), sum(counts), len(counts), 4104
+    x, w = whole(rng, (n, depth)), whole(rng, (e, wide, depth))
+    want = ex.gemm(x, None, off, n, w, np.zeros((n, wide)))[0]
+    for index in (None, rng.permutation(n).astype(np.int32)):
+        rows = x if index is None else np.empty_like(x)
+        if index is not None:
+            rows[index] = x  # the row that index[r] names is x[r]
+        out = torch.zeros((n, wide), device=DEV)
+        assert tk.tk_expert_gemm(bf16(rows), None, BF16, 0, 0, n, dev(index), dev(off), n, bf16(w), None, BF16, 0, 0, e,
+                                 wide, depth, FP32, out) == OK
+        same_or(host(out, False), want, False)
+        out.zero_()
+        wt = np.ascontiguousarray(np.swapaxes(w, 1, 2))
+        assert tk.tk_expert_gemm_dgrad(bf16(rows), n, dev(index), dev(off), n, bf16(wt), e, depth, wide, FP32, out) == OK
+        same_or(host(out, False), want, False)
