@@ -543,7 +543,7 @@ __global__ __launch_bounds__(512) void gemm_big_kernel(GemmParams p)
             const uint32_t k = i * 32u + code_k, keep = code_in[i] ? ~0u : 0u;
             const uint32_t word[4] = {codes[i].x & keep, codes[i].y & keep, codes[i].z & keep, codes[i].w & keep};
             char* const to = s_c[buf] + k * (TC * 2u) + (code_s ^ hash(k)) * 32u;
-            const float scale = as_float(scale_there[i] << 23);
+            const float scale = as_float((scale_there[i] & keep) << 23); // (255, a NaN, would make one of the zeros)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 *reinterpret_cast<uint4*>(to + 16 * h) =

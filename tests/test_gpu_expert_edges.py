@@ -1,0 +1,52 @@
+"""The operators of include/tk_expert.h at the ends of what they take."""
+import numpy as np
+import pytest
+import torch
+
+import expert_ref as ex
+import layer_ref as ref
+import moe_activation_bit_amd as tk
+import test_gpu_expert_products as products
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+OK = tk.TkStatus.TK_OK
+BF16, FP32, FP8, FP4 = tk.TK_DTYPE_BF16, tk.TK_DTYPE_FP32, tk.TK_DTYPE_FP8, tk.TK_DTYPE_FP4
+INF = float("inf")
+
+
+def say(*a):
+    print("[gpu-case]", *a, flush=True)
+
+
+@pytest.mark.parametrize("gather_dy", [False, True])
+@pytest.mark.parametrize("out_f,in_f,group", [(264, 256, 0), (264, 256, 32), (136, 64, 0), (136, 64, 8)], ids=str)
+def test_wgrad_rows_of_none_take_no_scale(out_f, in_f, group, gather_dy):
+    """An entry of x_index that names no row is a row of zeros whatever the scales of x's first row are; a NaN
+    among the scales reaches the columns of its group in the experts that have its row."""
+    say("scales of rows of none", out_f, in_f, group, gather_dy)
+    rng = np.random.default_rng(out_f + group + gather_dy)
+    counts = [30, 70, 41]
+    off, n, x_rows = products.offsets_of(counts), sum(counts), 37
+    index = rng.integers(1, x_rows, n).astype(np.int32)  # nobody's: row 0
+    index[[3, 29, 30, 64, 99, 140]] = [-1, x_rows, -1, 2 ** 31 - 1, -2 ** 31, -1]
+    index[index == 36] = 1  # the last expert's alone
+    index[120] = 36
+    codes = products.whole_codes(rng, (x_rows, in_f))
+    scales = rng.integers(125, 130, (x_rows, in_f // (group or in_f))).astype(np.uint8)
+    scales[0], scales[36, 0] = 255, 255
+    dy_rows = 19 if gather_dy else n
+    dyi = rng.integers(0, dy_rows, n).astype(np.int32) if gather_dy else None
+    dy = products.whole(rng, (dy_rows, out_f))
+    dy[dy == 0] = 1
+    x = ex.coded(codes, scales, True)
+    with np.errstate(invalid="ignore"):
+        want = ex.wgrad(dy, dyi, x, index, off, n, np.zeros((3, out_f, in_f)))[0]
+    dw = torch.ones((3, out_f, in_f), device=DEV)
+    assert tk.tk_expert_gemm_wgrad(products.bf16(dy), dy_rows, products.dev(dyi), products.dev(codes), products.dev(scales),
+                                   FP8, group, x_rows, products.dev(index), products.dev(off), n, 3, out_f, in_f, 0, FP32,
+                                   dw) == OK
+    got = products.host(dw, False)
+    first = group or in_f
+    assert np.isfinite(want[:2]).all() and np.isnan(want[2, :, :first]).all() and np.isfinite(want[2, :, first:]).all()
+    assert np.array_equal(got, want.astype(np.float32), equal_nan=True)
