@@ -3,6 +3,7 @@
 // (tk_swiglu_backward), behind include/tk_expert.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -161,12 +162,11 @@ template <int FROM, bool CLAMP, int W>
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(BackwardParams p)
 {
     constexpr uint32_t kRows = kThreads / kWaveSize / W;
-    __shared__ float s_sum[kThreads / kWaveSize];
+    __shared__ float s_sum[2][kThreads / kWaveSize]; // of one pass and of the next
     const uint32_t lane = threadIdx.x & (kWaveSize - 1);
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
-    const uint32_t row = blockIdx.x * kRows + wave / W;
-    float sum = 0.0f;
-    if (row < p.n) {
+    auto gradient = [&](uint32_t row) { // the wave's part of a row; a lane's part of the sum for dweight
+        float sum = 0.0f;
         const float w = p.weight ? p.weight[row] : 1.0f;
         const uint4* const dy = p.dy + (size_t)row * p.slots;
         const size_t line = (size_t)row * (2u * p.slots);
@@ -252,30 +252,39 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(BackwardParam
             if (p.y)
                 store(p.y + (size_t)row * p.slots + slot, y2);
         }
-    }
-    if (!p.dweight) // the same for every thread
-        return;
+        return sum;
+    };
+    uint32_t parity = 0;
+    for (uint32_t row0 = blockIdx.x * kRows; row0 < p.n; row0 += gridDim.x * kRows, parity ^= 1u) {
+        const uint32_t row = row0 + wave / W;
+        float sum = row < p.n ? gradient(row) : 0.0f;
+        if (!p.dweight) // the same for every thread, as row0 is
+            continue;
 #pragma unroll
-    for (int m = kWaveSize / 2; m >= 1; m >>= 1)
-        sum += __shfl_xor(sum, m);
-    if constexpr (W > 1) {
-        if (lane == 0)
-            s_sum[wave] = sum;
-        __syncthreads();
-        if (wave % W == 0)
+        for (int m = kWaveSize / 2; m >= 1; m >>= 1)
+            sum += __shfl_xor(sum, m);
+        if constexpr (W > 1) {
+            if (lane == 0)
+                s_sum[parity][wave] = sum;
+            __syncthreads();
+            if (wave % W == 0)
 #pragma unroll
-            for (int i = 1; i < W; ++i)
-                sum += s_sum[wave + i];
+                for (int i = 1; i < W; ++i)
+                    sum += s_sum[parity][wave + i];
+        }
+        if (wave % W == 0 && lane == 0 && row < p.n)
+            p.dweight[row] = sum;
     }
-    if (wave % W == 0 && lane == 0 && row < p.n)
-        p.dweight[row] = sum;
 }
+
+// Workgroups at most, each taking several rows from there on: a launch holds fewer than 2^32 work-items.
+constexpr uint32_t kMaxBackwardBlocks = 1u << 20;
 
 template <int FROM, bool CLAMP>
 void launch_backward(const BackwardParams& p, hipStream_t s)
 {
     // 32768 x 2048 115, 111 and 109 us with one, two and four waves a row, 1000 x 2048 8, 7 and 5, 16384 x 512 16, 17, 21
-    auto blocks = [&](uint32_t rows) { return dim3((uint32_t)(((uint64_t)p.n + rows - 1) / rows)); };
+    auto blocks = [&](uint32_t rows) { return dim3(std::min((p.n + rows - 1u) / rows, kMaxBackwardBlocks)); };
     if (p.slots <= kWaveSize)
         hipLaunchKernelGGL((swiglu_backward_kernel<FROM, CLAMP, 1>), blocks(4), dim3(kThreads), 0, s, p);
     else if (p.slots <= 2 * kWaveSize)
@@ -412,8 +421,6 @@ extern "C" tk_status tk_swiglu_backward(const void* dy, const void* h, const voi
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool clamp = !std::isinf(clamp_limit);
     const int from = !fp8 ? kFromBf16 : f32 ? kFromF32 : kFromE8;
-    if (p.slots > 2 * kWaveSize && rows * kThreads >= (1ull << 32))
-        return TK_ERR_UNSUPPORTED;
     switch (from * 2 + clamp) {
     case 0: launch_backward<kFromBf16, false>(p, s); break;
     case 1: launch_backward<kFromBf16, true>(p, s); break;

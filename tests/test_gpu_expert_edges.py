@@ -50,3 +50,41 @@ def test_wgrad_rows_of_none_take_no_scale(out_f, in_f, group, gather_dy):
     first = group or in_f
     assert np.isfinite(want[:2]).all() and np.isnan(want[2, :, :first]).all() and np.isfinite(want[2, :, first:]).all()
     assert np.array_equal(got, want.astype(np.float32), equal_nan=True)
+
+
+def backward_rows(n, hidden, fp8, gen):
+    """n rows of dy and h, few distinct ones, on the device."""
+    dy = torch.randn((64, hidden), generator=gen, device=DEV).to(torch.bfloat16)
+    dy = dy.repeat((n + 63) // 64, 1)[:n].contiguous()
+    if fp8:
+        h = torch.randint(0, 120, (64, 2 * hidden), generator=gen, device=DEV, dtype=torch.uint8)
+        scales = torch.randint(110, 125, (n, 1), generator=gen, device=DEV, dtype=torch.uint8)
+    else:
+        h, scales = torch.randn((64, 2 * hidden), generator=gen, device=DEV).to(torch.bfloat16), None
+    return dy, h.repeat((n + 63) // 64, 1)[:n].contiguous(), scales
+
+
+@pytest.mark.parametrize("n,hidden,fp8", [(2 ** 26 + 5, 8, True), (2 ** 22 + 7, 8, False), (2 ** 21 + 3, 520, True),
+                                          (2 ** 20 + 9, 1032, True)], ids=str)
+def test_backward_of_more_rows_than_workgroups(n, hidden, fp8):
+    """2^32 work-items are the most that a launch holds: rows beyond the grid's are taken by the same workgroups."""
+    say("backward rows", n, hidden, fp8)
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    dy, h, scales = backward_rows(n, hidden, fp8, gen)
+    weight = torch.rand(n, generator=gen, device=DEV)
+    kind, fmt, group = (FP8, 1, 0) if fp8 else (BF16, 0, 0)
+
+    def outputs(rows):
+        return (torch.zeros((rows, 2 * hidden), dtype=torch.bfloat16, device=DEV), torch.zeros(rows, device=DEV),
+                torch.zeros((rows, hidden), dtype=torch.bfloat16, device=DEV))
+
+    whole = outputs(n)
+    assert tk.tk_swiglu_backward(dy, h, scales, kind, fmt, group, weight, n, hidden, 2.0, *whole) == OK
+    most = 1 << 19  # rows that one pass of the grid takes at any width
+    part = outputs(most)
+    for lo in range(0, n, most):
+        rows = min(most, n - lo)
+        assert tk.tk_swiglu_backward(dy[lo:], h[lo:], scales[lo:] if fp8 else None, kind, fmt, group, weight[lo:], rows,
+                                     hidden, 2.0, *part) == OK
+        for a, b in zip(whole, part):
+            assert torch.equal(a[lo:lo + rows], b[:rows])
