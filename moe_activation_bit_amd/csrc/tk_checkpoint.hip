@@ -88,15 +88,14 @@ __global__ __launch_bounds__(kThreads) void swiglu_checkpoint_kernel(Params p, P
             finish(p, codes, slot, y, m);
             auto as_is = [&](const uint4& v, uint32_t at) {
                 const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-                float x[8];
-                uint32_t top = 0;
+                float x[8], top = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     x[2 * k] = as_float(word[k] << 16);
                     x[2 * k + 1] = as_float(word[k] & 0xFFFF0000u);
-                    top = max(top, max(word[k] << 16 & 0x7FFFFFFFu, word[k] & 0x7FFF0000u));
+                    top = fmaxf(top, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1]))); // (passes over NaN, as tk_cast_fp8)
                 }
-                finish(px, x_codes, at, x, top);
+                finish(px, x_codes, at, x, as_uint(top));
             };
             as_is(g[s], slot);
             as_is(up[s], p.slots + slot);

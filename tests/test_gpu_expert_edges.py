@@ -88,3 +88,31 @@ def test_backward_of_more_rows_than_workgroups(n, hidden, fp8):
                                      hidden, 2.0, *part) == OK
         for a, b in zip(whole, part):
             assert torch.equal(a[lo:lo + rows], b[:rows])
+
+
+@pytest.mark.parametrize("clamp", [INF, 2.5])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("n,hidden,group", [(37, 1024, 128), (5, 520, 8), (64, 96, 32), (130, 1536, 512),
+                                            (16390, 2048, 128)])
+def test_checkpoint_has_the_bits_of_two_calls_with_nan_too(n, hidden, group, fmt, clamp):
+    """A NaN or an infinity among the inputs leaves what the two calls leave, in its group and in the others."""
+    say("checkpoint NaN", n, hidden, group, fmt, clamp)
+    gen = torch.Generator(device=DEV).manual_seed(n + hidden)
+    x = (torch.randn((n, 2 * hidden), generator=gen, device=DEV) * 3).to(torch.bfloat16)
+    at = torch.rand(x.shape, generator=gen, device=DEV)
+    for i, bits in enumerate((0x7FC0, 0x7F81, -0x40, 0x7F80, -0x80)):  # NaN of either sign, infinities
+        x.view(torch.int16).masked_fill_((at >= i * 3e-3) & (at < (i + 1) * 3e-3), bits)
+    weight = torch.rand(n, generator=gen, device=DEV)
+
+    def buffers(cols):
+        return (torch.full((n + 1, cols), 0xA5, dtype=torch.uint8, device=DEV),
+                torch.full((n + 1, cols // group), 77, dtype=torch.uint8 if fmt else torch.float32, device=DEV))
+
+    (c0, s0), (c1, s1) = buffers(hidden), buffers(hidden)
+    (xc0, xs0), (xc1, xs1) = buffers(2 * hidden), buffers(2 * hidden)
+    assert tk.tk_swiglu_cast_fp8(x, weight, n, hidden, group, clamp, fmt, c0, s0) == OK
+    assert tk.tk_cast_fp8(x, 0, n, 2 * hidden, group, fmt, xc0, xs0) == OK
+    assert tk.tk_swiglu_checkpoint_fp8(x, weight, n, hidden, group, clamp, fmt, c1, s1, xc1, xs1) == OK
+    torch.cuda.synchronize()
+    for a, b in ((c0, c1), (s0, s1), (xc0, xc1), (xs0, xs1)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
