@@ -76,7 +76,8 @@ extern "C" {
  *               (UE8M0) or 128 (FP32) columns (other divisors:
  *               TK_ERR_UNSUPPORTED).  For bf16 NULL, x_scale_fmt and x_group
  *               then being ignored.
- *  x_rows       0 <= x_rows < 2^31.
+ *  x_rows       0 <= x_rows < 2^31; with 0, x and x_scales may be NULL (an empty
+ *               tensor has no address), as dy may be with 0 dy_rows.
  *  row_index    int32 [n_rows], 4-byte aligned, or NULL.
  *  expert_offsets  int32 [experts + 1], 4-byte aligned, or NULL (experts 1).
  *  n_rows       0 <= n_rows < 2^31.

@@ -856,7 +856,7 @@ extern "C" tk_status tk_expert_gemm_dgrad(const void* dy, int64_t dy_rows, const
     if (!valid_rows(rows, expert_offsets, n_rows, experts) || !valid_shape(out_features, in_features, 8) ||
         (!out_bf16 && (int)out_dtype != TK_DTYPE_FP32))
         return TK_ERR_INVALID_ARG;
-    if (n_rows > 0 && (!dy || !w || !dx))
+    if (n_rows > 0 && ((dy_rows > 0 && !dy) || !w || !dx))
         return TK_ERR_INVALID_ARG;
     if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(dx, 16))
         return TK_ERR_INVALID_ARG;
@@ -906,7 +906,7 @@ extern "C" tk_status tk_expert_gemm_wgrad(const void* dy, int64_t dy_rows, const
         return TK_ERR_INVALID_ARG;
     if (fp8 && (x_group < 0 || (x_group && in_features % x_group != 0)))
         return TK_ERR_INVALID_ARG;
-    if (!dw || (n_rows > 0 && (!dy || !x || (fp8 && !x_scales))))
+    if (!dw || (n_rows > 0 && ((dy_rows > 0 && !dy) || (x_rows > 0 && (!x || (fp8 && !x_scales))))))
         return TK_ERR_INVALID_ARG;
     if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16))
         return TK_ERR_INVALID_ARG;

@@ -755,7 +755,7 @@ extern "C" tk_status tk_expert_gemm(const void* x, const void* x_scales, int x_d
     };
     if ((x8 && bad_scales((int)x_scale_fmt, x_group)) || ((w8 || w4) && bad_scales((int)w_scale_fmt, w_group)))
         return TK_ERR_INVALID_ARG;
-    if (n_rows > 0 && (!x || !w || !out || (x8 && !x_scales) || ((w8 || w4) && !w_scales)))
+    if (n_rows > 0 && ((x_rows > 0 && (!x || (x8 && !x_scales))) || !w || !out || ((w8 || w4) && !w_scales)))
         return TK_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) ||
         (x8 && (int)x_scale_fmt == TK_SCALE_FP32 && !aligned(x_scales, 4)) ||

@@ -116,3 +116,35 @@ def test_checkpoint_has_the_bits_of_two_calls_with_nan_too(n, hidden, group, fmt
     torch.cuda.synchronize()
     for a, b in ((c0, c1), (s0, s1), (xc0, xc1), (xs0, xs1)):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_no_rows_and_no_address():
+    """x or dy of no rows has no address (torch's is 0): every index names none, every result is zero."""
+    off = products.dev(np.array([0, 70, 80], np.int32))
+    index = products.dev(np.arange(80, dtype=np.int32))
+    none = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
+    codes = torch.empty((0, 64), dtype=torch.uint8, device=DEV)
+    scales = torch.empty((0, 2), dtype=torch.uint8, device=DEV)
+    assert none.data_ptr() == codes.data_ptr() == scales.data_ptr() == 0
+    w = torch.ones((2, 64, 64), dtype=torch.bfloat16, device=DEV)
+    y = torch.ones((80, 64), device=DEV)
+    assert tk.tk_expert_gemm(none, None, BF16, 0, 0, 0, index, off, 80, w, None, BF16, 0, 0, 2, 64, 64, FP32, y) == OK
+    assert not y.any()
+    y.fill_(1)
+    assert tk.tk_expert_gemm_dgrad(none, 0, index, off, 80, w, 2, 64, 64, FP32, y) == OK
+    assert not y.any()
+    w8 = torch.full((128, 64), 0x38, dtype=torch.uint8, device=DEV)
+    for x_group, w_group in ((32, 32), (0, 32), (32, 0)):
+        ws = torch.full((128, 64 // (w_group or 64)), 127, dtype=torch.uint8, device=DEV)
+        out = torch.ones((80, 64), dtype=torch.bfloat16, device=DEV)
+        assert tk.tk_expert_gemm(codes, scales, FP8, 1, x_group, 0, index, off, 80, w8, ws, FP8, 1, w_group, 2, 64, 64,
+                                 BF16, out) == OK
+        assert not out.any()
+    dy = torch.ones((80, 64), dtype=torch.bfloat16, device=DEV)
+    start = torch.arange(2 * 64 * 64, device=DEV, dtype=torch.float32).view(2, 64, 64)
+    for accumulate in (0, 1):
+        for args in ((dy, 80, None, none, None, BF16, 0, 0, index), (none, 0, index, dy, None, BF16, 0, 80, None),
+                     (dy, 80, None, codes, scales, FP8, 32, 0, index), (none, 0, index, none, None, BF16, 0, 0, index)):
+            dw = start.clone()
+            assert tk.tk_expert_gemm_wgrad(*args, off, 80, 2, 64, 64, accumulate, FP32, dw) == OK
+            assert torch.equal(dw, start if accumulate else torch.zeros_like(start))
