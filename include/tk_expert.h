@@ -66,7 +66,10 @@ extern "C" {
  * result does not show as long as the sum is not much smaller than its largest
  * term; so they have no fp32 results.  UE8M0 scales of groups of columns enter
  * the instruction, one scale a row is applied to the finished sum, and fp32
- * scales of groups to each 128 columns' sum, all in fp32.
+ * scales of groups to each 128 columns' sum, all in fp32: a sum with its groups'
+ * scales, and the product of two fp32 scales of groups, have to lie in its range;
+ * of two scales a row only their product and the result have to.  A scale that is a
+ * NaN (UE8M0 byte 255) makes one of what it scales.
  *
  *  x            [x_rows, in_features]: TK_DTYPE_BF16 elements, or TK_DTYPE_FP8
  *               codes with x_scales.  16-byte aligned.

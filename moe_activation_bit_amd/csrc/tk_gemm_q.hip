@@ -46,6 +46,16 @@ __device__ __forceinline__ float e8m0_value(uint32_t b)
     return b == 0u ? 0x1p-127f : as_float(b == 255u ? 0x7FC00000u : b << 23);
 }
 
+// A finished sum times one scale a row of x and one of the weights.  Of x's, what is below 1 comes before the weights'
+// and what is above behind it: two scales at the ends of the range, whose product is an ordinary number, do not
+// overflow on the way.  (Nor do powers of two lose bits: a sum is a multiple of 2^-18, and a multiple of 2^-145
+// below 2^-121 is a fp32 number.)
+struct RowScale {
+    float before, after;
+    __device__ __forceinline__ explicit RowScale(float r) : before(r < 1.0f ? r : 1.0f), after(r < 1.0f ? 1.0f : r) {}
+    __device__ __forceinline__ float operator()(float sum, float c_scale) const { return sum * before * c_scale * after; }
+};
+
 // Groups of any width (a scale of one step, read in front of its products, may serve many steps or a part of one), and
 // UE8M0 bytes at any address.  The layout and the pace of gemm_kernel (tk_gemm.hip) with 128 k a step and two steps in
 // LDS; bound by reading the scales: FP4 weights with scales of 32 columns, one row of each of 64 experts 7168 -> 4096,
@@ -298,7 +308,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
             continue;
         const uint32_t at = source(row);
         const bool none = at >= p.x_rows;
-        const float r_scale = none ? 0.0f : row_scale(p.xs, at);
+        const RowScale scale(none ? 0.0f : row_scale(p.xs, at));
         const size_t line = (size_t)(row0 + row) * p.cols;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -308,7 +318,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
             v4b v;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                v[e] = (__bf16)(none ? 0.0f : acc[i][j][e] * r_scale * c_scale[i][e]);
+                v[e] = (__bf16)(none ? 0.0f : scale(acc[i][j][e], c_scale[i][e]));
             *reinterpret_cast<v4b*>(static_cast<__bf16*>(p.out) + line + col) = v;
         }
     }
@@ -618,13 +628,13 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p
         for (int j = 0; j < N; ++j) {
             const uint32_t row = row_of(j) + r, at = source(row);
             const bool none = at >= p.x_rows;
-            const float r_scale = none ? 0.0f : row_scale(p.xs, at);
+            const RowScale scale(none ? 0.0f : row_scale(p.xs, at));
             const size_t line = (size_t)(row0 + row) * p.cols;
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = none ? 0.0f : acc[i][j][e] * r_scale * c_scale[i][e];
+                    acc[i][j][e] = none ? 0.0f : scale(acc[i][j][e], c_scale[i][e]);
             if constexpr (kBlocks % 2 == 0) {
 #pragma unroll
                 for (int i = 0; i < kBlocks; i += 2) {

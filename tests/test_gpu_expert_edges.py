@@ -148,3 +148,38 @@ def test_no_rows_and_no_address():
             dw = start.clone()
             assert tk.tk_expert_gemm_wgrad(*args, off, 80, 2, 64, 64, accumulate, FP32, dw) == OK
             assert torch.equal(dw, start if accumulate else torch.zeros_like(start))
+
+
+@pytest.mark.parametrize("counts,out_f", [([9, 5], 72), ([90, 40], 1032), ([300, 90], 8200)], ids=str)
+@pytest.mark.parametrize("x_group,w_group", [(0, 0), (32, 32), (0, 32), (128, 0), (64, 64)], ids=str)
+def test_gemm_scale_bytes_at_the_ends(x_group, w_group, counts, out_f):
+    """Scales of 2^-127 to 2^127 against each other, over every tile size: the product of a row's two scales is
+    anything that a result of normal size may have (of groups against one a row, which the sum with the groups' scales
+    meets later, those that leave this sum in fp32's range); byte 255 is a NaN in its row (its column) alone."""
+    say("scale bytes", x_group, w_group, counts, out_f)
+    rng = np.random.default_rng(out_f + x_group + w_group)
+    off, n, e, in_f = products.offsets_of(counts), sum(counts), 2, 512
+
+
+    def operand(rows, first, small, large, group, other):
+        """Scale bytes of the rows of expert 0 (`first` of them) and of expert 1."""
+        byte = np.array([(small if r < first else large)[r % len(small)] for r in range(rows)])
+        if group and not other:
+            byte = np.clip(byte, 20, 227)
+        scales = np.repeat(byte[:, None], in_f // (group or in_f), 1).astype(np.uint8)
+        scales[3] = 255
+        codes = products.whole_codes(rng, (rows, in_f))
+        return codes, scales, ex.coded(codes, scales, True)
+
+    xc, xs, x = operand(n, counts[0], (0, 3, 60), (254, 251, 200), x_group, w_group)
+    wc, ws, w = operand(e * out_f, out_f, (254, 190), (0, 40), w_group, x_group)
+    out = torch.zeros((n, out_f), dtype=torch.int16, device=DEV)
+    assert tk.tk_expert_gemm(products.dev(xc), products.dev(xs), FP8, 1, x_group, n, None, products.dev(off), n,
+                             products.dev(wc), products.dev(ws), FP8, 1, w_group, e, out_f, in_f, BF16, out) == OK
+    got = products.host(out, True)
+    with np.errstate(all="ignore"):
+        want = np.concatenate([x[lo:hi] @ w[i * out_f:(i + 1) * out_f].T for i, (lo, hi) in enumerate(ex.spans(off, n))])
+        want = ref.round_bf16(want.astype(np.float32))  # whole numbers times powers of two: exact before the rounding
+    normal = np.isnan(want) | (want == 0) | (np.abs(want) >= 2.0 ** -126)
+    assert np.isnan(want).sum() > n and normal.mean() > 0.9
+    assert np.array_equal(got[normal], want[normal], equal_nan=True)
