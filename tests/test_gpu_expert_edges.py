@@ -183,3 +183,25 @@ def test_gemm_scale_bytes_at_the_ends(x_group, w_group, counts, out_f):
     normal = np.isnan(want) | (want == 0) | (np.abs(want) >= 2.0 ** -126)
     assert np.isnan(want).sum() > n and normal.mean() > 0.9
     assert np.array_equal(got[normal], want[normal], equal_nan=True)
+
+
+@pytest.mark.parametrize("out_f,in_f,group", [(200, 256, 0), (200, 256, 16), (24, 256, 0), (24, 256, 8)], ids=str)
+def test_wgrad_scale_bytes_at_the_ends(out_f, in_f, group):
+    """Every code under every scale byte, one row an expert: the value as bf16 holds it (below 2^-133 rounded, from
+    2^128 on infinite, byte 255 a NaN) times a power of two."""
+    say("wgrad scale bytes", out_f, in_f, group)
+    codes = np.tile(np.arange(256, dtype=np.uint8), (256, 1))
+    scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], in_f // (group or in_f), 1)
+    off = np.arange(257, dtype=np.int32)
+    for power in (0, 40, -40):
+        dy = np.full((256, out_f), 2.0 ** power, np.float32)
+        dw = torch.zeros((256, out_f, in_f), device=DEV)
+        assert tk.tk_expert_gemm_wgrad(products.bf16(dy), 256, None, products.dev(codes), products.dev(scales), FP8, group,
+                                       256, None, products.dev(off), 256, 256, out_f, in_f, 0, FP32, dw) == OK
+        got = products.host(dw, False)
+        with np.errstate(all="ignore"):
+            x = ref.round_bf16(ex.coded(codes, scales, True).astype(np.float32))
+            want = (x.astype(np.float64) * 2.0 ** power).astype(np.float32)
+        for row in range(256):
+            for o in (0, out_f - 1):
+                assert np.array_equal(got[row, o], want[row], equal_nan=True), (power, row, o)
