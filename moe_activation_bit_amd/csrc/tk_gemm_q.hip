@@ -60,8 +60,8 @@ struct RowScale {
 // UE8M0 bytes at any address.  The layout and the pace of gemm_kernel (tk_gemm.hip) with 128 k a step and two steps in
 // LDS; bound by reading the scales: FP4 weights with scales of 32 columns, one row of each of 64 experts 7168 -> 4096,
 // 299 us where gemm_q_turn_kernel takes 227.
-// W4: weights in FP4.  MX: some operand has power-of-two scales of groups.  STEP: some operand has fp32 ones.
-template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
+// W4: weights in FP4.  STEP: one operand has fp32 scales of groups (the other, or both, have power-of-two ones).
+template <bool W4, bool STEP, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
 {
     constexpr uint32_t kWaves = WC * WR, kThr = 64 * kWaves;
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
     constexpr int kOwn = (TC + TR + kThr - 1) / kThr; // rows whose scales a thread fetches
     __shared__ __attribute__((aligned(1024))) char s_c[2][kBytesC];
     __shared__ __attribute__((aligned(1024))) char s_r[2][kBytesR];
-    __shared__ uint32_t s_mx[MX ? 2 : 1][MX ? TC + TR : 1];
+    __shared__ uint32_t s_mx[2][TC + TR];
     __shared__ __attribute__((aligned(16))) float s_step[STEP ? 2 : 1][STEP ? TC + TR : 1];
 
     const uint32_t lane = threadIdx.x & (kWaveSize - 1), r = lane & 15u, q = lane >> 4;
@@ -163,34 +163,32 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
         own_row[i] = row < TC ? w_row0 + min(row, p.cols - 1u - col0) : min(source(row - TC), p.x_rows);
     }
     auto fetch_scales = [&](uint32_t t) {
-        if constexpr (MX || STEP) {
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) {
-                const uint32_t row = i * kThr + threadIdx.x;
-                const bool weights = row < TC; // the same for the whole wave
-                const Scales& s = weights ? p.ws : p.xs;
-                const bool none = row >= TC + TR || (!weights && own_row[i] >= p.x_rows);
-                own_mx[i] = 0x7F7F7F7Fu;
-                own_step[i] = 1.0f;
-                if (none)
-                    continue;
-                if (MX && s.kind == kScaleMx) {
-                    const uint8_t* const at = static_cast<const uint8_t*>(s.at) + own_row[i] * s.groups;
-                    const uint32_t block = 4u * t, last = depth / 32u - 1u;
-                    if (s.words && s.width == 1)
-                        own_mx[i] = *reinterpret_cast<const uint32_t*>(at + block);
-                    else if (s.width % 4u == 0)
-                        own_mx[i] = at[t / (s.width / 4u)] * 0x01010101u;
-                    else {
-                        uint32_t v = 0;
-                        for (uint32_t b = 0; b < 4u; ++b)
-                            v |= (block + b <= last ? (uint32_t)at[(block + b) / s.width] : 127u) << (8u * b);
-                        own_mx[i] = v;
-                    }
+        for (int i = 0; i < kOwn; ++i) {
+            const uint32_t row = i * kThr + threadIdx.x;
+            const bool weights = row < TC; // the same for the whole wave
+            const Scales& s = weights ? p.ws : p.xs;
+            const bool none = row >= TC + TR || (!weights && own_row[i] >= p.x_rows);
+            own_mx[i] = 0x7F7F7F7Fu;
+            own_step[i] = 1.0f;
+            if (none)
+                continue;
+            if (s.kind == kScaleMx) {
+                const uint8_t* const at = static_cast<const uint8_t*>(s.at) + own_row[i] * s.groups;
+                const uint32_t block = 4u * t, last = depth / 32u - 1u;
+                if (s.words && s.width == 1)
+                    own_mx[i] = *reinterpret_cast<const uint32_t*>(at + block);
+                else if (s.width % 4u == 0)
+                    own_mx[i] = at[t / (s.width / 4u)] * 0x01010101u;
+                else {
+                    uint32_t v = 0;
+                    for (uint32_t b = 0; b < 4u; ++b)
+                        v |= (block + b <= last ? (uint32_t)at[(block + b) / s.width] : 127u) << (8u * b);
+                    own_mx[i] = v;
                 }
-                if (STEP && s.kind == kScaleStep)
-                    own_step[i] = static_cast<const float*>(s.at)[own_row[i] * s.groups + t / s.width];
             }
+            if (STEP && s.kind == kScaleStep)
+                own_step[i] = static_cast<const float*>(s.at)[own_row[i] * s.groups + t / s.width];
         }
     };
     auto put_scales = [&](uint32_t buf) {
@@ -198,8 +196,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
         for (int i = 0; i < kOwn; ++i) {
             const uint32_t row = i * kThr + threadIdx.x;
             if (kOwn * kThr == TC + TR || row < TC + TR) {
-                if constexpr (MX)
-                    s_mx[buf][row] = own_mx[i];
+                s_mx[buf][row] = own_mx[i];
                 if constexpr (STEP)
                     s_step[buf][row] = own_step[i];
             }
@@ -225,7 +222,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
             const char* const at = s_r[buf] + row * 128u;
             b[j] = join(*reinterpret_cast<const v4u*>(at + (q ^ (r & 7u)) * 16u),
                         *reinterpret_cast<const v4u*>(at + ((q + 4u) ^ (r & 7u)) * 16u));
-            b_mx[j] = MX ? reinterpret_cast<const uint8_t*>(s_mx[buf] + TC + row)[q] : 127;
+            b_mx[j] = reinterpret_cast<const uint8_t*>(s_mx[buf] + TC + row)[q];
             b_step[j] = STEP ? s_step[buf][TC + row] : 1.0f;
         }
         struct Weights {
@@ -244,7 +241,7 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
                 a.v = join(*reinterpret_cast<const v4u*>(at + (q ^ (r & 7u)) * 16u),
                            *reinterpret_cast<const v4u*>(at + ((q + 4u) ^ (r & 7u)) * 16u));
             }
-            a.mx = MX ? reinterpret_cast<const uint8_t*>(s_mx[buf] + row)[q] : 127;
+            a.mx = reinterpret_cast<const uint8_t*>(s_mx[buf] + row)[q];
             a.step = STEP ? *reinterpret_cast<const v4f*>(s_step[buf] + 16u * (wc * NC + i) + 4u * q)
                           : v4f{1.0f, 1.0f, 1.0f, 1.0f};
             return a;
@@ -695,13 +692,13 @@ tk_status launch_turn(const QuantParams& p, hipStream_t s)
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
 
-template <bool W4, bool MX, bool STEP, int TC, int TR, int WC, int WR>
+template <bool W4, bool STEP, int TC, int TR, int WC, int WR>
 tk_status launch(const QuantParams& p, hipStream_t s)
 {
     const uint64_t blocks = workgroups(p, TC, TR);
     if (!launchable(blocks, 64 * WC * WR))
         return TK_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((gemm_q_kernel<W4, MX, STEP, TC, TR, WC, WR>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0, s,
+    hipLaunchKernelGGL((gemm_q_kernel<W4, STEP, TC, TR, WC, WR>), dim3((uint32_t)blocks), dim3(64 * WC * WR), 0, s,
                        p);
     return hipGetLastError() == hipSuccess ? TK_OK : TK_ERR_HIP;
 }
@@ -714,16 +711,14 @@ tk_status launch_size(const QuantParams& p, hipStream_t s)
     auto tiles = [&](uint32_t tr, uint32_t tc) { return tiles_of(load, p.experts, p.cols, tr, tc); };
     auto turns = [](const Scales& a) { return a.kind != kScaleMx || (a.words && (a.width == 1 || a.width == 4)); };
     const bool mid = load > 16 && tiles(64, 128) >= 128;
-    if (turns(p.ws) && turns(p.xs)) {
-        if (load > 64 && tiles(256, 256) >= 128)
-            return launch_turn<W4, MX, STEP, 256, 256, 4, 2, 2>(p, s);
-        if (mid)
-            return launch_turn<W4, MX, STEP, 128, 64, 2, 2, 3>(p, s);
-        return launch_turn<W4, MX, STEP, 64, 16, 4, 1, 4>(p, s);
-    }
+    if constexpr (MX)
+        if (!turns(p.ws) || !turns(p.xs))
+            return mid ? launch<W4, STEP, 128, 64, 2, 2>(p, s) : launch<W4, STEP, 64, 16, 4, 1>(p, s);
+    if (load > 64 && tiles(256, 256) >= 128)
+        return launch_turn<W4, MX, STEP, 256, 256, 4, 2, 2>(p, s);
     if (mid)
-        return launch<W4, MX, STEP, 128, 64, 2, 2>(p, s);
-    return launch<W4, MX, STEP, 64, 16, 4, 1>(p, s);
+        return launch_turn<W4, MX, STEP, 128, 64, 2, 2, 3>(p, s);
+    return launch_turn<W4, MX, STEP, 64, 16, 4, 1, 4>(p, s);
 }
 
 // The scales of rows of `depth` columns in groups of `group` (0: the row).  False: not taken.
