@@ -36,9 +36,13 @@
  * A row index is int32 [n_rows]: the row of x (or dy) that each row takes, e.g.
  * its token, with the number of those rows given; an entry outside 0 .. rows-1
  * stands for a row of zeros, whose products with the weights are zeros whatever
- * the weights hold.  NULL: each row its own (the number of rows is then
- * n_rows or more).  Products of more tiles than one launch holds (2^23 of 256 x
- * 256 results, or 2^24 of the smallest, 64 x 16): TK_ERR_UNSUPPORTED.
+ * the weights hold (in the weights' gradient, times an infinity or a NaN in the
+ * other operand's row, a NaN as with any zero).  NULL: each row its own (the
+ * number of rows is then n_rows or more).  Products of more tiles than one launch
+ * holds (2^23 of 256 x 256 results, or 2^24 of the smallest, 64 x 16):
+ * TK_ERR_UNSUPPORTED.  The tiles are chosen by n_rows / experts, since how the rows
+ * lie is not known on the host: rows that nearly all fall to a few of many experts
+ * are multiplied in smaller tiles, and more slowly, than those would choose alone.
  */
 #ifndef TK_EXPERT_H_
 #define TK_EXPERT_H_
@@ -64,7 +68,8 @@ extern "C" {
  * matrix instruction for them, 128 columns at a time: sums in fp32, but of each
  * 128 products what lies some 2^-14 below the largest is dropped, which a bf16
  * result does not show as long as the sum is not much smaller than its largest
- * term; so they have no fp32 results.  UE8M0 scales of groups of columns enter
+ * term; so they have no fp32 results, and a sum that nearly cancels differs from
+ * that of tk_expert_gemv_fp4, whose products are exact.  UE8M0 scales of groups of columns enter
  * the instruction, one scale a row is applied to the finished sum, and fp32
  * scales of groups to each 128 columns' sum, all in fp32: a sum with its groups'
  * scales, and the product of two fp32 scales of groups, have to lie in its range;
@@ -131,7 +136,7 @@ tk_status tk_expert_gemm_dgrad(const void* dy, int64_t dy_rows, const int32_t* r
  *              multiple of 8; other divisors: TK_ERR_UNSUPPORTED).  Their values,
  *              code * 2^(byte-127), are bf16 numbers, so that the products are
  *              exact (those of fp32 scales would not be); below 2^-133 they are
- *              rounded.
+ *              rounded, from 2^128 on infinite, and under the byte 255 NaN.
  *  accumulate  0: dw is overwritten, with zeros for an expert without rows; 1:
  *              the sum is added to dw in fp32 before the rounding.
  *  dw          [experts, out_features, in_features] of out_dtype (TK_DTYPE_BF16

@@ -30,7 +30,7 @@ struct NoCount { // (the clamp's counter is tk_swiglu_cast_fp8's alone)
 // same table, products and cast), and both halves are cast as they are, each
 // group of 2^gl_log2 lanes by its own abs-max.  Bound by its bytes: 4 read and 3
 // written for each column (two calls: 8 and 3).  32768 x 2048 in groups of 128: 87
-// us, 5.4 TB/s; 349 x 7168 7.0, the table's copy into LDS and one trip to memory.
+// us, 5.4 TB/s; 349 x 7168 6.3, the table's copy into LDS and one trip to memory.
 template <int SFMT, bool CLAMP, int SPU>
 __global__ __launch_bounds__(kThreads) void swiglu_checkpoint_kernel(Params p, Params px, const float2* table)
 {

@@ -830,7 +830,9 @@ namespace tk_gemm {
 // Which tiles: the largest that the rows of an expert fill, of which there are enough for 256 CUs.  In us, 4096 ->
 // 4096 for one expert: 64 rows 50 with 256 x 256 tiles, 29 with 128 columns x 64 rows, 19 with 64 x 64, 15 with 64 x
 // 16; 256 rows 78, 30, 21, 35; 1024 rows 81, 45, 56, 133; 4096 rows 125, 200, 240, 494.  7168 -> 4096 for 64 experts:
-// 24 rows each 772, 668, 697, 859; 64 each 787, 694, 794, 1324; 128 each 793 (256 x 256), 942 (128 x 64).
+// 24 rows each 772, 668, 697, 859; 64 each 787, 694, 794, 1324; 128 each 793 (256 x 256), 942 (128 x 64).  The rows of
+// each expert are on the device; their average stands for them: 1000 rows of 4096 -> 4096 that all fall to one of 64
+// experts take 138 us in 64 x 16 tiles (42 where that expert is the only one).
 tk_status launch_forward(const GemmParams& p, hipStream_t s)
 {
     const uint64_t load = average_rows(p.n_rows, p.experts);
@@ -943,6 +945,8 @@ extern "C" tk_status tk_expert_gemm_wgrad(const void* dy, int64_t dy_rows, const
     p.out_bf16 = out_bf16;
     p.accumulate = accumulate;
     hipStream_t s = static_cast<hipStream_t>(stream);
+    // The large tiles wherever a result is not much smaller than one, however few there are: a sum is one workgroup's.
+    // 8192 rows of one expert 1024 x 1024 165 us (16 workgroups, 128 steps each), of eight experts 35.
     if (p.out_rows >= 192 && p.cols >= 192 && (!fp8 || group % 16 == 0)) {
         if (fp8)
             return x_index ? (dy_index ? launch_big<kWgrad, true, true, true>(p, s) : launch_big<kWgrad, true, true>(p, s))

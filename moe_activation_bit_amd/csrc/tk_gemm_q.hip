@@ -327,14 +327,18 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_kernel(QuantParams p)
 // those of one of the tile's rows, and they meet in LDS, power-of-two ones with a
 // lane's four steps in one word, from which the instruction picks a byte.
 //
-// Bound by the matrix units and their power with scales of rows or powers of two:
-// 8192 x 8192 x 8192 FP8 415 us (2.64 PFLOP/s) with one scale a row, 470 with
-// UE8M0 ones, FP8 x FP4 416; by the two vector operations that fp32 scales of
-// groups take for each result and 128 k with those (600 us).  4096 tokens' top-8 of
-// 64 experts: 7168 -> 4096 FP8 x FP4 970 us, 2048 -> 7168 FP8 with fp32 scales of
-// 128 columns 775.  Scales fetched step by step, in front of the products, took
-// 1226 and 926.  Small tiles for few rows, bound by the weights' bytes: one row of
-// each of 64 experts 7168 -> 4096 FP8 345 us (5.4 TB/s), FP4 227.
+// 8192 x 8192 x 8192 FP8 410 .. 450 us (2.4 .. 2.7 PFLOP/s) with one scale a row,
+// the matrix units busy in 59% of cycles at 1.9 .. 2.0 GHz; 460 with UE8M0 scales
+// of groups (50%, 2.1 GHz); FP8 x FP4 412 (54%); fp32 scales of groups, whose two
+// vector operations for each result and 128 k take half of the cycles, 600 (39%).
+// What is open beside them: a step's first fragments are read behind the meeting,
+// and a tile's start (offsets, index, first copies) and its stores lie between
+// sums.  These count for more where sums are short and experts' rows ragged: 4096
+// tokens' top-8 of 64 experts 7168 -> 4096 FP8 x FP4 970 us (42%), 2048 -> 7168
+// FP8 with fp32 scales of 128 columns 775 (25%).  Scales fetched step by step, in
+// front of the products, took 1226 and 926.  Small tiles for few rows, bound by
+// the weights' bytes: one row of each of 64 experts 7168 -> 4096 FP8 345 us (5.4
+// TB/s), FP4 227.
 struct NoScale {
     uint32_t mx;
     float one;
@@ -653,7 +657,9 @@ __global__ __launch_bounds__(64 * WC * WR) void gemm_q_turn_kernel(QuantParams p
     using std::bool_constant;
     using std::integral_constant;
     auto run_blocks = [&](auto fast) {
-        if constexpr (kRowBlocks == 8) { // large tiles: no more blocks than there are rows
+        // Large tiles: no more blocks than there are rows, in even numbers (FP8 x FP4 964 us with odd ones too instead of
+        // 976, FP8 785 and 782; they would double these kernels).
+        if constexpr (kRowBlocks == 8) {
             const uint32_t blocks = uniform((rows + 16u * WR - 1u) / (16u * WR));
             if (blocks > 6)
                 run(integral_constant<int, 8>{}, fast);
