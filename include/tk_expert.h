@@ -64,17 +64,19 @@ extern "C" {
  * tk_expert_gemm: out[r] = W[e] x[i] for every row r of every expert e, i its
  * index (or r).
  *
- * bf16 x bf16: products exact, sums in fp32.  FP8 x FP8 and FP8 x FP4 on the
- * matrix instruction for them, 128 columns at a time: sums in fp32, but of each
- * 128 products what lies some 2^-14 below the largest is dropped, which a bf16
+ * bf16 x bf16: products exact, sums in fp32, one running sum over the whole
+ * depth (fp32 results of normal numbers are off by some 6e-9 sqrt(depth) of
+ * their norm; so are both gradients').  FP8 x FP8 and FP8 x FP4 on the matrix
+ * instruction for them, 128 columns at a time: sums in fp32, but of each 128
+ * products what lies some 2^-14 below the largest is dropped, which a bf16
  * result does not show as long as the sum is not much smaller than its largest
  * term; so they have no fp32 results, and a sum that nearly cancels differs from
- * that of tk_expert_gemv_fp4, whose products are exact.  UE8M0 scales of groups of columns enter
- * the instruction, one scale a row is applied to the finished sum, and fp32
- * scales of groups to each 128 columns' sum, all in fp32: a sum with its groups'
- * scales, and the product of two fp32 scales of groups, have to lie in its range;
- * of two scales a row only their product and the result have to.  A scale that is a
- * NaN (UE8M0 byte 255) makes one of what it scales.
+ * that of tk_expert_gemv_fp4, whose products are exact.  UE8M0 scales of groups
+ * of columns enter the instruction, one scale a row is applied to the finished
+ * sum, and fp32 scales of groups to each 128 columns' sum, all in fp32: a sum
+ * with its groups' scales, and the product of two fp32 scales of groups, have to
+ * lie in its range; of two scales a row only their product and the result have
+ * to.  A scale that is a NaN (UE8M0 byte 255) makes one of what it scales.
  *
  *  x            [x_rows, in_features]: TK_DTYPE_BF16 elements, or TK_DTYPE_FP8
  *               codes with x_scales.  16-byte aligned.
